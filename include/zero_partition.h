@@ -25,8 +25,9 @@
  *   - "device" pointers point into GPU memory of the current HIP device;
  *     "host" pointers into ordinary host memory.  The caller owns every
  *     buffer it passes; the library keeps no pointer beyond the call except
- *     the tensor tables given to zero_layout_bind_tensors and
- *     zero_layout_bind_contributions.
+ *     the tensor tables given to zero_layout_bind_tensors,
+ *     zero_layout_bind_contributions, zero_tensor_set_create and
+ *     zero_tensor_set_bind_grads.
  *   - `stream` is a hipStream_t passed as void* (NULL = the null stream).
  *     Device work is ordered on that stream, which must belong to the
  *     current device (a stream of another device is a STATE error).
@@ -393,15 +394,193 @@ int zero_owner_step(const zero_layout* layout, int32_t rank, zero_shard_state* s
                     uint16_t* out_slot, void* stream, int32_t* overflow);
 
 /* ------------------------------------------------------------------------ */
+/* Tensor sets: AdamW over many tensors at once                              */
+/* ------------------------------------------------------------------------ */
+
+/* The update of a list of tensors of any sizes (the parameters of a model, or
+ * the pieces of them that a rank's shard holds, zero_layout_rank_segments) in
+ * one launch, with decoupled weight decay, parameter groups, clipping by the
+ * global gradient norm and dynamic loss scaling.  A step is three calls, none
+ * of which waits for the device:
+ *
+ *   zero_grad_sumsq   sum of squares of every gradient value, into device memory
+ *                     (several sets and ranks add theirs up: pass accumulate = 1
+ *                     for further sets, all-reduce the one double over ranks)
+ *   zero_step_begin   decides from it, on the device, whether the step is taken
+ *                     and what gradients are multiplied by; counts the step
+ *   zero_adamw_step   the update of one set, in place
+ *
+ * Step count, loss scale and decision live in a zero_step_control in device
+ * memory, so the three calls can be captured into a graph and replayed. */
+
+/* Opaque handle, created by zero_tensor_set_create and freed by
+ * zero_tensor_set_destroy. */
+typedef struct zero_tensor_set zero_tensor_set;
+
+/* Element types of a set's arrays. */
+enum {
+    ZERO_DTYPE_NONE = 0,
+    ZERO_DTYPE_FP16 = 1,
+    ZERO_DTYPE_BF16 = 2,
+    ZERO_DTYPE_FP32 = 3,
+    ZERO_DTYPE_MXFP8 = 4  /* states only, below */
+};
+
+#define ZERO_MAX_GROUPS 16
+#define ZERO_STATE_BLOCK 32
+
+/* One tensor.  Device pointers; only element alignment is required (4 bytes
+ * for p and fp32 states and gradients, 2 for 16-bit ones, 1 for codes and
+ * scales).  Pointers of an empty tensor are ignored. */
+typedef struct zero_tensor {
+    int64_t numel;       /* >= 0 */
+    float* p;            /* fp32 master values */
+    const void* grad;    /* gradient, grad_type */
+    void* m;             /* momentum, state_type */
+    void* v;             /* variance, state_type */
+    uint8_t* m_scale;    /* MXFP8 only: ceil(numel / 32) scale bytes */
+    uint8_t* v_scale;
+    void* out;           /* 16-bit copy of p that a step writes, out_type */
+    int32_t group;       /* index of the tensor's hyper-parameters, 0..15 */
+    int32_t reserved;
+} zero_tensor;
+
+/* States in 8 bits (ZERO_DTYPE_MXFP8, the microscaling format MXFP8 E4M3): a
+ * block is 32 consecutive elements of a tensor, from its first element on (the
+ * last block may be shorter).  Element i of a block with scale byte s stands
+ * for e4m3(code[i]) * 2^(s - 127).  An encoder takes the least scale that
+ * brings the block's largest magnitude to 448 or below, and at least s = 1
+ * (2^-126), so nothing saturates and a block that is decoded and encoded again
+ * keeps its values.  All codes zero is the zero state whatever the scales; s = 255
+ * is not a scale.
+ *
+ * m is rounded to nearest, ties to even.  The variance is a slow average:
+ * rounding it to nearest would freeze it, since a step moves it by less than
+ * half a unit.  So a step rounds v to one of its two neighbours at random, up
+ * with the probability (to 2^-16) that keeps the mean, and only ever to zero
+ * when it is zero (a lost v would divide a surviving m by eps).  The random
+ * bits are a function of the set's seed, the tensor's index, the step count
+ * and the element, so a run can be repeated bit for bit.  The update of p uses
+ * the new m and v before they are rounded. */
+
+/* Build a set of n tensors.
+ *   grad_type   FP16, BF16 or FP32; NONE for a set that only converts states
+ *   state_type  FP32 or MXFP8; NONE for a set that only sums squares
+ *   out_type    FP16, BF16, or NONE (no 16-bit copies)
+ *   seed        of the random rounding of MXFP8 variances
+ * Of the non-empty tensors, all or none have p, and all or none have grad (none:
+ * zero_tensor_set_bind_grads comes first); m and v are set when state_type is
+ * not NONE, the scales when it is MXFP8, out when out_type is not NONE, and are
+ * NULL otherwise.  No two arrays that a step writes may overlap, nor a gradient
+ * one of them.  Tables are uploaded on the current device, ordered on `stream`,
+ * and the call waits for that.  The tensors must stay allocated while the set
+ * is used, and the set must be kept until the work that uses it has finished
+ * (graphs that captured it among it).
+ * Errors: INVALID_ARG, ALIGNMENT, INDEX_OVERFLOW, OUT_OF_MEMORY (more than 2^25
+ * tiles of 1024 elements, each tensor's last one counting as whole), STATE,
+ * HIP. */
+int zero_tensor_set_create(const zero_tensor* tensors, int64_t n, int32_t grad_type,
+                           int32_t state_type, int32_t out_type, uint32_t seed, void* stream,
+                           zero_tensor_set** out);
+
+int zero_tensor_set_destroy(zero_tensor_set* set); /* NULL is accepted */
+
+/* Replace every gradient address (host array of n pointers, as in
+ * zero_tensor_set_create).  Ordered on `stream`: calls on it that were enqueued
+ * before use the old addresses, later ones (replayed graphs too) the new.
+ * Waits for the upload; on an error the old addresses stay.
+ * Errors: INVALID_ARG, ALIGNMENT, STATE (grad_type is NONE, or another device),
+ * OUT_OF_MEMORY, HIP. */
+int zero_tensor_set_bind_grads(zero_tensor_set* set, const void* const* grads, void* stream);
+
+/* Sum of squares of every gradient value of the set, in fp64, into the device
+ * double *sumsq (accumulate = 1: added to it).  The values are summed as they
+ * are, with their loss scale.  The order of the sum is fixed by the tensors'
+ * sizes: equal inputs give equal bits.  inf and NaN values give an inf or NaN.
+ *   sumsq   device, 8-byte aligned
+ *   work    device, zero_grad_sumsq_work_bytes(set) bytes, 8-byte aligned, that
+ *           nothing else uses until the call's work is done; may be NULL when
+ *           that is 0
+ * Asynchronous on `stream`.  Errors: INVALID_ARG, ALIGNMENT, STATE (no
+ * gradients, another device), HIP. */
+int64_t zero_grad_sumsq_work_bytes(const zero_tensor_set* set);
+int zero_grad_sumsq(const zero_tensor_set* set, double* sumsq, int32_t accumulate, void* work,
+                    void* stream);
+
+/* State of an optimizer's steps, in device memory (8-byte aligned).  The caller
+ * writes t, skipped, scale, lr_mult and good_steps once at the start, and may
+ * change lr_mult, scale and t between steps, ordered on the stream; sumsq
+ * holds the sum of squares when zero_step_begin runs.  The rest is written by
+ * zero_step_begin. */
+typedef struct zero_step_control {
+    int64_t t;             /* steps taken so far (skipped steps excluded) */
+    int64_t skipped;       /* steps skipped so far */
+    double sumsq;          /* in: sum of squares of all gradients, with their scale */
+    float scale;           /* loss scale that the next gradients carry, >= 2^-24 */
+    float lr_mult;         /* every group's lr is multiplied by it (a schedule) */
+    int32_t good_steps;    /* taken steps since the scale last changed */
+    int32_t skip;          /* out: 1 when the step is skipped, else 0 */
+    float norm;            /* out: global norm of the unscaled gradients, 0 unchecked */
+    float grad_mult;       /* out: what gradients are multiplied by: clip / scale */
+    float group[ZERO_MAX_GROUPS][8];  /* out: the groups' constants for this step */
+} zero_step_control;
+
+/* Begin a step.  With S = ctl->scale, and check = 1:
+ *   norm = sqrt(ctl->sumsq) / S;  c = max_norm / norm when max_norm > 0 and
+ *   norm > max_norm, else 1.  The step is skipped unless norm * c < 2^62 (inf
+ *   and NaN skip), S is at least 2^-24 and finite, and lr_mult is finite.
+ *   A skipped step leaves t and every tensor as they are.
+ * With check = 0 sumsq is not read, norm is 0 and c is 1; max_norm must be 0.
+ * A taken step counts t up and sets the constants of zero_adamw_step.
+ *   groups    host, n_groups hyper-parameters (1..16), read during the call
+ *   scaler    host, or NULL for a constant scale: a taken step counts
+ *             good_steps, and at growth_interval (> 0) scale is multiplied by
+ *             growth (kept when not finite) and good_steps reset; a skipped one
+ *             sets scale = max(scale * backoff, min_scale), good_steps = 0.  Its
+ *             own scale and good_steps are ignored.
+ * Asynchronous on `stream`.  Errors: INVALID_ARG (as for zero_shard_step),
+ * ALIGNMENT, STATE, HIP. */
+int zero_step_begin(zero_step_control* ctl, const zero_adam_hparams* groups, int32_t n_groups,
+                    float max_norm, int32_t check, const zero_loss_scaler* scaler, void* stream);
+
+/* AdamW over the set's tensors, unless the begun step is skipped:
+ *   g = grad_mult * grad
+ *   m = beta1 * m + (1 - beta1) * g
+ *   v = beta2 * v + (1 - beta2) * g * g
+ *   p = p - (lr * weight_decay * p + lr / (1 - beta1^t) * (m / (sqrt(v) / sqrt(1 - beta2^t) + eps)))
+ *   out = p rounded to nearest even
+ * with the hyper-parameters of the tensor's group and lr * lr_mult for lr, in
+ * fp32.  Several sets can follow one zero_step_begin.
+ *   ctl       device, as zero_step_begin left it on this stream
+ *   n_groups  as given to zero_step_begin; every tensor's group is below it
+ * The set's gradients must be finite unless the step was begun with check = 1
+ * and a sum over all of them.  Asynchronous on `stream`.
+ * Errors: INVALID_ARG, ALIGNMENT, STATE (no p, gradients or states, another
+ * device), HIP. */
+int zero_adamw_step(const zero_tensor_set* set, const zero_step_control* ctl, int32_t n_groups,
+                    void* stream);
+
+/* Write src's states to dst, in dst's type: FP32 to MXFP8 (both rounded to
+ * nearest, a v above zero not to zero; values must be finite, v not negative)
+ * or MXFP8 to FP32 (exact, save where the product leaves fp32's normal range).
+ * The sets have the same number of tensors of the same sizes, different state
+ * types, and the states do not overlap.  Asynchronous on `stream`.
+ * Errors: INVALID_ARG, STATE (no states, another device), HIP. */
+int zero_states_convert(const zero_tensor_set* dst, const zero_tensor_set* src, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Kernel timing (profiling aid)                                            */
 /* ------------------------------------------------------------------------ */
 
 /* Per calling thread.  While enabled (enable != 0), zero_shard_step,
- * zero_owner_step, zero_pack_bucket and zero_reduce_to_owner time their
- * kernels with a pair of HIP events that the launch itself records at the
+ * zero_owner_step, zero_pack_bucket, zero_reduce_to_owner, zero_grad_sumsq,
+ * zero_adamw_step and zero_states_convert time their kernels with a pair of
+ * HIP events that the launch itself records at the
  * start of their first kernel and at the end of their last (for
  * zero_shard_step: the fused pass, or the check and update passes in place;
  * for zero_owner_step: the pass, without the one-thread flag hand-over).
+ * zero_grad_sumsq, zero_adamw_step and zero_states_convert are not timed on a
+ * stream that is being captured.
  * The pairs go into a ring of 4096 per thread, so calls can be timed back to
  * back without waiting on the events; enabling or disabling clears it.
  * zero_last_kernel_ms waits for the most recent pair's end event and returns
@@ -425,7 +604,8 @@ const char* zero_last_error(void);     /* thread-local, never NULL */
 int zero_last_hip_error(void);         /* hipError_t of the last ZERO_ERR_HIP */
 
 /* sizeof of the ABI structs, for binding checks: 0 layout_info, 1 segment,
- * 2 shard_state, 3 adam_hparams, 4 loss_scaler, 5 arena_plan; -1 otherwise. */
+ * 2 shard_state, 3 adam_hparams, 4 loss_scaler, 5 arena_plan, 6 tensor,
+ * 7 step_control; -1 otherwise. */
 int64_t zero_abi_struct_size(int32_t which);
 
 /* Architecture of the current device as a number (gfx950 -> 950) and its

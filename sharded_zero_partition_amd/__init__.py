@@ -11,7 +11,7 @@ generators; `build` compiles the library.
 
 __all__ = ["partition_layout", "Layout", "ShardState", "shard_step", "PreparedStep", "AdamHParams",
            "LossScaler", "ZeroError", "version", "device_info", "set_kernel_timing",
-           "last_kernel_ms", "kernel_times", "carve_arena", "ArenaPlan"]
+           "last_kernel_ms", "kernel_times", "carve_arena", "ArenaPlan", "TensorSet", "StepControl"]
 
 
 def __getattr__(name):

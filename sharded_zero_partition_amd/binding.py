@@ -15,6 +15,12 @@ Names follow the C ABI in include/zero_partition.h:
   Layout.reduce_to_owner(...)          (zero_reduce_to_owner)
   shard_step(...), PreparedStep(...)   (zero_shard_step; zero_shard_step_noalloc with noalloc=True)
   Layout.owner_step(...)               (zero_owner_step)
+  TensorSet(...)                       (zero_tensor_set_create)
+  TensorSet.bind_grads(...)            (zero_tensor_set_bind_grads)
+  TensorSet.grad_sumsq(...)            (zero_grad_sumsq)
+  StepControl(...), StepControl.begin(...)   (zero_step_control, zero_step_begin)
+  TensorSet.adamw_step(...)            (zero_adamw_step)
+  TensorSet.states_from(...)           (zero_states_convert)
   set_kernel_timing, last_kernel_ms, kernel_times   (kernel timing)
 """
 
@@ -101,7 +107,28 @@ class ArenaPlan(ctypes.Structure):
                 if self.offset[i] >= 0}
 
 
-ABI_STRUCTS = [LayoutInfo, Segment, ShardStateC, AdamHParams, LossScaler, ArenaPlan]
+MAX_GROUPS = 16
+STATE_BLOCK = 32
+DTYPE_NONE, DTYPE_FP16, DTYPE_BF16, DTYPE_FP32, DTYPE_MXFP8 = range(5)
+
+
+class TensorC(ctypes.Structure):
+    _fields_ = [("numel", ctypes.c_int64), ("p", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("group", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class StepControlC(ctypes.Structure):
+    _fields_ = [("t", ctypes.c_int64), ("skipped", ctypes.c_int64), ("sumsq", ctypes.c_double),
+                ("scale", ctypes.c_float), ("lr_mult", ctypes.c_float),
+                ("good_steps", ctypes.c_int32), ("skip", ctypes.c_int32),
+                ("norm", ctypes.c_float), ("grad_mult", ctypes.c_float),
+                ("group", (ctypes.c_float * 8) * MAX_GROUPS)]
+
+
+ABI_STRUCTS = [LayoutInfo, Segment, ShardStateC, AdamHParams, LossScaler, ArenaPlan, TensorC,
+               StepControlC]
 
 # exported symbol -> (restype, argtypes)
 _P = ctypes.c_void_p
@@ -123,6 +150,14 @@ SIGNATURES = {
     "zero_shard_step": (ctypes.c_int, [_P, _P, _I32, _P, _P, _P, _P, _P]),
     "zero_shard_step_noalloc": (ctypes.c_int, [_P, _P, _I32, _P, _P, _P, _P, _P]),
     "zero_owner_step": (ctypes.c_int, [_P, _I32, _P, _P, _P, _P, _P, _P]),
+    "zero_tensor_set_create": (ctypes.c_int, [_P, _I64, _I32, _I32, _I32, ctypes.c_uint32, _P, _P]),
+    "zero_tensor_set_destroy": (ctypes.c_int, [_P]),
+    "zero_tensor_set_bind_grads": (ctypes.c_int, [_P, _P, _P]),
+    "zero_grad_sumsq_work_bytes": (ctypes.c_int64, [_P]),
+    "zero_grad_sumsq": (ctypes.c_int, [_P, _P, _I32, _P, _P]),
+    "zero_step_begin": (ctypes.c_int, [_P, _P, _I32, ctypes.c_float, _I32, _P, _P]),
+    "zero_adamw_step": (ctypes.c_int, [_P, _P, _I32, _P]),
+    "zero_states_convert": (ctypes.c_int, [_P, _P, _P]),
     "zero_set_kernel_timing": (ctypes.c_int, [_I32]),
     "zero_last_kernel_ms": (ctypes.c_int, [_P]),
     "zero_kernel_times": (ctypes.c_int, [_P, _I64, _P]),
@@ -463,6 +498,207 @@ class PreparedStep:
         st.t = c.t
         st.cur = c.cur
         return self._flag.value
+
+
+# ---------------------------------------------------------------------------
+# tensor sets: AdamW over many tensors at once
+# ---------------------------------------------------------------------------
+
+class StepControl:
+    """An optimizer's step state on the device (a zero_step_control): step
+    count, loss scale and the decision of the step at hand.  The attributes are
+    0-dim tensors on its memory: reading one on the host waits for the device;
+    writing (`control.lr_mult.fill_(0.5)`) is ordered like any other work.
+
+      t, skipped      steps taken and skipped (int64)
+      sumsq           sum of squares of the gradients (float64): where
+                      TensorSet.grad_sumsq puts it, and what ranks all-reduce
+      scale, lr_mult  loss scale of the next gradients, factor on every lr
+      good_steps      taken steps since the scale last changed (int32)
+      skip, norm, grad_mult   of the begun step: 1 when it is skipped, the
+                      global norm, what gradients are multiplied by
+    """
+
+    def __init__(self, scale: float = 1.0, t: int = 0, lr_mult: float = 1.0, device=None):
+        c = StepControlC()
+        c.t, c.scale, c.lr_mult = int(t), float(scale), float(lr_mult)
+        if c.t < 0:
+            raise ValueError("t must not be negative")
+        if not (c.scale >= 2.0 ** -24 and c.scale < float("inf")):
+            raise ValueError("scale must be finite and at least 2^-24")
+        dev = torch.device("cuda", _current_device()) if device is None else torch.device(device)
+        if dev.type != "cuda":
+            raise ValueError("the control block lives on a device")
+        self.buffer = torch.frombuffer(bytearray(c), dtype=torch.uint8).to(dev)
+        self.device_index = self.buffer.device.index
+        self._ptr = self.buffer.data_ptr()
+        for name, dtype in (("t", torch.int64), ("skipped", torch.int64), ("sumsq", torch.float64),
+                            ("scale", torch.float32), ("lr_mult", torch.float32),
+                            ("good_steps", torch.int32), ("skip", torch.int32),
+                            ("norm", torch.float32), ("grad_mult", torch.float32)):
+            f = getattr(StepControlC, name)
+            setattr(self, name, self.buffer[f.offset:f.offset + f.size].view(dtype)[0])
+        self._groups = None
+        self._n_groups = 0
+
+    def begin(self, groups, max_norm: float = 0.0, check: bool = True, scaler: "LossScaler" = None,
+              stream=None):
+        """zero_step_begin: decide the step from `sumsq` (check=False: take it
+        unseen) with clipping to `max_norm` (0: none), and set the constants of
+        `groups` (AdamHParams, one for each parameter group).  `scaler` gives
+        the rule of a dynamic loss scale; its own scale is not used."""
+        _on_current_device(self.device_index, "the control block")
+        n = len(groups)
+        arr = (AdamHParams * max(1, n))(*groups)
+        _check(lib.zero_step_begin(self._ptr, arr, n, max_norm, int(bool(check)),
+                                   None if scaler is None else _ref(scaler), _stream_ptr(stream)))
+        self._n_groups = n
+
+
+def _on_current_device(index: int, what: str):
+    if index != _current_device():
+        raise ValueError(f"{what} is on cuda:{index}, the current device is another")
+
+
+def _dtype_of(tensors, what: str, kinds) -> int:
+    """The one dtype of a list's non-empty tensors, as a ZERO_DTYPE number."""
+    seen = {t.dtype for t in tensors if t.numel() > 0} or {t.dtype for t in tensors}
+    if len(seen) > 1:
+        raise ValueError(f"{what}: the tensors have different dtypes")
+    for d in seen:
+        if d not in kinds:
+            raise ValueError(f"{what}: dtype {d} is not supported")
+        return kinds[d]
+    return DTYPE_NONE
+
+
+_BITS16 = {torch.float16: DTYPE_FP16, torch.int16: DTYPE_FP16, torch.bfloat16: DTYPE_BF16}
+_GRAD_DTYPES = {**_BITS16, torch.float32: DTYPE_FP32}
+_STATE_DTYPES = {torch.float32: DTYPE_FP32, torch.uint8: DTYPE_MXFP8, torch.float8_e4m3fn: DTYPE_MXFP8}
+
+
+class TensorSet:
+    """Owner of a zero_tensor_set: lists of device tensors, contiguous and of
+    any size, one entry for each parameter (or each piece of one that a rank's
+    shard holds, Layout.rank_segments).
+
+      p        fp32 master values
+      grads    fp16 (or int16 bit patterns), bf16 or fp32
+      m, v     fp32 states, or e4m3 codes (float8_e4m3fn or uint8) with
+               m_scale, v_scale: a scale byte for each 32 elements (uint8 or
+               float8_e8m0fnu).  All zeros is the state to start from.
+      out      fp16 (or int16) or bf16 copies that a step writes
+      groups   each tensor's parameter group (default 0)
+      seed     of the random rounding of 8-bit variances
+
+    Lists that an operator does not need may be left out: grad_sumsq needs
+    grads, adamw_step p, grads, m and v, states_from m and v.  The tensors'
+    storage must not be moved or resized while the set is in use."""
+
+    def __init__(self, p=None, grads=None, m=None, v=None, m_scale=None, v_scale=None, out=None,
+                 groups=None, seed: int = 0, stream=None):
+        self._h = None
+        lists = dict(p=p, grad=grads, m=m, v=v, m_scale=m_scale, v_scale=v_scale, out=out)
+        lists = {k: list(x) for k, x in lists.items() if x is not None}
+        if not lists:
+            raise ValueError("a tensor set needs tensors")
+        if ("m" in lists) != ("v" in lists):
+            raise ValueError("m and v come together")
+        self._numels = [t.numel() for t in lists.get("m", next(iter(lists.values())))]
+        n = len(self._numels)
+        self._dev = _current_device()
+        self._grad_type = _dtype_of(lists.get("grad", []), "grads", _GRAD_DTYPES)
+        state_type = _dtype_of(lists.get("m", []), "m", _STATE_DTYPES)
+        if state_type != _dtype_of(lists.get("v", []), "v", _STATE_DTYPES):
+            raise ValueError("m and v have different dtypes")
+        out_type = _dtype_of(lists.get("out", []), "out", _BITS16)
+        _dtype_of(lists.get("p", []), "p", {torch.float32: DTYPE_FP32})
+        mx = state_type == DTYPE_MXFP8
+        if ("m_scale" in lists, "v_scale" in lists) != (mx, mx):
+            raise ValueError("m_scale and v_scale come with states in 8 bits, and only with them")
+        width = dict(p=4, grad=4 if self._grad_type == DTYPE_FP32 else 2, m=1 if mx else 4,
+                     v=1 if mx else 4, m_scale=1, v_scale=1, out=2)
+        if groups is not None and len(groups) != n:
+            raise ValueError(f"groups has {len(groups)} entries, the set {n} tensors")
+        recs = (TensorC * max(1, n))()
+        blocks = [-(-k // STATE_BLOCK) for k in self._numels]
+        for name, lst in lists.items():
+            sizes = blocks if name in ("m_scale", "v_scale") else self._numels
+            if len(lst) != n:
+                raise ValueError(f"{name} has {len(lst)} tensors, the set {n}")
+            for i, (t, k) in enumerate(zip(lst, sizes)):
+                if t.numel() != k:
+                    raise ValueError(f"{name}[{i}] has {t.numel()} elements, expected {k}")
+                if k:
+                    setattr(recs[i], name, _dev_ptr(t, f"{name}[{i}]", width[name], self._dev))
+        for i, k in enumerate(self._numels):
+            recs[i].numel = k
+            recs[i].group = 0 if groups is None else int(groups[i])
+        h = ctypes.c_void_p()
+        _check(lib.zero_tensor_set_create(recs, n, self._grad_type, state_type, out_type,
+                                          int(seed) & 0xFFFFFFFF, _stream_ptr(stream), _ref(h)))
+        self._h = h
+        self._keep = lists
+        self._work_elems = lib.zero_grad_sumsq_work_bytes(h) // 8
+
+    def close(self):
+        """Free the set's tables.  Work that uses them must have finished."""
+        if self._h:
+            lib.zero_tensor_set_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def bind_grads(self, grads, stream=None):
+        """Replace the gradient tensors (same sizes and dtype)."""
+        grads = list(grads)
+        if len(grads) != len(self._numels):
+            raise ValueError(f"grads has {len(grads)} tensors, the set {len(self._numels)}")
+        kind = _dtype_of(grads, "grads", _GRAD_DTYPES)
+        if any(self._numels) and kind != self._grad_type:
+            raise ValueError("the set's gradients have another dtype")
+        w = 4 if kind == DTYPE_FP32 else 2
+        ptrs = (ctypes.c_void_p * max(1, len(grads)))()
+        for i, (t, k) in enumerate(zip(grads, self._numels)):
+            if t.numel() != k:
+                raise ValueError(f"grads[{i}] has {t.numel()} elements, expected {k}")
+            ptrs[i] = _dev_ptr(t, f"grads[{i}]", w, self._dev) if k else None
+        _check(lib.zero_tensor_set_bind_grads(self._h, ptrs, _stream_ptr(stream)))
+        self._keep["grad"] = grads
+
+    def grad_sumsq(self, out, accumulate: bool = False, stream=None):
+        """zero_grad_sumsq: the sum of squares of every gradient value into
+        `out` (one float64 on the device, StepControl.sumsq); accumulate=True
+        adds it to what is there."""
+        if out.dtype != torch.float64 or out.numel() != 1:
+            raise ValueError("out must be one float64")
+        work = None
+        if self._work_elems:
+            # workspace of this call alone, from the pool of its stream: calls
+            # on other streams and captured graphs get their own
+            if stream is None:
+                work = torch.empty(self._work_elems, dtype=torch.float64, device=out.device)
+            else:
+                with torch.cuda.stream(stream):
+                    work = torch.empty(self._work_elems, dtype=torch.float64, device=out.device)
+        _check(lib.zero_grad_sumsq(self._h, _dev_ptr(out, "out", 8), int(bool(accumulate)),
+                                   None if work is None else work.data_ptr(), _stream_ptr(stream)))
+
+    def adamw_step(self, control: "StepControl", stream=None):
+        """zero_adamw_step: the step that `control` began, on every tensor."""
+        if control._n_groups == 0:
+            raise ValueError("the step has not begun (StepControl.begin)")
+        _on_current_device(control.device_index, "the control block")
+        _check(lib.zero_adamw_step(self._h, control._ptr, control._n_groups, _stream_ptr(stream)))
+
+    def states_from(self, source: "TensorSet", stream=None):
+        """zero_states_convert: write `source`'s states into this set's, fp32
+        to 8 bits or back."""
+        _check(lib.zero_states_convert(self._h, source._h, _stream_ptr(stream)))
 
 
 def version() -> int:

@@ -21,7 +21,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libzero_partition.so")
 PROBE_LIB = os.path.join(PKG, "libzero_probe.so")
 
-SOURCES = ["layout.cpp", "capi.cpp", "pack.hip", "shard_step.hip", "reduce_owner.hip", "noalloc.hip"]
+SOURCES = ["layout.cpp", "capi.cpp", "pack.hip", "shard_step.hip", "reduce_owner.hip", "noalloc.hip",
+           "tensor_set.cpp", "tensor_step.hip", "grad_norm.hip"]
 PROBE_SOURCES = ["stream_probe.hip"]
 
 ARCH = "gfx950"

@@ -641,6 +641,8 @@ extern "C" int64_t zero_abi_struct_size(int32_t which) {
         case 3: return int64_t(sizeof(zero_adam_hparams));
         case 4: return int64_t(sizeof(zero_loss_scaler));
         case 5: return int64_t(sizeof(zero_arena_plan));
+        case 6: return int64_t(sizeof(zero_tensor));
+        case 7: return int64_t(sizeof(zero_step_control));
         default: return -1;
     }
 }

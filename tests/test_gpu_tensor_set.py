@@ -1,0 +1,520 @@
+"""The tensor sets on the GPU against the numpy oracle: bit for bit against its fp32 form, within derived bounds against
+its 64-bit form."""
+
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+import sharded_zero_partition_amd as zp
+from oracle import tensor_set as T
+from set_harness import GRAD, SIZES, Twin, bits, read, same_control
+
+pytestmark = pytest.mark.gpu
+
+HP = [T.HParams(1e-3, 0.9, 0.999, 1e-8, 0.1), T.HParams(2e-3, 0.8, 0.95, 1e-6, 0.0)]
+
+
+def hparams(hs):
+    return [zp.AdamHParams(h.lr, h.beta1, h.beta2, h.eps, h.weight_decay) for h in hs]
+
+
+def follow(c, d):
+    """The oracle's control takes the device's factor and constants (their last bits come from a pow and a sum)."""
+    c.grad_mult = d.grad_mult
+    if not c.skip:
+        names = ("beta1", "omb1", "beta2", "omb2", "decay", "step", "rbc2", "eps")
+        for k, want in enumerate(c.consts):
+            got = dict(zip(names, d.group[k]))
+            for n in names:
+                assert abs(got[n] - want[n]) <= 2.0 ** -23 * abs(want[n]), n
+            c.consts[k] = got
+
+
+def take_step(twins, control, c, groups=HP, max_norm=0.0, check=True, scaler=None, what=""):
+    if check:
+        for k, t in enumerate(twins):
+            t.set.grad_sumsq(control.sumsq, accumulate=k > 0)
+        c.sumsq = sum(t.sumsq() for t in twins)
+    control.begin(hparams(groups), max_norm=max_norm, check=check, scaler=scaler)
+    c.begin(groups, max_norm, check, scaler)
+    for t in twins:
+        t.set.adamw_step(control)
+    torch.cuda.synchronize()
+    follow(c, same_control(control, c, rel=2.0 ** -23))
+    for t in twins:
+        t.expect(c)
+        t.compare(what)
+
+
+@pytest.mark.parametrize("grad", ["fp16", "bf16", "fp32"])
+def test_sumsq_against_64_bits(grad):
+    for sizes in ([1], [0], [], [1024], [3, 0, 1025], SIZES, [40000] * 30 + [5]):
+        t = Twin(sizes or [0], grad=grad, out="none", seed=len(sizes))
+        out = torch.full((), -1.0, dtype=torch.float64, device="cuda")
+        t.set.grad_sumsq(out)
+        first = out.item()
+        n = sum(sizes)
+        # n exact squares (fp32's are rounded once), summed in some order: n 2^-53 relative at most
+        assert abs(first - t.sumsq()) <= (n + 1) * 2.0 ** -53 * t.sumsq(), (grad, sizes)
+        t.set.grad_sumsq(out)
+        assert out.item() == first
+        t.set.grad_sumsq(out, accumulate=True)
+        assert out.item() == 2 * first
+
+
+@pytest.mark.parametrize("value,want", [(np.inf, np.inf), (-np.inf, np.inf), (np.nan, np.nan), (65504.0, 65504.0 ** 2)])
+@pytest.mark.parametrize("where", [0, 1000, 1500, 5999])
+def test_sumsq_of_special_values(value, want, where):
+    g = torch.zeros(6000, dtype=torch.float16, device="cuda")
+    g[where] = value
+    out = torch.zeros(1, dtype=torch.float64, device="cuda")
+    zp.TensorSet(grads=[g]).grad_sumsq(out)
+    assert out.item() == want or (np.isnan(want) and np.isnan(out.item()))
+
+
+@pytest.mark.parametrize("state", ["fp32", "mx"])
+@pytest.mark.parametrize("out", ["fp16", "bf16", "none"])
+@pytest.mark.parametrize("grad", ["fp16", "bf16", "fp32"])
+def test_steps_match_the_oracle(grad, out, state):
+    print(f"[adamw] {grad} {out} {state}", flush=True)
+    t = Twin(SIZES, grad, out, state, seed=11)
+    control, c = zp.StepControl(scale=1024.0, t=3), T.Control(t=3, scale=1024.0)
+    for step in range(4):
+        t.new_grads()
+        take_step([t], control, c, max_norm=0.05 if step % 2 else 0.0, check=step != 2, what=f"step {step}")
+
+
+@pytest.mark.parametrize("state", ["fp32", "mx"])
+def test_a_step_against_64_bits(state):
+    """From values that the states hold exactly, p (and fp32 states) within the bound that the roundings add up to."""
+    t = Twin([50001, 257, 33], "fp32", "none", state, seed=5)
+    control = zp.StepControl(scale=256.0, t=41)
+    before = [{k: a[i].copy() for k, a in t.host.items()} for i in range(3)]
+    t.set.grad_sumsq(control.sumsq)
+    control.begin(hparams(HP), max_norm=0.05)
+    t.set.adamw_step(control)
+    norm = np.sqrt(t.sumsq()) / 256.0
+    assert norm > 0.05
+    for i, b in enumerate(before):
+        m = T.decode(b["m"], b["ms"]) if state == "mx" else b["m"]
+        v = T.decode(b["v"], b["vs"]) if state == "mx" else b["v"]
+        want, off = T.adamw_wide(HP[i % 2], 1.0, 42, b["g"], 0.05 / norm / 256.0, b["p"], m, v)
+        names = "p" if state == "mx" else "pmv"
+        for k, w, o in zip(names, want, off):
+            d = np.abs(t.view[k][i].cpu().numpy().astype(np.float64) - w)
+            assert (d <= o).all(), (k, float((d / o).max()))
+        if state == "mx":
+            for k, w, s, half in (("m", want[1], "ms", 2.0 ** -4), ("v", want[2], "vs", 2.0 ** -3)):
+                got = T.decode(t.view[k][i].cpu().numpy(), t.view[s][i].cpu().numpy()).astype(np.float64)
+                power = np.repeat(2.0 ** (t.view[s][i].cpu().numpy().astype(np.float64) - 127), 32)[:got.size]
+                # m: half a step, v: one; steps are 2^-3 of the power of two below, at least 2^-9 of the scale
+                # (v above zero is at least one); 2^-20 covers the fp32 roundings before
+                lim = np.maximum(np.abs(w) * half, power * 2.0 ** -9 * (0.5 if k == "m" else 1)) * (1 + 2.0 ** -20)
+                assert (np.abs(got - w) <= lim).all(), k
+
+
+@pytest.mark.parametrize("state", ["fp32", "mx"])
+@pytest.mark.parametrize("bad", [np.inf, np.nan])
+def test_a_skipped_step_changes_nothing(state, bad):
+    t = Twin(SIZES, "fp16", "bf16", state, seed=2)
+    control, c = zp.StepControl(scale=1024.0), T.Control(scale=1024.0)
+    rule = zp.LossScaler.make(min_scale=300.0, growth_interval=2)
+    for step in range(7):
+        t.new_grads()
+        if step in (1, 2, 5):
+            i = len(SIZES) - 1 if step == 1 else step
+            t.view["g"][i][-1] = bad
+            t.host["g"][i][-1] = bad
+        take_step([t], control, c, max_norm=1.0, scaler=rule, what=f"step {step}")
+    # 1024, two skips: 512 and the floor 300, two taken steps: 600, a skip: 300
+    assert (c.skipped, c.t, c.scale) == (3, 4, 300.0)
+
+
+def test_device_side_values_that_skip():
+    """A scale or factor on lr that the caller left unusable, and a norm whose squares would leave fp32."""
+    t = Twin([100], "fp32", "none", "fp32", seed=1)
+    for name, value, std in (("scale", 0.0, 1), ("scale", float("inf"), 1), ("scale", float("nan"), 1),
+                             ("lr_mult", float("inf"), 1), ("lr_mult", float("nan"), 1), (None, 0, 2.0 ** 63)):
+        t.new_grads([np.full(100, std, np.float32)])
+        control = zp.StepControl()
+        if name:
+            getattr(control, name).fill_(value)
+        t.set.grad_sumsq(control.sumsq)
+        control.begin(hparams(HP[:1]))
+        t.set.adamw_step(control)
+        assert (control.skip.item(), control.t.item(), control.skipped.item()) == (1, 0, 1), name
+        t.compare(str(name))
+    control = zp.StepControl()                        # clipped, the same gradients are fine
+    t.set.grad_sumsq(control.sumsq)
+    control.begin(hparams(HP[:1]), max_norm=1.0)
+    t.set.adamw_step(control)
+    assert control.skip.item() == 0 and torch.isfinite(t.view["p"][0]).all()
+
+
+def test_two_sets_under_one_norm():
+    """Large tensors in 8 bits, small ones in 32, one clip over both, and a schedule on the device."""
+    a = Twin([4099, 50001], "fp16", "fp16", "mx", seed=7)
+    b = Twin([1, 33, 700], "fp16", "fp16", "fp32", seed=8)
+    control, c = zp.StepControl(scale=1024.0), T.Control(scale=1024.0)
+    for step in range(3):
+        for t in (a, b):
+            t.new_grads()
+        control.lr_mult.fill_(0.5 ** step)
+        c.lr_mult = 0.5 ** step
+        take_step([a, b], control, c, max_norm=0.1, what=f"step {step}")
+
+
+def test_gradients_bound_later_and_replaced():
+    t = Twin(SIZES, "bf16", "none", "fp32", seed=4)
+    p = [x.clone() for x in t.view["p"]]
+    late = zp.TensorSet(p=p, grads=None, m=[x.clone() for x in t.view["m"]], v=[x.clone() for x in t.view["v"]])
+    control = zp.StepControl()
+    control.begin(hparams(HP), check=False)
+    with pytest.raises(zp.ZeroError, match="STATE"):
+        late.adamw_step(control)
+    with pytest.raises(ValueError):
+        t.set.bind_grads([x.float() for x in t.view["g"]])
+    with pytest.raises(zp.ZeroError, match="INVALID_ARG"):
+        t.set.bind_grads([v.view(torch.bfloat16)[: v.numel()] for v in t.view["p"]])   # in the master values
+    moved = [torch.cat([x.new_zeros(1), x])[1:] for x in t.view["g"]]                  # 2-byte aligned copies
+    for x in t.view["g"]:
+        x.fill_(float("nan"))                                                          # the old ones are not read again
+    t.set.bind_grads(moved)
+    del t.kinds["g"]                                                                   # the old buffer is not compared
+    c = T.Control(scale=1024.0)
+    take_step([t], zp.StepControl(scale=1024.0), c, max_norm=0.05)
+
+
+def test_bind_grads_refusal_keeps_the_old_addresses():
+    t = Twin([100, 200], "fp16", "none", "fp32", seed=6)
+    with pytest.raises(zp.ZeroError):
+        t.set.bind_grads([t.view["g"][0], t.view["m"][1].view(torch.float16)[:200]])
+    c = T.Control(scale=1024.0)
+    take_step([t], zp.StepControl(scale=1024.0), c)
+
+
+def test_refusals_on_the_device():
+    t = Twin([100, 40], "fp16", "fp16", "mx", seed=3)
+    control = zp.StepControl()
+    with pytest.raises(ValueError, match="begun"):
+        t.set.adamw_step(control)
+    with pytest.raises(zp.ZeroError, match="INVALID_ARG"):
+        control.begin([])
+    control.begin(hparams(HP[:1]), check=False)
+    with pytest.raises(zp.ZeroError, match="group"):
+        t.set.adamw_step(control)                           # tensor 1 is of group 1
+    grads_only = zp.TensorSet(grads=t.view["g"])
+    states_only = zp.TensorSet(m=t.view["m"], v=t.view["v"], m_scale=t.view["ms"], v_scale=t.view["vs"])
+    control.begin(hparams(HP), check=False)
+    for s in (grads_only, states_only):
+        with pytest.raises(zp.ZeroError, match="STATE"):
+            s.adamw_step(control)
+    with pytest.raises(zp.ZeroError, match="STATE"):
+        states_only.grad_sumsq(control.sumsq)
+    with pytest.raises(zp.ZeroError, match="STATE"):
+        states_only.states_from(grads_only)
+    with pytest.raises(zp.ZeroError, match="same type"):
+        states_only.states_from(t.set)
+    f = [torch.zeros(n, device="cuda") for n in (100, 41)]
+    with pytest.raises(zp.ZeroError, match="sizes"):
+        zp.TensorSet(m=f, v=[x.clone() for x in f]).states_from(t.set)
+    mem = torch.zeros(4096, dtype=torch.uint8, device="cuda")
+    inside = zp.TensorSet(m=[mem[:400].view(torch.float32)], v=[mem[400:800].view(torch.float32)])
+    codes = zp.TensorSet(m=[mem[700:800]], v=[mem[1000:1100]], m_scale=[mem[1200:1204]], v_scale=[mem[1204:1208]])
+    with pytest.raises(zp.ZeroError, match="overlap"):
+        inside.states_from(codes)
+    with pytest.raises(ValueError):
+        t.set.grad_sumsq(torch.zeros(1, device="cuda"))
+    with pytest.raises(ValueError, match="contiguous"):
+        zp.TensorSet(grads=[torch.zeros(8, 8, device="cuda").half()[:, ::2]])
+    t.compare()                                              # nothing was written
+
+
+@pytest.mark.parametrize("sizes", [SIZES, [0], [1], [200003]])
+def test_states_convert_both_ways(sizes):
+    t = Twin(sizes, "fp16", "none", "mx", seed=9)
+    wide = [[torch.full((n,), float("nan"), device="cuda") for n in sizes] for _ in range(2)]
+    f = zp.TensorSet(m=wide[0], v=wide[1])
+    f.states_from(t.set)
+    for i in range(len(sizes)):
+        for k, s, w in (("m", "ms", wide[0]), ("v", "vs", wide[1])):
+            assert np.array_equal(bits(w[i]), T.decode(t.host[k][i], t.host[s][i]).view(np.int32)), (i, k)
+    # fp32 states of every magnitude to 8 bits
+    rng = np.random.default_rng(1)
+    for i, n in enumerate(sizes):
+        m = (rng.standard_normal(n) * 10.0 ** rng.uniform(-44, 30, 1)).astype(np.float32)
+        v = np.square(rng.standard_normal(n) * 10.0 ** rng.uniform(-22, 15, 1)).astype(np.float32)
+        m[::7], v[::5] = 0, 0
+        wide[0][i].copy_(torch.from_numpy(m))
+        wide[1][i].copy_(torch.from_numpy(v))
+        t.host["m"][i], t.host["ms"][i] = T.encode(m, False)
+        t.host["v"][i], t.host["vs"][i] = T.encode(v, True)
+    t.set.states_from(f)
+    torch.cuda.synchronize()
+    t.compare()
+
+
+def test_scale_byte_ends():
+    """Scales 0 (2^-127) to 254 decode to their products; encoding reaches its own ends, 1 and 247."""
+    s = torch.arange(255, dtype=torch.int32).to(torch.uint8)
+    code = torch.randint(0, 0x7F, (255 * 32,), dtype=torch.uint8)
+    code |= torch.randint(0, 2, code.shape, dtype=torch.uint8) * 0x80
+    dev = [x.cuda() for x in (code, code & 0x7F, s, s.clone())]
+    wide = [torch.zeros(code.numel(), device="cuda") for _ in range(2)]
+    f, e = zp.TensorSet(m=wide[:1], v=wide[1:]), zp.TensorSet(m=dev[:1], v=dev[1:2], m_scale=dev[2:3], v_scale=dev[3:])
+    f.states_from(e)
+    with np.errstate(over="ignore"):
+        want = T.decode(code.numpy(), s.numpy())
+    got = wide[0].cpu().numpy()
+    assert np.array_equal(got, want)
+    big = torch.tensor([np.finfo(np.float32).max, 0.0, 1e-45] + [1.0] * 29, device="cuda")
+    tiny = torch.tensor([1e-45, 0.0] + [0.0] * 30, device="cuda")
+    x = torch.cat([big, tiny, torch.zeros(32, device="cuda")])
+    f, out = zp.TensorSet(m=[x], v=[x.clone()]), [torch.zeros(96, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    sc = [torch.zeros(3, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    zp.TensorSet(m=out[:1], v=out[1:], m_scale=sc[:1], v_scale=sc[1:]).states_from(f)
+    for k, positive in ((0, False), (1, True)):
+        c, b = T.encode(x.cpu().numpy(), positive)
+        assert np.array_equal(out[k].cpu().numpy(), c) and np.array_equal(sc[k].cpu().numpy(), b)
+        assert list(b) == [247, 1, 1]
+
+
+@pytest.mark.parametrize("state", ["fp32", "mx"])
+def test_captured_steps_replay_like_eager_ones(state):
+    """One captured step, replayed with new gradients, another learning rate and an overflow between eager work, against
+    the oracle; the step count advances on the device, so each replay is a new step."""
+    t = Twin(SIZES + [300000], "fp16", "fp16", state, seed=12)
+    control, c = zp.StepControl(scale=1024.0), T.Control(scale=1024.0)
+    rule = zp.LossScaler.make(growth_interval=3)
+    take_step([t], control, c, max_norm=0.05, scaler=rule, what="eager")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        t.set.grad_sumsq(control.sumsq)
+        control.begin(hparams(HP), max_norm=0.05, scaler=rule)
+        t.set.adamw_step(control)
+    torch.cuda.synchronize()
+    t.compare("capturing runs nothing")
+    for step in range(6):
+        t.new_grads()
+        if step == 2:
+            t.view["g"][6][0] = float("inf")
+            t.host["g"][6][0] = np.inf
+        control.lr_mult.fill_(1.0 / (1 + step))
+        c.lr_mult = float(np.float32(1.0 / (1 + step)))
+        torch.randn(1 << 20, device="cuda").sum()             # the program's own work between replays
+        c.sumsq = t.sumsq()
+        graph.replay()
+        torch.cuda.synchronize()
+        c.begin(HP, 0.05, True, rule)
+        follow(c, same_control(control, c, rel=2.0 ** -23))
+        t.expect(c)
+        t.compare(f"replay {step}")
+        if step == 3:                                         # an eager step in between, with memory of its own
+            take_step([t], control, c, max_norm=0.05, scaler=rule, what="eager between")
+
+
+def test_two_graphs_of_one_set_on_two_streams():
+    """Sums of one set captured twice and replayed at the same time do not share a workspace."""
+    g = torch.randn(3_000_000, device="cuda")
+    s = zp.TensorSet(grads=[g])
+    outs = [torch.zeros(1, dtype=torch.float64, device="cuda") for _ in range(2)]
+    s.grad_sumsq(outs[0])
+    want = outs[0].item()
+    graphs = []
+    for o in outs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(20):
+                s.grad_sumsq(o)
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for graph, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert [o.item() for o in outs] == [want, want]
+
+
+def test_another_stream():
+    t = Twin(SIZES, "bf16", "bf16", "mx", seed=13)
+    control, c = zp.StepControl(scale=1024.0), T.Control(scale=1024.0)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    t.set.grad_sumsq(control.sumsq, stream=st)
+    control.begin(hparams(HP), max_norm=0.05, stream=st)
+    t.set.adamw_step(control, stream=st)
+    st.synchronize()
+    c.sumsq = t.sumsq()
+    c.begin(HP, 0.05)
+    follow(c, same_control(control, c, rel=2.0 ** -23))
+    t.expect(c)
+    t.compare()
+
+
+def test_two_threads_with_their_own_sets():
+    twins = [Twin(SIZES, "fp16", "fp16", s, seed=20 + k) for k, s in enumerate(("fp32", "mx"))]
+    errors = []
+
+    def work(t):
+        try:
+            st = torch.cuda.Stream()
+            control, c = zp.StepControl(scale=1024.0), T.Control(scale=1024.0)
+            st.wait_stream(torch.cuda.default_stream())
+            with torch.cuda.stream(st):
+                for _ in range(5):
+                    t.set.grad_sumsq(control.sumsq)
+                    control.begin(hparams(HP), max_norm=0.05)
+                    t.set.adamw_step(control)
+                    st.synchronize()
+                    c.sumsq = t.sumsq()
+                    c.begin(HP, 0.05)
+                    follow(c, same_control(control, c, rel=2.0 ** -23))
+                    t.expect(c)
+            st.synchronize()
+        except Exception as e:                                # noqa: BLE001
+            errors.append(e)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(t,)) for t in twins]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not errors, errors
+    for t in twins:
+        t.compare()
+
+
+def test_equal_runs_give_equal_bits_and_another_seed_does_not():
+    def run(seed):
+        t = Twin([50001], "fp16", "none", "mx", seed=30)
+        s = zp.TensorSet(p=t.view["p"], grads=t.view["g"], m=t.view["m"], v=t.view["v"], m_scale=t.view["ms"],
+                         v_scale=t.view["vs"], seed=seed)
+        control = zp.StepControl(scale=1024.0)
+        for _ in range(5):
+            s.grad_sumsq(control.sumsq)
+            control.begin(hparams(HP))
+            s.adamw_step(control)
+        return bits(t.view["p"][0]), bits(t.view["v"][0])
+    a, b, c = run(1), run(1), run(2)
+    assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+    assert not np.array_equal(a[1], c[1])
+
+
+def test_empty_sets_and_many_tiny_tensors():
+    z = [torch.zeros(0, device="cuda")]
+    control = zp.StepControl()
+    s = zp.TensorSet(p=z, grads=z, m=z, v=z)
+    control.sumsq.fill_(7.0)
+    s.grad_sumsq(control.sumsq)
+    assert control.sumsq.item() == 0.0
+    control.begin(hparams(HP[:1]))
+    s.adamw_step(control)
+    assert control.t.item() == 1
+    rng = np.random.default_rng(2)
+    t = Twin([int(x) for x in rng.integers(1, 40, 3000)], "fp16", "bf16", "mx", seed=14)
+    take_step([t], zp.StepControl(scale=1024.0), T.Control(scale=1024.0), max_norm=0.05)
+
+
+def test_a_tensor_past_2_31_elements():
+    """Element numbers past 2^31 and byte offsets past 2^32: the last tiles against the oracle, and the sum."""
+    n = (1 << 31) + 4099
+    g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g[-4099:] = 1.0
+    g[: 1 << 20] = 2.0
+    p = torch.zeros(n, device="cuda")
+    m, v = (torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ms, vs = (torch.zeros(-(-n // 32), dtype=torch.uint8, device="cuda") for _ in range(2))
+    s = zp.TensorSet(p=[p], grads=[g], m=[m], v=[v], m_scale=[ms], v_scale=[vs], seed=5)
+    control, c = zp.StepControl(), T.Control()
+    s.grad_sumsq(control.sumsq)
+    assert control.sumsq.item() == 4099 + 4 * (1 << 20)
+    control.begin(hparams(HP[:1]), check=False)
+    s.adamw_step(control)
+    torch.cuda.synchronize()
+    c.begin(HP[:1], check=False)
+    follow(c, read(control))
+    k = 4099 + 1024
+    lo = n - n % 1024 - 4096 - 1024
+    k = n - lo
+    hg = g[lo:].float().cpu().numpy()
+    hp, hm, hv = T.adamw(c.consts[0], hg, c.grad_mult, *(np.zeros(k, np.float32) for _ in range(3)))
+    assert np.array_equal(bits(p[lo:]), hp.view(np.int32))
+    for x, sc, want, w in ((m, ms, hm, None), (v, vs, hv, T.chances(k, 5, 0, 1, lo))):
+        code, scale = T.encode(want, w is not None, w)
+        assert np.array_equal(x[lo:].cpu().numpy(), code) and np.array_equal(sc[lo // 32:].cpu().numpy(), scale)
+    middle = slice(1 << 20, lo)                    # no gradient, no state, no decay of zeros
+    assert int(torch.count_nonzero(p[middle])) == 0 and int(torch.count_nonzero(m[middle])) == 0
+
+
+@pytest.mark.parametrize("state", ["fp32", "mx"])
+def test_training_together(state):
+    """The operators as a program uses them: a linear model's gradients through autograd, norm, clip, step and the fp16
+    copies feeding the next pass; p follows a 64-bit AdamW on the same gradients."""
+    torch.manual_seed(0)
+    n_in, n_out, batch = 96, 41, 64
+    x = torch.randn(batch, n_in, device="cuda")
+    y = x @ torch.randn(n_in, n_out, device="cuda") * 0.1
+    p = [torch.randn(n_in, n_out, device="cuda") * 0.02, torch.zeros(n_out, device="cuda")]
+    low = [q.half().requires_grad_() for q in p]
+    for q in low:
+        q.grad = torch.zeros_like(q)
+    st = dict(m=[torch.zeros_like(q) for q in p], v=[torch.zeros_like(q) for q in p])
+    if state == "mx":
+        st = {k: [torch.zeros(q.shape, dtype=torch.float8_e4m3fn, device="cuda") for q in p] for k in "mv"}
+        st.update({k: [torch.zeros(-(-q.numel() // 32), dtype=torch.uint8, device="cuda") for q in p] for k in ("m_scale", "v_scale")})
+    s = zp.TensorSet(p=p, grads=[q.grad for q in low], out=[q.data for q in low], groups=[0, 1], **st)
+    control = zp.StepControl(scale=64.0)
+    ref = [q.double().cpu().numpy().ravel() for q in p]
+    rm, rv = [np.zeros_like(q) for q in ref], [np.zeros_like(q) for q in ref]
+    first = None
+    for step in range(1, 21):
+        for q in low:
+            q.grad.zero_()
+        loss = ((x.half() @ low[0] + low[1]).float() - y).square().mean()
+        (loss * 64.0).backward()
+        first = loss.item() if first is None else first
+        g = [q.grad.double().cpu().numpy().ravel() for q in low]
+        s.grad_sumsq(control.sumsq)
+        control.begin(hparams(HP), max_norm=0.5)
+        s.adamw_step(control)
+        norm = np.sqrt(sum((k ** 2).sum() for k in g)) / 64.0
+        assert abs(control.norm.item() - norm) <= 2.0 ** -22 * norm
+        mult = min(1.0, 0.5 / norm) / 64.0
+        for i in range(2):
+            h = HP[i]
+            rm[i] = h.beta1 * rm[i] + (1 - h.beta1) * g[i] * mult
+            rv[i] = h.beta2 * rv[i] + (1 - h.beta2) * (g[i] * mult) ** 2
+            ref[i] = ref[i] - (h.lr * h.weight_decay * ref[i] + h.lr / (1 - h.beta1 ** step) * rm[i] /
+                               (np.sqrt(rv[i]) / np.sqrt(1 - h.beta2 ** step) + h.eps))
+        assert torch.equal(low[0].detach(), p[0].half()) and torch.equal(low[1].detach(), p[1].half())
+    assert control.t.item() == 20 and np.isfinite(loss.item())
+    if state == "fp32":
+        # a step is off by at most p_off, about 16 U of |update| <= 8 lr here and U |p|; the updates' own errors add up
+        for q, r in zip(p, ref):
+            assert np.abs(q.cpu().numpy().ravel() - r).max() <= 20 * (T.U * np.abs(r).max() + 16 * T.U * 8 * 2e-3) * 2
+
+
+def test_kernel_timing_covers_the_set_calls():
+    t = Twin([50001], "fp16", "fp16", "fp32", seed=40)
+    control = zp.StepControl(scale=1024.0)
+    zp.set_kernel_timing(True)
+    try:
+        t.set.grad_sumsq(control.sumsq)
+        control.begin(hparams(HP))
+        t.set.adamw_step(control)
+        assert len(zp.kernel_times()) == 2 and all(0 < x < 100 for x in zp.kernel_times())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            t.set.adamw_step(control)                         # captured: not timed
+        assert len(zp.kernel_times()) == 2
+        t.set.adamw_step(control)
+        assert len(zp.kernel_times()) == 3
+    finally:
+        zp.set_kernel_timing(False)
