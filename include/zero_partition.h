@@ -550,7 +550,9 @@ int zero_step_begin(zero_step_control* ctl, const zero_adam_hparams* groups, int
  *   p = p - (lr * weight_decay * p + lr / (1 - beta1^t) * (m / (sqrt(v) / sqrt(1 - beta2^t) + eps)))
  *   out = p rounded to nearest even
  * with the hyper-parameters of the tensor's group and lr * lr_mult for lr, in
- * fp32.  Several sets can follow one zero_step_begin.
+ * fp32, one rounding an operation.  With MXFP8 states root and quotient are the
+ * hardware's approximations, within 1 ulp each, and v counts as 2^-126 at least
+ * under the root.  Several sets can follow one zero_step_begin.
  *   ctl       device, as zero_step_begin left it on this stream
  *   n_groups  as given to zero_step_begin; every tensor's group is below it
  * The set's gradients must be finite unless the step was begun with check = 1

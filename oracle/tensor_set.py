@@ -72,13 +72,16 @@ def encode(x, positive, chance=None):
     s = scale_bytes(np.abs(_blocks(x)).max(1) if x.size else np.zeros(0))
     with np.errstate(under="ignore"):
         y = x * np.repeat(np.ldexp(np.float32(1), 127 - s).astype(np.float32), BLOCK)[:x.size]
-    if chance is not None:
-        lift = np.where(y < np.float32(2.0 ** -6), np.float32(2.0 ** -6), np.float32(0))
-        up = (chance.astype(np.uint32) << 4) | np.uint32(8)
-        y = (((y + lift).view(np.uint32) + up) & np.uint32(0xFFF00000)).view(np.float32) - lift
-    code = e4m3_nearest(y)
     if positive:
-        code = np.maximum(code, (x > 0).astype(np.uint8))
+        y = np.maximum(y, np.where(x > 0, np.float32(2.0 ** -9), np.float32(0)))
+    if chance is None:
+        return e4m3_nearest(y), s.astype(np.uint8)
+    # the next number below and the share of the step to the one above, in which 20 bits are added and cut off; below
+    # 2^-6 the steps are 2^-9
+    up = (chance.astype(np.int64) << 4) | 8
+    _, e = np.frexp(np.maximum(y, np.float32(2.0 ** -6)))
+    step = np.ldexp(1.0, e - 4)
+    code = e4m3_nearest(np.floor(y.astype(np.float64) / step + up / 2.0 ** 20) * step)
     return code, s.astype(np.uint8)
 
 
@@ -114,6 +117,7 @@ class Control:
     grad_mult: float = 0.0
     sumsq: float = 0.0
     consts: list = field(default_factory=list)
+    groups: list = field(default_factory=list)
 
     def begin(self, groups, max_norm=0.0, check=True, scaler=None):
         scale = float(np.float32(self.scale))
@@ -126,6 +130,7 @@ class Control:
         self.norm = float(np.float32(norm))
         self.grad_mult = float(np.float32(clip / scale)) if ok else 0.0
         self.skip = 0 if ok else 1
+        self.groups = list(groups)
         if ok:
             self.t += 1
             self.consts = []
@@ -165,7 +170,7 @@ def adamw(c, grad, mult, p, m, v):
     return p, m, v
 
 
-def adamw_wide(h, lr_mult, t, grad, mult, p, m, v):
+def adamw_wide(h, lr_mult, t, grad, mult, p, m, v, fast=False):
     """((p, m, v) in 64 bits, how far fp32 results may be from each).  `mult` is the exact factor, clip / scale.
 
     Each rounding to fp32 is off by U relative at most.  g: the factor's and the product's.  beta1 m: the product's and
@@ -173,6 +178,8 @@ def adamw_wide(h, lr_mult, t, grad, mult, p, m, v):
     twice g's two and its own; v: those 5, its product's and the sum's: 7 U of its terms, none of them negative.  den:
     half of v's 7 and sqrt's own, the constant's, the product's and the sum's: 7.5 U.  m / den: m's error over den, den's
     7.5 and the quotient's; times the step: 2 more; the term with p: 2; the sum of the two and the difference: 1 each.
+    fast (the step with MXFP8 states): root and reciprocal are within 1 ulp, 2 U, each where sqrt and the quotient were
+    within 1: a product takes the quotient's place, so 12 become 14; v counts as 2^-126 at least under the root.
     U stands for U (1 + 16 U); subnormal results add 2^-149 a rounding."""
     w = np.float64
     p, m, v, g = p.astype(w), m.astype(w), v.astype(w), grad.astype(w) * mult
@@ -182,12 +189,12 @@ def adamw_wide(h, lr_mult, t, grad, mult, p, m, v):
     m_off = 4 * u * (np.abs(m1) + np.abs(m2)) + tiny
     v_new = h.beta2 * v + (1 - h.beta2) * g * g
     v_off = 7 * u * v_new + tiny
-    den = np.sqrt(v_new) / np.sqrt(1 - h.beta2 ** t) + h.eps
+    den = np.sqrt(np.maximum(v_new, 2.0 ** -126) if fast else v_new) / np.sqrt(1 - h.beta2 ** t) + h.eps
     step = lr / (1 - h.beta1 ** t)
     update = step * m_new / den
     decay = lr * h.weight_decay * p
     p_new = p - (decay + update)
-    p_off = np.abs(step) * m_off / den + 12 * u * np.abs(update) + 4 * u * np.abs(decay) + u * np.abs(p_new) + tiny
+    p_off = np.abs(step) * m_off / den + (14 if fast else 12) * u * np.abs(update) + 4 * u * np.abs(decay) + u * np.abs(p_new) + tiny
     # where v is subnormal its absolute error reaches den through a root
     p_off += np.abs(update) / den * np.sqrt(tiny) * (v_new < 2.0 ** -120)
     return (p_new, m_new, v_new), (p_off, m_off, v_off)

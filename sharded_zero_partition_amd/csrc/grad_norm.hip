@@ -18,7 +18,7 @@ constexpr int kWaves = kThreads / 64;
 constexpr int64_t kMaxBlocks = 2048;   // 8 blocks of 4 waves on each of 256 CUs
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 
 template <typename T>
 using Global = __attribute__((address_space(1))) T;
@@ -28,19 +28,22 @@ struct Grad;
 template <>
 struct Grad<ZERO_DTYPE_FP16> {
     typedef uint16_t elem;
-    typedef u16x4 at __attribute__((aligned(2)));
+    typedef u16x8 at __attribute__((aligned(2)));
+    static constexpr int kWide = 8, kLoads = int(kSetTile) / 512;
     static __device__ __forceinline__ double wide(uint16_t x) { return double(float(__builtin_bit_cast(_Float16, x))); }
 };
 template <>
 struct Grad<ZERO_DTYPE_BF16> {
     typedef uint16_t elem;
-    typedef u16x4 at __attribute__((aligned(2)));
+    typedef u16x8 at __attribute__((aligned(2)));
+    static constexpr int kWide = 8, kLoads = int(kSetTile) / 512;
     static __device__ __forceinline__ double wide(uint16_t x) { return double(__builtin_bit_cast(float, uint32_t(x) << 16)); }
 };
 template <>
 struct Grad<ZERO_DTYPE_FP32> {
     typedef float elem;
     typedef f32x4 at __attribute__((aligned(4)));
+    static constexpr int kWide = 4, kLoads = int(kSetTile) / 256;
     static __device__ __forceinline__ double wide(float x) { return double(x); }
 };
 
@@ -68,22 +71,24 @@ __global__ __launch_bounds__(kThreads) void sumsq_kernel(const SetLaunch a, doub
          w += int64_t(gridDim.x) * kWaves) {
         const TileRec tile = a.tile[w];
         const TensorRec& r = a.rec[tile.tensor];
-        const int64_t base = int64_t(tile.tile) * kSetTile;
+        const int64_t base = int64_t(tile.tile) * kSetTile - tile_shift(r.grad, int(sizeof(typename T::elem)), r.spare);
         const auto* g = (Global<const typename T::elem>*)r.grad + base;
         const int64_t left = r.numel - base;
-        if (left >= kSetTile) {
-            typename T::at x[4];
+        if (base >= 0 && left >= kSetTile) {
+            typename T::at x[T::kLoads];
 #pragma unroll
-            for (int h = 0; h < 4; ++h) x[h] = *(Global<const typename T::at>*)(g + h * 256 + 4 * lane);
+            for (int h = 0; h < T::kLoads; ++h) x[h] = *(Global<const typename T::at>*)(g + (h * 64 + lane) * T::kWide);
 #pragma unroll
-            for (int h = 0; h < 4; ++h)
+            for (int h = 0; h < T::kLoads; ++h)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < T::kWide; ++k) {
                     const double y = T::wide(x[h][k]);
                     s += y * y;
                 }
         } else {
-            for (int e = lane; e < int(left); e += 64) {
+            const int lo = base < 0 ? int(-base) : 0, hi = left < kSetTile ? int(left) : int(kSetTile);
+#pragma unroll 4
+            for (int e = lo + lane; e < hi; e += 64) {
                 const double y = T::wide(g[e]);
                 s += y * y;
             }

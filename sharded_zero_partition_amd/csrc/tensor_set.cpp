@@ -23,6 +23,8 @@ struct zero_tensor_set {
     int32_t out_type = ZERO_DTYPE_NONE;
     bool has_p = false;
     bool has_grads = false;
+    bool staged_step = false;
+    bool staged_codes = false;
     int32_t max_group = 0;
     int64_t n_tiles = 0;
     std::vector<int64_t> numel;              // as given, empty tensors too
@@ -101,7 +103,8 @@ int check_set_device(const zero_tensor_set* set, void* stream, const char* who) 
 }
 
 SetLaunch set_launch(const zero_tensor_set* s) {
-    return SetLaunch{s->d_rec, s->d_tile, s->n_tiles, s->grad_type, s->state_type, s->out_type};
+    return SetLaunch{s->d_rec, s->d_tile, s->n_tiles, s->grad_type, s->state_type, s->out_type,
+                     s->staged_step, s->staged_codes};
 }
 
 // Events for a timed call; none while its stream is being captured (a graph's
@@ -165,7 +168,16 @@ int create(const zero_tensor* tensors, int64_t n, int32_t grad_type, int32_t sta
         if (st && (!is_aligned(t.m, sw) || !is_aligned(t.v, sw)))
             return fail(ZERO_ERR_ALIGNMENT, "a state lacks its element's alignment");
         if (t.out && !is_aligned(t.out, 2)) return fail(ZERO_ERR_ALIGNMENT, "out is not 2-byte aligned");
-        const int64_t tiles = (t.numel - 1) / kSetTile + 1;
+        if (t.numel > kMaxSetTiles * kSetTile) return fail(ZERO_ERR_OUT_OF_MEMORY, "more than 2^25 tiles of 1024 elements");
+        // the arrays that a step or a conversion writes come first; the tiles
+        // reach the end with any of their shifts
+        int64_t shift = 0;
+        const uint32_t any = uint32_t(kSetTile);
+        if (t.p) shift = tile_shift(t.p, 4, any);
+        if (state_type == ZERO_DTYPE_FP32) shift = std::max<int64_t>(shift, tile_shift(t.m, 4, any));
+        if (mx) shift = ((reinterpret_cast<uintptr_t>(t.p) / 4) | reinterpret_cast<uintptr_t>(t.m)) & 32;
+        if (!t.p && !st && t.grad) shift = tile_shift(t.grad, dtype_bytes(grad_type), any);
+        const int64_t tiles = (t.numel + shift - 1) / kSetTile + 1;
         if (tiles > kMaxSetTiles - set->n_tiles) return fail(ZERO_ERR_OUT_OF_MEMORY, "more than 2^25 tiles of 1024 elements");
         set->n_tiles += tiles;
         set->max_group = std::max(set->max_group, t.group);
@@ -189,6 +201,11 @@ int create(const zero_tensor* tensors, int64_t n, int32_t grad_type, int32_t sta
         r.numel = t.numel;
         r.key = mix32(mix32(seed) + uint32_t(i));
         r.group = t.group;
+        r.spare = uint32_t(tiles * kSetTile - t.numel);
+        if (mx) {
+            set->staged_step |= !step_on_sectors(r);
+            set->staged_codes |= !codes_on_sectors(r);
+        }
         set->rec.push_back(r);
     }
     std::sort(set->states.begin(), set->states.end());
@@ -205,7 +222,7 @@ int create(const zero_tensor* tensors, int64_t n, int32_t grad_type, int32_t sta
     std::vector<TileRec> tiles;
     tiles.reserve(size_t(set->n_tiles));
     for (size_t k = 0; k < set->rec.size(); ++k)
-        for (int64_t j = 0; j * kSetTile < set->rec[k].numel; ++j) tiles.push_back({uint32_t(k), uint32_t(j)});
+        for (int64_t j = 0; j * kSetTile < set->rec[k].numel + set->rec[k].spare; ++j) tiles.push_back({uint32_t(k), uint32_t(j)});
 
     hipError_t e = hipGetDevice(&set->device);
     if (e != hipSuccess) return fail_hip(e, "hipGetDevice");
@@ -405,7 +422,7 @@ extern "C" int zero_states_convert(const zero_tensor_set* dst, const zero_tensor
     int rc = zp::check_set_device(dst, stream, "zero_states_convert");
     if (rc == ZERO_OK) rc = zp::check_set_device(src, stream, "zero_states_convert");
     if (rc != ZERO_OK) return rc;
-    if (src->n_tiles == 0) return ZERO_OK;
+    if (dst->n_tiles == 0) return ZERO_OK;
     hipStream_t s = static_cast<hipStream_t>(stream);
     zp::KernelEvents ev;
     bool timed = false;

@@ -18,17 +18,54 @@ struct TensorRec {
     int64_t numel;
     uint32_t key;     // of the tensor's random bits: mix32(mix32(seed) + index)
     int32_t group;
-    int64_t pad;
+    uint32_t spare;   // tiles * kSetTile - numel
+    uint32_t reserved;
 };
 static_assert(sizeof(TensorRec) == 80, "TensorRec layout");
 
-// A tile is kSetTile consecutive elements of one tensor, from a multiple of
-// kSetTile on (the tensor's last tile may be shorter); one wave takes it.
+// A tile is kSetTile consecutive elements of one tensor; one wave takes it.
+// Tile k of a tensor starts at element k kSetTile - shift, so the first and the
+// last one may be shorter.  The shift (0 .. kAlign - 1) puts an array's whole
+// tiles on kAlign-element boundaries in memory, for 16- and 32-bit elements on
+// lines of 128 bytes: a store that leaves a 64-byte sector unfinished costs
+// about 30% of a pass (state conversion to fp32, 200 M elements: 346 us on
+// sectors, 459 us one element off them), a load off its lines 5 to 10%.  Flat
+// buffers of several kinds mostly start on lines, so one tensor's shift is the
+// same in all of them; where it is not, only the array it was taken from gains.
 constexpr int64_t kSetTile = 1024;
+constexpr int64_t kAlign = 64;
 struct TileRec {
     uint32_t tensor;   // index of its TensorRec
     uint32_t tile;     // which tile of the tensor
 };
+
+// The shift of the tiles for an array of `bytes`-byte elements at p; none where
+// the tensor's tiles would not reach its end.
+__host__ __device__ inline uint32_t tile_shift(const void* p, int bytes, uint32_t spare) {
+    const uint32_t s = uint32_t(reinterpret_cast<uintptr_t>(p) / uintptr_t(bytes)) & uint32_t(kAlign - 1);
+    return s <= spare ? s : 0u;
+}
+// In a set with MXFP8 states blocks do not cross tiles, so a shift is a multiple
+// of the block: 32 where p stands there (codes alone: where they do), else 0.
+__host__ __device__ inline uint32_t block_shift(const TensorRec& r) {
+    const uint32_t s = r.p ? uint32_t(reinterpret_cast<uintptr_t>(r.p) / 4) : uint32_t(reinterpret_cast<uintptr_t>(r.m));
+    return (s & 32u) <= r.spare ? s & 32u : 0u;
+}
+// Whether the whole tiles of an array of `bytes`-byte elements then fill whole
+// 64-byte sectors.
+__host__ __device__ inline bool on_sectors(const void* p, int bytes, uint32_t shift) {
+    return ((reinterpret_cast<uintptr_t>(p) - uintptr_t(bytes) * shift) & 63u) == 0;
+}
+// Those of a step and of a conversion.  Sets with a tensor that is off them run
+// kernels that put such tiles' results in order through LDS first.
+__host__ __device__ inline bool step_on_sectors(const TensorRec& r) {
+    const uint32_t s = block_shift(r);
+    return on_sectors(r.p, 4, s) && on_sectors(r.m, 1, s) && on_sectors(r.v, 1, s) && (!r.out || on_sectors(r.out, 2, s));
+}
+__host__ __device__ inline bool codes_on_sectors(const TensorRec& r) {
+    const uint32_t s = block_shift(r);
+    return on_sectors(r.m, 1, s) && on_sectors(r.v, 1, s);
+}
 constexpr int64_t kMaxSetTiles = int64_t(1) << 25;
 static_assert(kMaxSetTiles <= kMaxGridWaves, "one wave per tile fits one launch");
 static_assert(kSetTile % ZERO_STATE_BLOCK == 0, "blocks do not cross tiles");
@@ -50,6 +87,8 @@ struct SetLaunch {
     int32_t grad_type;
     int32_t state_type;
     int32_t out_type;
+    bool staged_step;      // MXFP8: a tensor whose step, or conversion, is off the sectors
+    bool staged_codes;
 };
 
 // Blocks of the sum-of-squares pass, each of which leaves one double in `work`
@@ -76,7 +115,7 @@ hipError_t launch_step_begin(const BeginLaunch& a, hipStream_t stream);
 
 hipError_t launch_adamw(const SetLaunch& a, const zero_step_control* ctl, hipStream_t stream, const KernelEvents& ev);
 
-// src's states into dst's; the tiles are src's (both sets have the same).
+// src's states into dst's, by dst's tiles.
 hipError_t launch_convert(const SetLaunch& dst, const SetLaunch& src, hipStream_t stream, const KernelEvents& ev);
 
 }  // namespace zp

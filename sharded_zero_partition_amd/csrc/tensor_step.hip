@@ -6,9 +6,11 @@
 //   g = grad_mult * grad
 //   m = beta1 m + (1 - beta1) g         v = beta2 v + (1 - beta2) g^2
 //   p = p - (lr wd p + step (m / (sqrt(v) rbc2 + eps)))
-// in fp32, one rounding per operation in that order, IEEE division and square
-// root, so a scalar reference gives the same bits.
+// in fp32, one rounding per operation in that order, so m, v and with fp32
+// states p equal a scalar reference bit for bit.
 #include <hip/hip_ext.h>
+
+#include <type_traits>
 
 #include "tensor_set.hpp"
 
@@ -24,6 +26,8 @@ constexpr int kGroups = int(kSetTile) / 256;   // 256-element groups of a tile, 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 // Four consecutive elements of type T, at T's own alignment: tensors may start
 // anywhere, and the hardware takes wide global accesses at any address.  The
@@ -50,40 +54,72 @@ struct Four<uint8_t> {   // as one word: the conversions take packed codes
 template <typename T>
 using Global = __attribute__((address_space(1))) T;
 
-// Elements p[0 .. n) (n = 1..4; zeros after them); non-temporal where whole:
-// no line is used again.
+// Which of a lane's four elements exist: [a, b).
+struct Part {
+    int a, b;
+    __device__ __forceinline__ bool none() const { return a >= b; }
+    __device__ __forceinline__ bool all() const { return b - a == 4; }
+    __device__ __forceinline__ bool has(int k) const { return k >= a && k < b; }
+};
+
+// Elements q + [a, b) of a tile, p being where its element 0 is (the same in all
+// lanes; outside the array for a tile that starts before it) and q a lane's
+// first; zeros in the others' places.  Non-temporal where whole: no line is used
+// again.
 template <typename T>
-__device__ __forceinline__ typename Four<T>::vec load4(const T* p, int n) {
+__device__ __forceinline__ typename Four<T>::vec load4(const T* p, uint32_t q, Part n) {
     typedef const typename Four<T>::at at;
-    if (n == 4) return __builtin_nontemporal_load((Global<at>*)p);
-    Global<const T>* q = (Global<const T>*)p;
+    Global<const T>* x = (Global<const T>*)((Global<const char>*)p + q * uint32_t(sizeof(T)));
+    if (n.all()) return __builtin_nontemporal_load((Global<at>*)x);
     typename Four<T>::vec r = {};
-    if constexpr (sizeof(T) == 1) {
 #pragma unroll
-        for (int k = 0; k < 3; ++k)
-            if (k < n) r |= uint32_t(q[k]) << (8 * k);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-            if (k < n) r[k] = q[k];
-    }
+    for (int k = 0; k < 4; ++k)
+        if (n.has(k)) {
+            if constexpr (sizeof(T) == 1) r |= uint32_t(x[k]) << (8 * k);
+            else r[k] = x[k];
+        }
     return r;
 }
 
 template <typename T>
-__device__ __forceinline__ void store4(T* p, typename Four<T>::vec v, int n) {
+__device__ __forceinline__ void store4(T* p, uint32_t q, typename Four<T>::vec v, Part n) {
     typedef typename Four<T>::at at;
-    if (n == 4) {
-        __builtin_nontemporal_store(v, (Global<at>*)p);
+    Global<T>* x = (Global<T>*)((Global<char>*)p + q * uint32_t(sizeof(T)));
+    if (n.all()) {
+        __builtin_nontemporal_store(v, (Global<at>*)x);
         return;
     }
-    Global<T>* q = (Global<T>*)p;
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
-        if (k < n) {
-            if constexpr (sizeof(T) == 1) q[k] = T(v >> (8 * k));
-            else q[k] = v[k];
+    for (int k = 0; k < 4; ++k)
+        if (n.has(k)) {
+            if constexpr (sizeof(T) == 1) x[k] = T(v >> (8 * k));
+            else x[k] = v[k];
         }
+}
+
+// A tile: elements [lo, hi) of its kSetTile, its element 0 being `base` of the
+// tensor.
+struct Extent {
+    int64_t base;
+    int lo, hi;
+    __device__ __forceinline__ bool whole() const { return hi - lo == int(kSetTile); }
+    template <bool kWhole>
+    __device__ __forceinline__ Part part(uint32_t q) const {
+        if (kWhole) return {0, 4};
+        const auto clamp = [](int x) { return x < 0 ? 0 : x > 4 ? 4 : x; };
+        return {clamp(lo - int(q)), clamp(hi - int(q))};
+    }
+};
+__device__ __forceinline__ Extent extent(const TensorRec& r, uint32_t tile, uint32_t shift) {
+    const int64_t base = int64_t(tile) * kSetTile - shift, left = r.numel - base;
+    return {base, base < 0 ? int(-base) : 0, left >= kSetTile ? int(kSetTile) : left < 0 ? 0 : int(left)};
+}
+
+// Where element 0 of a tile is in an array, as an integer-made pointer: it may
+// lie before the array.
+template <typename T>
+__device__ __forceinline__ T* tile_at(const void* p, int64_t base) {
+    return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(p) + uintptr_t(base * int64_t(sizeof(T))));
 }
 
 // Types behind the ABI's dtype numbers.
@@ -115,28 +151,37 @@ struct Type<ZERO_DTYPE_MXFP8> {
 // MXFP8 states: a block of 32 elements is 8 neighbouring lanes with 4 each
 // ---------------------------------------------------------------------------
 
-// Largest x (>= 0) of the 8 lanes of this lane's block: three exchanges inside
-// a row, no LDS.
-__device__ __forceinline__ float block_max(float x) {
-    const auto other = [](float v, auto ctrl) {
-        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 0xF, 0xF, false));
+// Largest of the 8 lanes' values, bits of fp32s that are not negative (these
+// order like the numbers): three exchanges inside a row, no LDS.
+__device__ __forceinline__ uint32_t block_max(uint32_t x) {
+    const auto other = [](uint32_t v, auto ctrl) {
+        return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), decltype(ctrl)::value, 0xF, 0xF, true));
     };
-    x = fmaxf(x, other(x, std::integral_constant<int, 0xB1>{}));    // lanes 1, 0, 3, 2 of each four
-    x = fmaxf(x, other(x, std::integral_constant<int, 0x4E>{}));    // lanes 2, 3, 0, 1
-    return fmaxf(x, other(x, std::integral_constant<int, 0x141>{}));   // eight lanes mirrored
+    const auto larger = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+    x = larger(x, other(x, std::integral_constant<int, 0xB1>{}));    // lanes 1, 0, 3, 2 of each four
+    x = larger(x, other(x, std::integral_constant<int, 0x4E>{}));    // lanes 2, 3, 0, 1
+    return larger(x, other(x, std::integral_constant<int, 0x141>{}));   // eight lanes mirrored
 }
+__device__ __forceinline__ uint32_t max4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    const uint32_t x = a > b ? a : b, y = c > d ? c : d;
+    return x > y ? x : y;
+}
+__device__ __forceinline__ uint32_t bits(float x) { return __builtin_bit_cast(uint32_t, x); }
+__device__ __forceinline__ float number(uint32_t x) { return __builtin_bit_cast(float, x); }
 
-// The scale byte of a block whose largest magnitude is `top`: the least s >= 1
-// with top 2^(127 - s) <= 448 = 1.75 2^8.  The exponent of top less 8, and one
-// more when its fraction is above 1.75.
-__device__ __forceinline__ int scale_of(float top) {
-    const int e = int((__builtin_bit_cast(uint32_t, top) + 0x1FFFFFu) >> 23) - 8;
+// The scale byte of a block whose largest magnitude has the bits `top`: the
+// least s >= 1 with top 2^(127 - s) <= 448 = 1.75 2^8.  The exponent of top less
+// 8, and one more when its fraction is above 1.75.
+__device__ __forceinline__ int scale_of(uint32_t top) {
+    const int e = int((top + 0x1FFFFFu) >> 23) - 8;
     return e > 1 ? e : 1;
 }
-__device__ __forceinline__ float two_to(int biased) { return __builtin_bit_cast(float, biased << 23); }
 
 // 2^(s - 127).  s = 0 is 2^-127, below the normal range.
-__device__ __forceinline__ float scale_value(int s) { return s ? two_to(s) : __builtin_bit_cast(float, 0x00400000); }
+__device__ __forceinline__ float scale_value(int s) {
+    const uint32_t b = uint32_t(s) << 23;
+    return number(b > 0x00400000u ? b : 0x00400000u);
+}
 
 __device__ __forceinline__ void decode4(uint32_t code, int s, float x[4]) {
     const float f = scale_value(s);
@@ -156,38 +201,37 @@ __device__ __forceinline__ uint32_t encode4(const float y[4]) {
 
 // The multiplier into a block's range, 2^(127 - s), exact for any value but
 // those that fall below fp32's normal range.
-__device__ __forceinline__ float into_block(int s) { return two_to(254 - s); }
+__device__ __forceinline__ float into_block(int s) { return number(uint32_t(254 - s) << 23); }
 
 __device__ __forceinline__ uint32_t encode_m(const float m[4], int* s) {
-    *s = scale_of(block_max(fmaxf(fmaxf(fabsf(m[0]), fabsf(m[1])), fmaxf(fabsf(m[2]), fabsf(m[3])))));
+    constexpr uint32_t kMag = 0x7FFFFFFFu;
+    *s = scale_of(block_max(max4(bits(m[0]) & kMag, bits(m[1]) & kMag, bits(m[2]) & kMag, bits(m[3]) & kMag)));
     const float f = into_block(*s);
     const float y[4] = {m[0] * f, m[1] * f, m[2] * f, m[3] * f};
     return encode4(y);
 }
 
-// v (>= 0), to nearest, or to a neighbour at random where `chance` is given
-// (16 random bits for each element); a value above zero gets at least code 1.
-// At random: the lower 20 bits of an fp32 are what an e4m3 has no room for;
-// adding random ones below them and cutting them off rounds up as often as they
-// say.  Below 2^-6 an e4m3's steps stay 2^-9, the steps of [2^-6, 2^-5): such
-// values are lifted into that range, rounded there and lowered again.
+// v (>= 0), to nearest, or to a neighbour at random; a value above zero gets at
+// least code 1.  At random: r0 holds 16 random bits for each of the first two
+// elements, r1 for the others.  The conversion adds the upper 20 bits of its
+// operand below the bits that an e4m3 has room for and cuts off there, so it
+// rounds up as often as they say; the 16 are followed by 1000, the middle of
+// what they leave open.
 template <bool kRandom>
-__device__ __forceinline__ uint32_t encode_v(const float v[4], const uint32_t* chance, int* s) {
-    *s = scale_of(block_max(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]))));
+__device__ __forceinline__ uint32_t encode_v(const float v[4], uint32_t r0, uint32_t r1, int* s) {
+    *s = scale_of(block_max(max4(bits(v[0]), bits(v[1]), bits(v[2]), bits(v[3]))));
     const float f = into_block(*s);
     float y[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const float x = v[k] * f;
-        y[k] = x;
-        if (kRandom) {
-            const float lift = x < 0x1p-6f ? 0x1p-6f : 0.0f;
-            const uint32_t up = (chance[k] << 4) | 8u;
-            y[k] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x + lift) + up) & 0xFFF00000u) - lift;
-        }
-        y[k] = fmaxf(y[k], v[k] > 0.0f ? 0x1p-9f : 0.0f);
+        const float x = v[k] * f, least = v[k] > 0.0f ? 0x1p-9f : 0.0f;
+        y[k] = x > least ? x : least;
     }
-    return encode4(y);
+    if (!kRandom) return encode4(y);
+    int c = __builtin_amdgcn_cvt_sr_fp8_f32(y[0], (r0 << 16) | 0x8000u, 0, 0);
+    c = __builtin_amdgcn_cvt_sr_fp8_f32(y[1], (r0 & 0xFFFF0000u) | 0x8000u, c, 1);
+    c = __builtin_amdgcn_cvt_sr_fp8_f32(y[2], (r1 << 16) | 0x8000u, c, 2);
+    return uint32_t(__builtin_amdgcn_cvt_sr_fp8_f32(y[3], (r1 & 0xFFFF0000u) | 0x8000u, c, 3));
 }
 
 // ---------------------------------------------------------------------------
@@ -257,11 +301,23 @@ __global__ __launch_bounds__(64) void step_begin_kernel(const BeginLaunch a) {
     c->good_steps = good;
 }
 
+// kFast (states in 8 bits): root and quotient by the hardware's approximations,
+// within 1 ulp each, which puts the update within 14 half-ulps instead of 12 of
+// the formula's; the states it came from are off by 2^-4.  IEEE's sequences cost
+// 21 of 78 instructions an element, and this kernel is bound by them as much as
+// by memory.  The approximate root takes no subnormals: v counts as 2^-126 at
+// least there.
+template <bool kFast>
 __device__ __forceinline__ void adamw_element(const Consts& c, float g, float& p, float& m, float& v) {
     m = c.beta1 * m + c.omb1 * g;
     v = c.beta2 * v + c.omb2 * (g * g);
-    const float den = __builtin_sqrtf(v) * c.rbc2 + c.eps;
-    p = p - (c.decay * p + c.step * (m / den));
+    if (kFast) {
+        const float den = __builtin_amdgcn_sqrtf(v > 0x1p-126f ? v : 0x1p-126f) * c.rbc2 + c.eps;
+        p = p - (c.decay * p + c.step * (m * __builtin_amdgcn_rcpf(den)));
+    } else {
+        const float den = __builtin_sqrtf(v) * c.rbc2 + c.eps;
+        p = p - (c.decay * p + c.step * (m / den));
+    }
 }
 
 template <int G, int S>
@@ -272,50 +328,126 @@ struct TileIn {
     int ms[kGroups], vs[kGroups];
 };
 
-// Elements that a lane has from `e` on: 0..4.
-__device__ __forceinline__ int count4(int64_t numel, int64_t e) {
-    const int64_t left = numel - e;
-    return left >= 4 ? 4 : left > 0 ? int(left) : 0;
-}
-
 template <int G, int S, bool kWhole>
-__device__ __forceinline__ void load_tile(const TensorRec& r, int64_t base, int lane, TileIn<G, S>& t) {
+__device__ __forceinline__ void load_tile(const TensorRec& r, const Extent& x, int lane, TileIn<G, S>& t) {
     typedef typename Type<G>::elem GT;
     typedef typename Type<S>::elem ST;
+    const GT* g = tile_at<GT>(r.grad, x.base);
+    const float* p = tile_at<float>(r.p, x.base);
+    const ST *m = tile_at<ST>(r.m, x.base), *v = tile_at<ST>(r.v, x.base);
+    const uint8_t* ms = tile_at<uint8_t>(r.m_scale, x.base / ZERO_STATE_BLOCK);
+    const uint8_t* vs = tile_at<uint8_t>(r.v_scale, x.base / ZERO_STATE_BLOCK);
 #pragma unroll
     for (int h = 0; h < kGroups; ++h) {
-        const int64_t e = base + h * 256 + 4 * lane;
-        const int n = kWhole ? 4 : count4(r.numel, e);
-        if (n == 0) {
-            t.g[h] = {};
-            t.p[h] = {};
-            t.m[h] = {};
-            t.v[h] = {};
-            t.ms[h] = t.vs[h] = 1;
-            continue;
-        }
-        t.g[h] = load4(static_cast<const GT*>(r.grad) + e, n);
-        t.p[h] = load4(r.p + e, n);
-        t.m[h] = load4(static_cast<const ST*>(r.m) + e, n);
-        t.v[h] = load4(static_cast<const ST*>(r.v) + e, n);
-        if constexpr (S == ZERO_DTYPE_MXFP8) {
-            const int64_t b = e / ZERO_STATE_BLOCK;
-            t.ms[h] = ((Global<const uint8_t>*)r.m_scale)[b];
-            t.vs[h] = ((Global<const uint8_t>*)r.v_scale)[b];
+        const uint32_t q = h * 256 + 4 * lane;
+        const Part n = x.part<kWhole>(q);
+        t.g[h] = {};
+        t.p[h] = {};
+        t.m[h] = {};
+        t.v[h] = {};
+        t.ms[h] = t.vs[h] = 1;
+        if (n.none()) continue;
+        t.g[h] = load4(g, q, n);
+        t.p[h] = load4(p, q, n);
+        t.m[h] = load4(m, q, n);
+        t.v[h] = load4(v, q, n);
+        if constexpr (S == ZERO_DTYPE_MXFP8) {   // a tile starts with a block
+            t.ms[h] = ((Global<const uint8_t>*)ms)[q / ZERO_STATE_BLOCK];
+            t.vs[h] = ((Global<const uint8_t>*)vs)[q / ZERO_STATE_BLOCK];
         }
     }
 }
 
-template <int G, int O, int S, bool kWhole>
-__device__ __forceinline__ void step_tile(const TensorRec& r, const Consts& c, float mult, uint32_t key, int64_t base,
-                                          int lane) {
+template <int O>
+__device__ __forceinline__ u16x4 narrow4(const float p[4]) {
+    return u16x4{Type<O>::narrow(p[0]), Type<O>::narrow(p[1]), Type<O>::narrow(p[2]), Type<O>::narrow(p[3])};
+}
+
+// ---- results that leave through LDS ----------------------------------------
+
+// One wave's results in a tile's own order, 16 bytes past the end for the reads
+// of whole vectors.
+template <int BYTES>
+struct Staged {
+    u32x4 v[kSetTile * BYTES / 16 + 1];
+};
+
+// The wave's LDS accesses complete in order; the fences keep the compiler from
+// reordering them.
+__device__ __forceinline__ void staged_written() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Elements [lo, hi) of a tile (0..kSetTile) to memory, `at` being where its
+// element 0 belongs (maybe outside the tensor): lane l takes the aligned 16
+// bytes l of each KiB, so every sector but the two at the ends is written whole
+// by one instruction.  A vector's bytes are cut out of two staged ones; the cut
+// is the same for all lanes.
+template <int BYTES>
+__device__ __forceinline__ void store_staged(const Staged<BYTES>& s, uintptr_t at, int lo, int hi, int lane) {
+    typedef std::conditional_t<BYTES == 1, uint8_t, std::conditional_t<BYTES == 2, uint16_t, uint32_t>> elem;
+    const int mis = int(at & 63u);
+    const int cut = (16 - (mis & 15)) & 15;
+    lo *= BYTES;
+    hi *= BYTES;
+#pragma unroll
+    for (int i = 0; i < (int(kSetTile) * BYTES + 63 + 1023) / 1024; ++i) {
+        const int c = i * 1024 + lane * 16 - mis;   // byte of the tile that the vector starts with
+        if (c >= lo && c + 16 <= hi) {
+            const u32x4 a = s.v[(c - cut) / 16], b = s.v[(c - cut) / 16 + 1];
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            u32x4 r;
+            const auto take = [&](int d) {
+                r = u32x4{__builtin_amdgcn_alignbyte(w[d + 1], w[d], cut & 3), __builtin_amdgcn_alignbyte(w[d + 2], w[d + 1], cut & 3),
+                          __builtin_amdgcn_alignbyte(w[d + 3], w[d + 2], cut & 3),
+                          __builtin_amdgcn_alignbyte(d < 3 ? w[(d + 4) & 7] : w[7], w[d + 3], cut & 3)};
+            };
+            if (cut == 0) r = a;
+            else if (BYTES == 4) {
+                r = cut == 4 ? u32x4{a.y, a.z, a.w, b.x} : cut == 8 ? u32x4{a.z, a.w, b.x, b.y} : u32x4{a.w, b.x, b.y, b.z};
+            } else switch (cut >> 2) {
+                case 0: take(0); break;
+                case 1: take(1); break;
+                case 2: take(2); break;
+                default: take(3); break;
+            }
+            __builtin_nontemporal_store(r, (Global<u32x4>*)(at + uintptr_t(int64_t(c))));
+        } else if (c + 16 > lo && c < hi) {
+            Global<elem>* to = (Global<elem>*)(at + uintptr_t(int64_t(c)));
+            const elem* from = reinterpret_cast<const elem*>(s.v) + c / BYTES;
+#pragma unroll
+            for (int k = 0; k < 16 / BYTES; ++k)
+                if (c + k * BYTES >= lo && c + k * BYTES < hi) to[k] = from[k];
+        }
+    }
+}
+
+template <int O>
+struct StepStage {
+    Staged<4> p;
+    Staged<1> m, v;
+    Staged<O == ZERO_DTYPE_NONE ? 0 : 2> out;
+};
+struct NoStage {};
+
+template <int G, int O, int S, bool kWhole, bool kStaged, typename Stage>
+__device__ __forceinline__ void step_tile(const TensorRec& r, const Consts& c, float mult, uint32_t key, const Extent& x,
+                                          int lane, Stage* stage) {
     typedef typename Type<S>::elem ST;
     TileIn<G, S> t;
-    load_tile<G, S, kWhole>(r, base, lane, t);
+    load_tile<G, S, kWhole>(r, x, lane, t);
+    float* po = tile_at<float>(r.p, x.base);
+    ST *mo = tile_at<ST>(r.m, x.base), *vo = tile_at<ST>(r.v, x.base);
+    uint16_t* oo = tile_at<uint16_t>(r.out, x.base);
+    Global<uint8_t>* ms_out = (Global<uint8_t>*)tile_at<uint8_t>(r.m_scale, x.base / ZERO_STATE_BLOCK);
+    Global<uint8_t>* vs_out = (Global<uint8_t>*)tile_at<uint8_t>(r.v_scale, x.base / ZERO_STATE_BLOCK);
+    const uint32_t pair0 = uint32_t(x.base >> 1) + key;
 #pragma unroll
     for (int h = 0; h < kGroups; ++h) {
-        const int64_t e = base + h * 256 + 4 * lane;
-        const int n = kWhole ? 4 : count4(r.numel, e);
+        const uint32_t q = h * 256 + 4 * lane;
+        const Part n = x.part<kWhole>(q);
         float p[4] = {t.p[h].x, t.p[h].y, t.p[h].z, t.p[h].w};
         float m[4], v[4];
         if constexpr (S == ZERO_DTYPE_MXFP8) {
@@ -326,34 +458,46 @@ __device__ __forceinline__ void step_tile(const TensorRec& r, const Consts& c, f
             for (int k = 0; k < 4; ++k) m[k] = t.m[h][k], v[k] = t.v[h][k];
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) adamw_element(c, Type<G>::wide(t.g[h][k]) * mult, p[k], m[k], v[k]);
+        for (int k = 0; k < 4; ++k)
+            adamw_element<S == ZERO_DTYPE_MXFP8>(c, Type<G>::wide(t.g[h][k]) * mult, p[k], m[k], v[k]);
         if constexpr (S == ZERO_DTYPE_MXFP8) {
-            // every lane takes part in its block's maxima; past the end all are zero
-            const uint32_t pair = uint32_t(e >> 1);
-            const uint32_t r0 = mix32(pair + key), r1 = mix32(pair + 1 + key);
-            const uint32_t chance[4] = {r0 & 0xFFFFu, r0 >> 16, r1 & 0xFFFFu, r1 >> 16};
+            // every lane takes part in its block's maxima, with zeros for
+            // elements that are not there
+            if (!kWhole)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (!n.has(k)) m[k] = v[k] = 0.0f;
+            const uint32_t r0 = mix32(pair0 + (q >> 1)), r1 = mix32(pair0 + (q >> 1) + 1);
             int ms, vs;
-            const uint32_t mc = encode_m(m, &ms), vc = encode_v<true>(v, chance, &vs);
-            if (n > 0) {
-                store4(static_cast<ST*>(r.m) + e, mc, n);
-                store4(static_cast<ST*>(r.v) + e, vc, n);
-                if ((lane & 7) == 0) {
-                    const int64_t b = e / ZERO_STATE_BLOCK;
-                    ((Global<uint8_t>*)r.m_scale)[b] = uint8_t(ms);
-                    ((Global<uint8_t>*)r.v_scale)[b] = uint8_t(vs);
-                }
+            const uint32_t mc = encode_m(m, &ms), vc = encode_v<true>(v, r0, r1, &vs);
+            if (!n.none() && (lane & 7) == 0) {
+                ms_out[q / ZERO_STATE_BLOCK] = uint8_t(ms);
+                vs_out[q / ZERO_STATE_BLOCK] = uint8_t(vs);
             }
-        } else if (n > 0) {
-            store4(static_cast<ST*>(r.m) + e, f32x4{m[0], m[1], m[2], m[3]}, n);
-            store4(static_cast<ST*>(r.v) + e, f32x4{v[0], v[1], v[2], v[3]}, n);
-        }
-        if (n > 0) {
-            store4(r.p + e, f32x4{p[0], p[1], p[2], p[3]}, n);
-            if constexpr (O != ZERO_DTYPE_NONE) {
-                const u16x4 o = {Type<O>::narrow(p[0]), Type<O>::narrow(p[1]), Type<O>::narrow(p[2]), Type<O>::narrow(p[3])};
-                store4(static_cast<uint16_t*>(r.out) + e, o, n);
+            if constexpr (kStaged) {
+                reinterpret_cast<uint32_t*>(stage->m.v)[q / 4] = mc;
+                reinterpret_cast<uint32_t*>(stage->v.v)[q / 4] = vc;
+                stage->p.v[q / 4] = __builtin_bit_cast(u32x4, f32x4{p[0], p[1], p[2], p[3]});
+                if constexpr (O != ZERO_DTYPE_NONE) reinterpret_cast<u32x2*>(stage->out.v)[q / 4] = __builtin_bit_cast(u32x2, narrow4<O>(p));
+                continue;
             }
+            if (n.none()) continue;
+            store4(mo, q, mc, n);
+            store4(vo, q, vc, n);
+        } else {
+            if (n.none()) continue;
+            store4(mo, q, f32x4{m[0], m[1], m[2], m[3]}, n);
+            store4(vo, q, f32x4{v[0], v[1], v[2], v[3]}, n);
         }
+        store4(po, q, f32x4{p[0], p[1], p[2], p[3]}, n);
+        if constexpr (O != ZERO_DTYPE_NONE) store4(oo, q, narrow4<O>(p), n);
+    }
+    if constexpr (kStaged) {
+        staged_written();
+        store_staged<4>(stage->p, reinterpret_cast<uintptr_t>(po), x.lo, x.hi, lane);
+        store_staged<1>(stage->m, reinterpret_cast<uintptr_t>(mo), x.lo, x.hi, lane);
+        store_staged<1>(stage->v, reinterpret_cast<uintptr_t>(vo), x.lo, x.hi, lane);
+        if constexpr (O != ZERO_DTYPE_NONE) store_staged<2>(stage->out, reinterpret_cast<uintptr_t>(oo), x.lo, x.hi, lane);
     }
 }
 
@@ -365,7 +509,7 @@ __device__ __forceinline__ bool wave_tile(const SetLaunch& a, TileRec* tile) {
     return true;
 }
 
-template <int G, int O, int S>
+template <int G, int O, int S, bool kStaged>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(const SetLaunch a, const zero_step_control* __restrict__ ctl) {
     TileRec tile;
     if (!wave_tile(a, &tile) || ctl->skip) return;
@@ -373,61 +517,141 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const SetLaunch a, cons
     const Consts c = *reinterpret_cast<const Consts*>(ctl->group[r.group]);
     const float mult = ctl->grad_mult;
     const uint32_t key = mix32(r.key + uint32_t(ctl->t) * 0x9E3779B9u);
-    const int64_t base = int64_t(tile.tile) * kSetTile;
+    const uint32_t shift = S == ZERO_DTYPE_MXFP8 ? block_shift(r) : tile_shift(r.p, 4, r.spare);
+    const Extent x = extent(r, tile.tile, shift);
+    if (x.hi == 0) return;   // a tile counted for another array's shift
     const int lane = threadIdx.x & 63;
-    if (r.numel - base >= kSetTile) step_tile<G, O, S, true>(r, c, mult, key, base, lane);
-    else step_tile<G, O, S, false>(r, c, mult, key, base, lane);
+    if constexpr (kStaged) {
+        __shared__ StepStage<O> stage[kWaves];
+        if (!step_on_sectors(r)) {
+            StepStage<O>* mine = &stage[threadIdx.x >> 6];
+            if (x.whole()) step_tile<G, O, S, true, true>(r, c, mult, key, x, lane, mine);
+            else step_tile<G, O, S, false, true>(r, c, mult, key, x, lane, mine);
+            return;
+        }
+    }
+    NoStage* none = nullptr;
+    if (x.whole()) step_tile<G, O, S, true, false>(r, c, mult, key, x, lane, none);
+    else step_tile<G, O, S, false, false>(r, c, mult, key, x, lane, none);
 }
-
-template <int G, int O>
-void run_adamw(const SetLaunch& a, const zero_step_control* ctl, dim3 grid, hipStream_t s, const KernelEvents& ev);
 
 // ---------------------------------------------------------------------------
 // state conversion
 // ---------------------------------------------------------------------------
 
-template <bool kEncode>
-__global__ __launch_bounds__(kThreads) void convert_kernel(const SetLaunch dst, const SetLaunch src) {
-    TileRec tile;
-    if (!wave_tile(src, &tile)) return;
-    const TensorRec from = src.rec[tile.tensor], to = dst.rec[tile.tensor];
-    const TensorRec& wide = kEncode ? from : to;
-    const TensorRec& mx = kEncode ? to : from;
-    const int lane = threadIdx.x & 63;
+struct CodeStage {
+    Staged<1> m, v;
+};
+
+template <bool kWhole>
+__device__ __forceinline__ void encode_tile(const TensorRec& to, const TensorRec& from, const Extent& x, int lane,
+                                            CodeStage* stage) {
+    const float *wm = tile_at<float>(from.m, x.base), *wv = tile_at<float>(from.v, x.base);
+    uint8_t *cm = tile_at<uint8_t>(to.m, x.base), *cv = tile_at<uint8_t>(to.v, x.base);
+    Global<uint8_t>* ms_out = (Global<uint8_t>*)tile_at<uint8_t>(to.m_scale, x.base / ZERO_STATE_BLOCK);
+    Global<uint8_t>* vs_out = (Global<uint8_t>*)tile_at<uint8_t>(to.v_scale, x.base / ZERO_STATE_BLOCK);
+    f32x4 m4[kGroups], v4[kGroups];
 #pragma unroll
     for (int h = 0; h < kGroups; ++h) {
-        const int64_t e = int64_t(tile.tile) * kSetTile + h * 256 + 4 * lane;
-        const int n = count4(from.numel, e);
-        const int64_t b = e / ZERO_STATE_BLOCK;
-        float* wm = static_cast<float*>(wide.m) + e;
-        float* wv = static_cast<float*>(wide.v) + e;
-        uint8_t* cm = static_cast<uint8_t*>(mx.m) + e;
-        uint8_t* cv = static_cast<uint8_t*>(mx.v) + e;
-        if (kEncode) {
-            f32x4 m4 = {}, v4 = {};
-            if (n > 0) {
-                m4 = load4(static_cast<const float*>(wm), n);
-                v4 = load4(static_cast<const float*>(wv), n);
-            }
-            const float m[4] = {m4.x, m4.y, m4.z, m4.w}, v[4] = {v4.x, v4.y, v4.z, v4.w};
-            int ms, vs;
-            const uint32_t mc = encode_m(m, &ms), vc = encode_v<false>(v, nullptr, &vs);
-            if (n > 0) {
-                store4(cm, mc, n);
-                store4(cv, vc, n);
-                if ((lane & 7) == 0) {
-                    ((Global<uint8_t>*)mx.m_scale)[b] = uint8_t(ms);
-                    ((Global<uint8_t>*)mx.v_scale)[b] = uint8_t(vs);
-                }
-            }
-        } else if (n > 0) {
-            float m[4], v[4];
-            decode4(load4(static_cast<const uint8_t*>(cm), n), ((Global<const uint8_t>*)mx.m_scale)[b], m);
-            decode4(load4(static_cast<const uint8_t*>(cv), n), ((Global<const uint8_t>*)mx.v_scale)[b], v);
-            store4(wm, f32x4{m[0], m[1], m[2], m[3]}, n);
-            store4(wv, f32x4{v[0], v[1], v[2], v[3]}, n);
+        const uint32_t q = h * 256 + 4 * lane;
+        const Part n = x.part<kWhole>(q);
+        m4[h] = v4[h] = {};
+        if (n.none()) continue;
+        m4[h] = load4(wm, q, n);
+        v4[h] = load4(wv, q, n);
+    }
+#pragma unroll
+    for (int h = 0; h < kGroups; ++h) {
+        const uint32_t q = h * 256 + 4 * lane;
+        const Part n = x.part<kWhole>(q);
+        const float m[4] = {m4[h].x, m4[h].y, m4[h].z, m4[h].w}, v[4] = {v4[h].x, v4[h].y, v4[h].z, v4[h].w};
+        int ms, vs;
+        const uint32_t mc = encode_m(m, &ms), vc = encode_v<false>(v, 0, 0, &vs);
+        if (!n.none() && (lane & 7) == 0) {
+            ms_out[q / ZERO_STATE_BLOCK] = uint8_t(ms);
+            vs_out[q / ZERO_STATE_BLOCK] = uint8_t(vs);
+        }
+        if (stage) {
+            reinterpret_cast<uint32_t*>(stage->m.v)[q / 4] = mc;
+            reinterpret_cast<uint32_t*>(stage->v.v)[q / 4] = vc;
+        } else if (!n.none()) {
+            store4(cm, q, mc, n);
+            store4(cv, q, vc, n);
         }
     }
+    if (!stage) return;
+    staged_written();
+    store_staged<1>(stage->m, reinterpret_cast<uintptr_t>(cm), x.lo, x.hi, lane);
+    store_staged<1>(stage->v, reinterpret_cast<uintptr_t>(cv), x.lo, x.hi, lane);
+}
+
+template <bool kStaged>
+__global__ __launch_bounds__(kThreads) void encode_kernel(const SetLaunch dst, const TensorRec* __restrict__ src) {
+    TileRec tile;
+    if (!wave_tile(dst, &tile)) return;
+    const TensorRec to = dst.rec[tile.tensor], from = src[tile.tensor];
+    const Extent x = extent(to, tile.tile, block_shift(to));
+    if (x.hi == 0) return;
+    const int lane = threadIdx.x & 63;
+    if constexpr (kStaged) {
+        __shared__ CodeStage stage[kWaves];
+        if (!codes_on_sectors(to)) {
+            CodeStage* mine = &stage[threadIdx.x >> 6];
+            if (x.whole()) encode_tile<true>(to, from, x, lane, mine);
+            else encode_tile<false>(to, from, x, lane, mine);
+            return;
+        }
+    }
+    if (x.whole()) encode_tile<true>(to, from, x, lane, nullptr);
+    else encode_tile<false>(to, from, x, lane, nullptr);
+}
+
+// Decoding follows the fp32 arrays' lines, so a lane's four elements (the first
+// of them element e of the tensor) may belong to two blocks.
+__device__ __forceinline__ f32x4 decode_across(uint32_t code, const uint8_t* scale, int64_t e, Part n) {
+    const int64_t b0 = (e + n.a) / ZERO_STATE_BLOCK, b1 = (e + n.b - 1) / ZERO_STATE_BLOCK;
+    const float f0 = scale_value(((Global<const uint8_t>*)scale)[b0]), f1 = scale_value(((Global<const uint8_t>*)scale)[b1]);
+    const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(int(code), false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(int(code), true);
+    f32x4 x = {lo.x, lo.y, hi.x, hi.y};
+    const int first = int((b0 + 1) * ZERO_STATE_BLOCK - e);   // the second block's first element, if it is one of the four
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = x[k] * (k < first ? f0 : f1);
+    return x;
+}
+
+template <bool kWhole>
+__device__ __forceinline__ void decode_tile(const TensorRec& to, const TensorRec& from, const Extent& x, int lane) {
+    float *wm = tile_at<float>(to.m, x.base), *wv = tile_at<float>(to.v, x.base);
+    const uint8_t *cm = tile_at<uint8_t>(from.m, x.base), *cv = tile_at<uint8_t>(from.v, x.base);
+    uint32_t mc[kGroups], vc[kGroups];
+#pragma unroll
+    for (int h = 0; h < kGroups; ++h) {
+        const uint32_t q = h * 256 + 4 * lane;
+        const Part n = x.part<kWhole>(q);
+        mc[h] = vc[h] = 0;
+        if (n.none()) continue;
+        mc[h] = load4(cm, q, n);
+        vc[h] = load4(cv, q, n);
+    }
+#pragma unroll
+    for (int h = 0; h < kGroups; ++h) {
+        const uint32_t q = h * 256 + 4 * lane;
+        const Part n = x.part<kWhole>(q);
+        if (n.none()) continue;
+        store4(wm, q, decode_across(mc[h], from.m_scale, x.base + q, n), n);
+        store4(wv, q, decode_across(vc[h], from.v_scale, x.base + q, n), n);
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void decode_kernel(const SetLaunch dst, const TensorRec* __restrict__ src) {
+    TileRec tile;
+    if (!wave_tile(dst, &tile)) return;
+    const TensorRec to = dst.rec[tile.tensor], from = src[tile.tensor];
+    const Extent x = extent(to, tile.tile, tile_shift(to.m, 4, to.spare));
+    if (x.hi == 0) return;
+    const int lane = threadIdx.x & 63;
+    if (x.whole()) decode_tile<true>(to, from, x, lane);
+    else decode_tile<false>(to, from, x, lane);
 }
 
 dim3 tile_grid(int64_t n_tiles) { return dim3(unsigned((n_tiles + kWaves - 1) / kWaves)); }
@@ -440,8 +664,9 @@ void launch(K kernel, dim3 grid, hipStream_t s, const KernelEvents& ev, Args... 
 
 template <int G, int O>
 void run_adamw(const SetLaunch& a, const zero_step_control* ctl, dim3 grid, hipStream_t s, const KernelEvents& ev) {
-    if (a.state_type == ZERO_DTYPE_MXFP8) launch(adamw_kernel<G, O, ZERO_DTYPE_MXFP8>, grid, s, ev, a, ctl);
-    else launch(adamw_kernel<G, O, ZERO_DTYPE_FP32>, grid, s, ev, a, ctl);
+    if (a.state_type == ZERO_DTYPE_FP32) launch(adamw_kernel<G, O, ZERO_DTYPE_FP32, false>, grid, s, ev, a, ctl);
+    else if (a.staged_step) launch(adamw_kernel<G, O, ZERO_DTYPE_MXFP8, true>, grid, s, ev, a, ctl);
+    else launch(adamw_kernel<G, O, ZERO_DTYPE_MXFP8, false>, grid, s, ev, a, ctl);
 }
 
 template <int G>
@@ -471,9 +696,10 @@ hipError_t launch_adamw(const SetLaunch& a, const zero_step_control* ctl, hipStr
 }
 
 hipError_t launch_convert(const SetLaunch& dst, const SetLaunch& src, hipStream_t stream, const KernelEvents& ev) {
-    const dim3 grid = tile_grid(src.n_tiles);
-    if (src.state_type == ZERO_DTYPE_FP32) launch(convert_kernel<true>, grid, stream, ev, dst, src);
-    else launch(convert_kernel<false>, grid, stream, ev, dst, src);
+    const dim3 grid = tile_grid(dst.n_tiles);
+    if (dst.state_type == ZERO_DTYPE_FP32) launch(decode_kernel, grid, stream, ev, dst, src.rec);
+    else if (dst.staged_codes) launch(encode_kernel<true>, grid, stream, ev, dst, src.rec);
+    else launch(encode_kernel<false>, grid, stream, ev, dst, src.rec);
     return hipGetLastError();
 }
 

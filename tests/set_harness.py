@@ -41,9 +41,10 @@ def to_bits(x, dtype):
 
 
 class Twin:
-    """A set with its own inputs from a seed.  state: "fp32" or "mx"."""
+    """A set with its own inputs from a seed.  state: "fp32" or "mx".  The tensors of each kind lie up to `gap` elements
+    apart, drawn for each kind, or in all kinds by the same `gaps` (buffers start on 512 bytes)."""
 
-    def __init__(self, sizes, grad="fp16", out="fp16", state="fp32", seed=0, groups=None, std=1e-3, scale=1024.0, gap=5):
+    def __init__(self, sizes, grad="fp16", out="fp16", state="fp32", seed=0, groups=None, std=1e-3, scale=1024.0, gap=5, gaps=None):
         rng = np.random.default_rng(seed)
         self.sizes, self.state, self.seed, self.grad_dtype, self.out_dtype = list(sizes), state, seed, GRAD[grad], OUT[out]
         self.groups = [i % 2 for i in range(len(sizes))] if groups is None else groups
@@ -69,10 +70,12 @@ class Twin:
             self.kinds["out"] = self.out_dtype
             host["out"] = [np.zeros(n, np.float32) for n in sizes]
         host["g"] = [np.zeros(n, np.float32) for n in sizes]
-        self.host, self.buf, self.view, self.start = host, {}, {}, {}
+        self.host, self.buf, self.view, self.start, self.bound = host, {}, {}, {}, {}
         for k, dtype in self.kinds.items():
-            gaps = rng.integers(0, gap + 1, len(sizes)) if gap else np.zeros(len(sizes), np.int64)
-            self.buf[k], self.view[k], self.start[k] = guarded(host[k], dtype, gaps)
+            apart = rng.integers(0, gap + 1, len(sizes)) if gaps is None else gaps
+            if gaps is not None and k in ("ms", "vs"):
+                apart = [0] * len(sizes)
+            self.buf[k], self.view[k], self.start[k] = guarded(host[k], dtype, apart)
             for t, a in zip(self.view[k], host[k]):
                 t.copy_(torch.from_numpy(a))
         self.new_grads()
@@ -102,6 +105,9 @@ class Twin:
             mx = self.state == "mx"
             m = T.decode(h["m"][i], h["ms"][i]) if mx else h["m"][i]
             v = T.decode(h["v"][i], h["vs"][i]) if mx else h["v"][i]
+            if mx:      # p by the hardware's root and reciprocal: compared within its bound, then taken over
+                w, off = T.adamw_wide(c.groups[self.groups[i]], float(np.float32(c.lr_mult)), c.t, h["g"][i], c.grad_mult, h["p"][i], m, v, fast=True)
+                self.bound[i] = w[0], off[0]
             p, m, v = T.adamw(c.consts[self.groups[i]], h["g"][i], c.grad_mult, h["p"][i], m, v)
             h["p"][i] = p
             if mx:
@@ -114,6 +120,14 @@ class Twin:
 
     def compare(self, what=""):
         """Every byte of every buffer: tensors as the host has them, guards untouched."""
+        for i, (w, off) in self.bound.items():
+            p = self.view["p"][i].cpu().numpy()
+            d = np.abs(p.astype(np.float64) - w)
+            assert (d <= off).all(), f"{what} p of tensor {i}: {np.max(d / off)} of its bound"
+            self.host["p"][i] = p
+            if "out" in self.host:
+                self.host["out"][i] = p
+        self.bound = {}
         for k, dtype in self.kinds.items():
             size = torch.empty(0, dtype=dtype).element_size()
             want = np.full(self.buf[k].numel(), GUARD, np.uint8)

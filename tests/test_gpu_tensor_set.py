@@ -50,8 +50,9 @@ def take_step(twins, control, c, groups=HP, max_norm=0.0, check=True, scaler=Non
 
 @pytest.mark.parametrize("grad", ["fp16", "bf16", "fp32"])
 def test_sumsq_against_64_bits(grad):
-    for sizes in ([1], [0], [], [1024], [3, 0, 1025], SIZES, [40000] * 30 + [5]):
-        t = Twin(sizes or [0], grad=grad, out="none", seed=len(sizes))
+    for sizes, gaps in (([1], None), ([0], None), ([], None), ([1024], None), ([3, 0, 1025], None), (SIZES, None), ([40000] * 30 + [5], None),
+                        ([2048, 1000, 4096], [64, 0, 24]), ([300000], [17]), ([1024, 1023, 961, 960], [63, 0, 0, 0])):
+        t = Twin(sizes or [0], grad=grad, out="none", seed=len(sizes), gaps=gaps)
         out = torch.full((), -1.0, dtype=torch.float64, device="cuda")
         t.set.grad_sumsq(out)
         first = out.item()
@@ -87,6 +88,35 @@ def test_steps_match_the_oracle(grad, out, state):
 
 
 @pytest.mark.parametrize("state", ["fp32", "mx"])
+@pytest.mark.parametrize("first", [0, 1, 16, 31, 32, 33, 63, 64, 96, 100])
+def test_starts_that_all_kinds_share(first, state):
+    """Tensors whose starts stand in the same place in every buffer: on lines, on half lines, beside them.  Sizes around
+    those at which a shifted tile needs one tile more."""
+    sizes = [5000, 1024 - first % 64, 1025 - first % 64, 64 * 33, 32, 992, 1, 4096 - 32, 960, 961, 31]
+    gaps = [first] + [0, 64, 32, 128, 1, 0, 33, 64, 31, 2][: len(sizes) - 1]
+    t = Twin(sizes, "bf16", "fp16", state, seed=first, gaps=gaps)
+    control, c = zp.StepControl(scale=1024.0), T.Control(scale=1024.0)
+    for step in range(2):
+        t.new_grads()
+        take_step([t], control, c, max_norm=0.05, what=f"step {step}")
+    if state == "mx":
+        wide = [[torch.empty(n + 3, device="cuda")[first % 4: first % 4 + n] if n < 64 else torch.empty(n, device="cuda") for n in sizes] for _ in range(2)]
+        f = zp.TensorSet(m=wide[0], v=wide[1])
+        f.states_from(t.set)
+        for i in range(len(sizes)):
+            for k, s, w in (("m", "ms", wide[0]), ("v", "vs", wide[1])):
+                assert np.array_equal(bits(w[i]), T.decode(t.host[k][i], t.host[s][i]).view(np.int32)), (i, k)
+        for k in ("m", "v", "ms", "vs"):
+            for x in t.view[k]:
+                x.zero_()
+        t.set.states_from(f)
+        for i in range(len(sizes)):
+            for k, s in (("m", "ms"), ("v", "vs")):
+                t.host[k][i], t.host[s][i] = T.encode(T.decode(t.host[k][i], t.host[s][i]), k == "v")
+        t.compare("read back")
+
+
+@pytest.mark.parametrize("state", ["fp32", "mx"])
 def test_a_step_against_64_bits(state):
     """From values that the states hold exactly, p (and fp32 states) within the bound that the roundings add up to."""
     t = Twin([50001, 257, 33], "fp32", "none", state, seed=5)
@@ -100,7 +130,8 @@ def test_a_step_against_64_bits(state):
     for i, b in enumerate(before):
         m = T.decode(b["m"], b["ms"]) if state == "mx" else b["m"]
         v = T.decode(b["v"], b["vs"]) if state == "mx" else b["v"]
-        want, off = T.adamw_wide(HP[i % 2], 1.0, 42, b["g"], 0.05 / norm / 256.0, b["p"], m, v)
+        want, off = T.adamw_wide(HP[i % 2], 1.0, 42, b["g"], 0.05 / norm / 256.0, b["p"], m, v,
+                                 fast=state == "mx")
         names = "p" if state == "mx" else "pmv"
         for k, w, o in zip(names, want, off):
             d = np.abs(t.view[k][i].cpu().numpy().astype(np.float64) - w)
@@ -376,7 +407,7 @@ def test_two_threads_with_their_own_sets():
                     c.begin(HP, 0.05)
                     follow(c, same_control(control, c, rel=2.0 ** -23))
                     t.expect(c)
-            st.synchronize()
+                    t.compare()
         except Exception as e:                                # noqa: BLE001
             errors.append(e)
 
@@ -444,8 +475,10 @@ def test_a_tensor_past_2_31_elements():
     lo = n - n % 1024 - 4096 - 1024
     k = n - lo
     hg = g[lo:].float().cpu().numpy()
-    hp, hm, hv = T.adamw(c.consts[0], hg, c.grad_mult, *(np.zeros(k, np.float32) for _ in range(3)))
-    assert np.array_equal(bits(p[lo:]), hp.view(np.int32))
+    zero = [np.zeros(k, np.float32) for _ in range(3)]
+    _, hm, hv = T.adamw(c.consts[0], hg, c.grad_mult, *zero)
+    wide, off = T.adamw_wide(HP[0], 1.0, 1, hg, 1.0, *zero, fast=True)
+    assert (np.abs(p[lo:].cpu().numpy().astype(np.float64) - wide[0]) <= off[0]).all()
     for x, sc, want, w in ((m, ms, hm, None), (v, vs, hv, T.chances(k, 5, 0, 1, lo))):
         code, scale = T.encode(want, w is not None, w)
         assert np.array_equal(x[lo:].cpu().numpy(), code) and np.array_equal(sc[lo // 32:].cpu().numpy(), scale)

@@ -78,7 +78,7 @@ def test_random_rounding_keeps_the_mean():
     gap = np.maximum(grid[hi] - grid[lo], 0)
     for k in range(32):
         assert set(np.unique(got[:, k])) <= {grid[lo[k]], grid[hi[k]]}
-    inside = x > grid[1]
+    inside = x >= grid[1]
     off = np.abs(got.mean(0) - x)
     assert (off <= 6 * gap / 2 / np.sqrt(N) + gap * 2.0 ** -17 + 1e-9)[inside].all()
 
