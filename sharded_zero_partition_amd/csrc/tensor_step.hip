@@ -365,76 +365,131 @@ __device__ __forceinline__ u16x4 narrow4(const float p[4]) {
 
 // ---- results that leave through LDS ----------------------------------------
 
-// One wave's results in a tile's own order, 16 bytes past the end for the reads
-// of whole vectors.
+// A block's results of one array, wave w's tile from w kSetTile elements on, and
+// 16 bytes past the end for the reads of whole vectors.
 template <int BYTES>
 struct Staged {
-    u32x4 v[kSetTile * BYTES / 16 + 1];
+    u32x4 v[kWaves * kSetTile * BYTES / 16 + 1];
 };
 
-// The wave's LDS accesses complete in order; the fences keep the compiler from
-// reordering them.
-__device__ __forceinline__ void staged_written() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+// How a wave's tile hangs together with its block's others: whether the wave
+// before (after) it has the tile before (after) it of the same tensor, and how
+// many elements that one after it has.
+struct Chain {
+    bool before, after;
+    int next;
+};
+__device__ __forceinline__ Chain chain(const SetLaunch& a, const TileRec& tile, const TensorRec& r, const Extent& x) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t w = int64_t(blockIdx.x) * kWaves + wave;
+    Chain c;
+    c.before = wave > 0 && a.tile[w - 1].tensor == tile.tensor;
+    c.after = wave < kWaves - 1 && w + 1 < a.n_tiles && a.tile[w + 1].tensor == tile.tensor;
+    const int64_t left = r.numel - x.base - kSetTile;
+    c.next = left >= kSetTile ? int(kSetTile) : left > 0 ? int(left) : 0;
+    return c;
 }
 
-// Elements [lo, hi) of a tile (0..kSetTile) to memory, `at` being where its
-// element 0 belongs (maybe outside the tensor): lane l takes the aligned 16
-// bytes l of each KiB, so every sector but the two at the ends is written whole
-// by one instruction.  A vector's bytes are cut out of two staged ones; the cut
-// is the same for all lanes.
-template <int BYTES>
-__device__ __forceinline__ void store_staged(const Staged<BYTES>& s, uintptr_t at, int lo, int hi, int lane) {
-    typedef std::conditional_t<BYTES == 1, uint8_t, std::conditional_t<BYTES == 2, uint16_t, uint32_t>> elem;
-    const int mis = int(at & 63u);
-    const int cut = (16 - (mis & 15)) & 15;
-    lo *= BYTES;
-    hi *= BYTES;
-#pragma unroll
-    for (int i = 0; i < (int(kSetTile) * BYTES + 63 + 1023) / 1024; ++i) {
-        const int c = i * 1024 + lane * 16 - mis;   // byte of the tile that the vector starts with
+// A wave's tile, from the block's staged results to memory; `at` is where its
+// element 0 belongs (maybe outside the tensor).  Lane l takes the aligned 16
+// bytes l of each KiB, so a sector is written whole by one instruction; where
+// the tile's neighbours are in the block too, the wave takes the sectors that
+// begin in its tile, and only the ends of the block's run are left unfinished.
+// (Each wave to its own ends: 648 us for 200 M elements one element off the
+// lines, and 582 us sixteen off.)  A vector is cut out of two staged ones;
+// the cut is the same for all lanes.
+//
+// `vec(c)` is the vector of the tile's bytes c .. c + 15, `one(k)` its
+// element k.
+template <typename T, typename Vec, typename One>
+__device__ __forceinline__ void store_run(uintptr_t at, const Extent& x, const Chain& link, Vec vec, One one) {
+    constexpr int kSize = int(sizeof(T)), kBytes = int(kSetTile) * kSize;
+    const int mis = int(at & 63u), begins = (64 - mis) & 63;   // first sector that begins in the tile
+    const int lo = link.before ? begins : x.lo * kSize;
+    const int to_next = begins < link.next * kSize ? begins : link.next * kSize;
+    const int hi = link.after && x.hi == int(kSetTile) ? kBytes + to_next : x.hi * kSize;
+    for (int c = (link.before ? begins : -mis) + int(threadIdx.x & 63) * 16; c < hi; c += 1024) {
         if (c >= lo && c + 16 <= hi) {
-            const u32x4 a = s.v[(c - cut) / 16], b = s.v[(c - cut) / 16 + 1];
-            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            u32x4 r;
-            const auto take = [&](int d) {
-                r = u32x4{__builtin_amdgcn_alignbyte(w[d + 1], w[d], cut & 3), __builtin_amdgcn_alignbyte(w[d + 2], w[d + 1], cut & 3),
-                          __builtin_amdgcn_alignbyte(w[d + 3], w[d + 2], cut & 3),
-                          __builtin_amdgcn_alignbyte(d < 3 ? w[(d + 4) & 7] : w[7], w[d + 3], cut & 3)};
-            };
-            if (cut == 0) r = a;
-            else if (BYTES == 4) {
-                r = cut == 4 ? u32x4{a.y, a.z, a.w, b.x} : cut == 8 ? u32x4{a.z, a.w, b.x, b.y} : u32x4{a.w, b.x, b.y, b.z};
-            } else switch (cut >> 2) {
-                case 0: take(0); break;
-                case 1: take(1); break;
-                case 2: take(2); break;
-                default: take(3); break;
-            }
-            __builtin_nontemporal_store(r, (Global<u32x4>*)(at + uintptr_t(int64_t(c))));
-        } else if (c + 16 > lo && c < hi) {
-            Global<elem>* to = (Global<elem>*)(at + uintptr_t(int64_t(c)));
-            const elem* from = reinterpret_cast<const elem*>(s.v) + c / BYTES;
+            __builtin_nontemporal_store(vec(c), (Global<u32x4>*)(at + uintptr_t(int64_t(c))));
+        } else if (c + 16 > lo) {
+            Global<T>* to = (Global<T>*)(at + uintptr_t(int64_t(c)));
 #pragma unroll
-            for (int k = 0; k < 16 / BYTES; ++k)
-                if (c + k * BYTES >= lo && c + k * BYTES < hi) to[k] = from[k];
+            for (int k = 0; k < 16 / kSize; ++k)
+                if (c + k * kSize >= lo && c + k * kSize < hi) to[k] = one(c / kSize + k);
         }
     }
 }
 
+// This wave's tile in staged results.
+template <int BYTES>
+__device__ __forceinline__ const u32x4* staged_tile(const Staged<BYTES>& s) {
+    return s.v + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * int(kSetTile * BYTES / 16);
+}
+
+__device__ __forceinline__ void store_codes(const Staged<1>& staged, const void* codes, const Extent& x, const Chain& link) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(codes) + uintptr_t(x.base);
+    const u32x4* s = staged_tile(staged);
+    const int cut = int(-at & 15u);
+    store_run<uint8_t>(at, x, link, [&](int c) {
+        const u32x4 a = s[(c - cut) / 16], b = s[(c - cut) / 16 + 1];
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const auto take = [&](int d) {
+            return u32x4{__builtin_amdgcn_alignbyte(w[d + 1], w[d], cut & 3), __builtin_amdgcn_alignbyte(w[d + 2], w[d + 1], cut & 3),
+                         __builtin_amdgcn_alignbyte(w[d + 3], w[d + 2], cut & 3), __builtin_amdgcn_alignbyte(w[d + 4], w[d + 3], cut & 3)};
+        };
+        switch (cut >> 2) {
+            case 0: return take(0);
+            case 1: return take(1);
+            case 2: return take(2);
+            default: return take(3);
+        }
+    }, [&](int k) { return reinterpret_cast<const uint8_t*>(s)[k]; });
+}
+
+__device__ __forceinline__ u32x4 four_of(const u32x4& a, const u32x4& b, int cut) {   // words cut .. cut + 3 of the eight
+    switch (cut) {
+        case 0: return a;
+        case 1: return u32x4{a.y, a.z, a.w, b.x};
+        case 2: return u32x4{a.z, a.w, b.x, b.y};
+        default: return u32x4{a.w, b.x, b.y, b.z};
+    }
+}
+
+__device__ __forceinline__ void store_p(const Staged<4>& staged, const void* p, const Extent& x, const Chain& link) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p) + uintptr_t(x.base * 4);
+    const u32x4* s = staged_tile(staged);
+    const int cut = int(-at & 15u);
+    store_run<uint32_t>(at, x, link, [&](int c) { return four_of(s[(c - cut) / 16], s[(c - cut) / 16 + 1], cut / 4); },
+                        [&](int k) { return reinterpret_cast<const uint32_t*>(s)[k]; });
+}
+
+// The 16-bit copies, from the staged p: they need no stage of their own, which
+// leaves room for six blocks on a CU instead of four.
 template <int O>
+__device__ __forceinline__ void store_out(const Staged<4>& staged, const void* out, const Extent& x, const Chain& link) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(out) + uintptr_t(x.base * 2);
+    const u32x4* s = staged_tile(staged);
+    const int cut = int(-at & 7u) / 2;   // element c / 2 less its place in an aligned four
+    store_run<uint16_t>(at, x, link, [&](int c) {
+        const int q = (c / 2 - cut) / 4;
+        const u32x4 mid = s[q + 1];
+        const f32x4 a = __builtin_bit_cast(f32x4, four_of(s[q], mid, cut)), b = __builtin_bit_cast(f32x4, four_of(mid, s[q + 2], cut));
+        const float lo[4] = {a.x, a.y, a.z, a.w}, hi[4] = {b.x, b.y, b.z, b.w};
+        const u32x2 l = __builtin_bit_cast(u32x2, narrow4<O>(lo)), h = __builtin_bit_cast(u32x2, narrow4<O>(hi));
+        return u32x4{l.x, l.y, h.x, h.y};
+    }, [&](int k) { return Type<O>::narrow(reinterpret_cast<const float*>(s)[k]); });
+}
+
 struct StepStage {
     Staged<4> p;
     Staged<1> m, v;
-    Staged<O == ZERO_DTYPE_NONE ? 0 : 2> out;
 };
 struct NoStage {};
 
 template <int G, int O, int S, bool kWhole, bool kStaged, typename Stage>
 __device__ __forceinline__ void step_tile(const TensorRec& r, const Consts& c, float mult, uint32_t key, const Extent& x,
                                           int lane, Stage* stage) {
+    const uint32_t own = kStaged ? (threadIdx.x >> 6) * uint32_t(kSetTile) : 0u;   // the wave's place in the stage
     typedef typename Type<S>::elem ST;
     TileIn<G, S> t;
     load_tile<G, S, kWhole>(r, x, lane, t);
@@ -475,10 +530,9 @@ __device__ __forceinline__ void step_tile(const TensorRec& r, const Consts& c, f
                 vs_out[q / ZERO_STATE_BLOCK] = uint8_t(vs);
             }
             if constexpr (kStaged) {
-                reinterpret_cast<uint32_t*>(stage->m.v)[q / 4] = mc;
-                reinterpret_cast<uint32_t*>(stage->v.v)[q / 4] = vc;
-                stage->p.v[q / 4] = __builtin_bit_cast(u32x4, f32x4{p[0], p[1], p[2], p[3]});
-                if constexpr (O != ZERO_DTYPE_NONE) reinterpret_cast<u32x2*>(stage->out.v)[q / 4] = __builtin_bit_cast(u32x2, narrow4<O>(p));
+                reinterpret_cast<uint32_t*>(stage->m.v)[(own + q) / 4] = mc;
+                reinterpret_cast<uint32_t*>(stage->v.v)[(own + q) / 4] = vc;
+                stage->p.v[(own + q) / 4] = __builtin_bit_cast(u32x4, f32x4{p[0], p[1], p[2], p[3]});
                 continue;
             }
             if (n.none()) continue;
@@ -492,13 +546,6 @@ __device__ __forceinline__ void step_tile(const TensorRec& r, const Consts& c, f
         store4(po, q, f32x4{p[0], p[1], p[2], p[3]}, n);
         if constexpr (O != ZERO_DTYPE_NONE) store4(oo, q, narrow4<O>(p), n);
     }
-    if constexpr (kStaged) {
-        staged_written();
-        store_staged<4>(stage->p, reinterpret_cast<uintptr_t>(po), x.lo, x.hi, lane);
-        store_staged<1>(stage->m, reinterpret_cast<uintptr_t>(mo), x.lo, x.hi, lane);
-        store_staged<1>(stage->v, reinterpret_cast<uintptr_t>(vo), x.lo, x.hi, lane);
-        if constexpr (O != ZERO_DTYPE_NONE) store_staged<2>(stage->out, reinterpret_cast<uintptr_t>(oo), x.lo, x.hi, lane);
-    }
 }
 
 // The tile of this wave, the same in all its lanes; false past the last one.
@@ -509,30 +556,52 @@ __device__ __forceinline__ bool wave_tile(const SetLaunch& a, TileRec* tile) {
     return true;
 }
 
-template <int G, int O, int S, bool kStaged>
+template <int G, int O, int S, bool kStaged, typename Stage>
+__device__ __forceinline__ void step_wave(const zero_step_control* __restrict__ ctl, const TensorRec& r, const Extent& x,
+                                          Stage* stage) {
+    const Consts c = *reinterpret_cast<const Consts*>(ctl->group[r.group]);
+    const float mult = ctl->grad_mult;
+    const uint32_t key = mix32(r.key + uint32_t(ctl->t) * 0x9E3779B9u);
+    const int lane = threadIdx.x & 63;
+    if (x.whole()) step_tile<G, O, S, true, kStaged>(r, c, mult, key, x, lane, stage);
+    else step_tile<G, O, S, false, kStaged>(r, c, mult, key, x, lane, stage);
+}
+
+template <int G, int O, int S>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(const SetLaunch a, const zero_step_control* __restrict__ ctl) {
     TileRec tile;
     if (!wave_tile(a, &tile) || ctl->skip) return;
     const TensorRec r = a.rec[tile.tensor];
-    const Consts c = *reinterpret_cast<const Consts*>(ctl->group[r.group]);
-    const float mult = ctl->grad_mult;
-    const uint32_t key = mix32(r.key + uint32_t(ctl->t) * 0x9E3779B9u);
-    const uint32_t shift = S == ZERO_DTYPE_MXFP8 ? block_shift(r) : tile_shift(r.p, 4, r.spare);
-    const Extent x = extent(r, tile.tile, shift);
+    const Extent x = extent(r, tile.tile, S == ZERO_DTYPE_MXFP8 ? block_shift(r) : tile_shift(r.p, 4, r.spare));
     if (x.hi == 0) return;   // a tile counted for another array's shift
-    const int lane = threadIdx.x & 63;
-    if constexpr (kStaged) {
-        __shared__ StepStage<O> stage[kWaves];
-        if (!step_on_sectors(r)) {
-            StepStage<O>* mine = &stage[threadIdx.x >> 6];
-            if (x.whole()) step_tile<G, O, S, true, true>(r, c, mult, key, x, lane, mine);
-            else step_tile<G, O, S, false, true>(r, c, mult, key, x, lane, mine);
-            return;
-        }
-    }
     NoStage* none = nullptr;
-    if (x.whole()) step_tile<G, O, S, true, false>(r, c, mult, key, x, lane, none);
-    else step_tile<G, O, S, false, false>(r, c, mult, key, x, lane, none);
+    step_wave<G, O, S, false>(ctl, r, x, none);
+}
+
+// For sets with MXFP8 states of which some tensors' whole tiles leave sectors
+// unfinished.
+template <int G, int O>
+__global__ __launch_bounds__(kThreads) void adamw_staged_kernel(const SetLaunch a, const zero_step_control* __restrict__ ctl) {
+    __shared__ StepStage stage;
+    if (ctl->skip) return;   // the same for every wave
+    TileRec tile = {};
+    TensorRec r = {};
+    Extent x = {0, 0, 0};
+    bool staged = false;
+    if (wave_tile(a, &tile)) {
+        r = a.rec[tile.tensor];
+        x = extent(r, tile.tile, block_shift(r));
+        staged = x.hi > 0 && !step_on_sectors(r);
+        if (staged) step_wave<G, O, ZERO_DTYPE_MXFP8, true>(ctl, r, x, &stage);
+        else if (x.hi > 0) step_wave<G, O, ZERO_DTYPE_MXFP8, false>(ctl, r, x, &stage);
+    }
+    __syncthreads();
+    if (!staged) return;
+    const Chain link = chain(a, tile, r, x);
+    store_p(stage.p, r.p, x, link);
+    if constexpr (O != ZERO_DTYPE_NONE) store_out<O>(stage.p, r.out, x, link);
+    store_codes(stage.m, r.m, x, link);
+    store_codes(stage.v, r.v, x, link);
 }
 
 // ---------------------------------------------------------------------------
@@ -572,38 +641,43 @@ __device__ __forceinline__ void encode_tile(const TensorRec& to, const TensorRec
             vs_out[q / ZERO_STATE_BLOCK] = uint8_t(vs);
         }
         if (stage) {
-            reinterpret_cast<uint32_t*>(stage->m.v)[q / 4] = mc;
-            reinterpret_cast<uint32_t*>(stage->v.v)[q / 4] = vc;
+            const uint32_t own = (threadIdx.x >> 6) * uint32_t(kSetTile);
+            reinterpret_cast<uint32_t*>(stage->m.v)[(own + q) / 4] = mc;
+            reinterpret_cast<uint32_t*>(stage->v.v)[(own + q) / 4] = vc;
         } else if (!n.none()) {
             store4(cm, q, mc, n);
             store4(cv, q, vc, n);
         }
     }
-    if (!stage) return;
-    staged_written();
-    store_staged<1>(stage->m, reinterpret_cast<uintptr_t>(cm), x.lo, x.hi, lane);
-    store_staged<1>(stage->v, reinterpret_cast<uintptr_t>(cv), x.lo, x.hi, lane);
+}
+
+__device__ __forceinline__ void encode_wave(const TensorRec& to, const TensorRec& from, const Extent& x, CodeStage* stage) {
+    const int lane = threadIdx.x & 63;
+    if (x.whole()) encode_tile<true>(to, from, x, lane, stage);
+    else encode_tile<false>(to, from, x, lane, stage);
 }
 
 template <bool kStaged>
 __global__ __launch_bounds__(kThreads) void encode_kernel(const SetLaunch dst, const TensorRec* __restrict__ src) {
-    TileRec tile;
-    if (!wave_tile(dst, &tile)) return;
-    const TensorRec to = dst.rec[tile.tensor], from = src[tile.tensor];
-    const Extent x = extent(to, tile.tile, block_shift(to));
-    if (x.hi == 0) return;
-    const int lane = threadIdx.x & 63;
-    if constexpr (kStaged) {
-        __shared__ CodeStage stage[kWaves];
-        if (!codes_on_sectors(to)) {
-            CodeStage* mine = &stage[threadIdx.x >> 6];
-            if (x.whole()) encode_tile<true>(to, from, x, lane, mine);
-            else encode_tile<false>(to, from, x, lane, mine);
-            return;
-        }
+    TileRec tile = {};
+    TensorRec to = {};
+    Extent x = {0, 0, 0};
+    if (wave_tile(dst, &tile)) {
+        to = dst.rec[tile.tensor];
+        x = extent(to, tile.tile, block_shift(to));
     }
-    if (x.whole()) encode_tile<true>(to, from, x, lane, nullptr);
-    else encode_tile<false>(to, from, x, lane, nullptr);
+    if constexpr (kStaged) {
+        __shared__ CodeStage stage;
+        const bool staged = x.hi > 0 && !codes_on_sectors(to);
+        if (x.hi > 0) encode_wave(to, src[tile.tensor], x, staged ? &stage : nullptr);
+        __syncthreads();
+        if (!staged) return;
+        const Chain link = chain(dst, tile, to, x);
+        store_codes(stage.m, to.m, x, link);
+        store_codes(stage.v, to.v, x, link);
+    } else if (x.hi > 0) {
+        encode_wave(to, src[tile.tensor], x, nullptr);
+    }
 }
 
 // Decoding follows the fp32 arrays' lines, so a lane's four elements (the first
@@ -664,9 +738,9 @@ void launch(K kernel, dim3 grid, hipStream_t s, const KernelEvents& ev, Args... 
 
 template <int G, int O>
 void run_adamw(const SetLaunch& a, const zero_step_control* ctl, dim3 grid, hipStream_t s, const KernelEvents& ev) {
-    if (a.state_type == ZERO_DTYPE_FP32) launch(adamw_kernel<G, O, ZERO_DTYPE_FP32, false>, grid, s, ev, a, ctl);
-    else if (a.staged_step) launch(adamw_kernel<G, O, ZERO_DTYPE_MXFP8, true>, grid, s, ev, a, ctl);
-    else launch(adamw_kernel<G, O, ZERO_DTYPE_MXFP8, false>, grid, s, ev, a, ctl);
+    if (a.state_type == ZERO_DTYPE_FP32) launch(adamw_kernel<G, O, ZERO_DTYPE_FP32>, grid, s, ev, a, ctl);
+    else if (a.staged_step) launch(adamw_staged_kernel<G, O>, grid, s, ev, a, ctl);
+    else launch(adamw_kernel<G, O, ZERO_DTYPE_MXFP8>, grid, s, ev, a, ctl);
 }
 
 template <int G>
