@@ -190,6 +190,7 @@ def _load():
 # first makes this library bind to that copy, so one runtime serves both;
 # loaded the other way round, a process would hold two runtimes, and the
 # second one initialised can find no device.
+import numpy as np  # noqa: E402
 import torch  # noqa: E402,F401
 
 lib = _load()
@@ -551,8 +552,16 @@ class StepControl:
         n = len(groups)
         arr = (AdamHParams * max(1, n))(*groups)
         _check(lib.zero_step_begin(self._ptr, arr, n, max_norm, int(bool(check)),
-                                   None if scaler is None else _ref(scaler), _stream_ptr(stream)))
+                                   None if scaler is None else _ref(scaler),
+                                   _raw_stream(stream, self.device_index)))
         self._n_groups = n
+
+
+def _raw_stream(stream, dev: int):
+    """hipStream_t of a torch stream (None -> the device's current stream), as a
+    number: looking the current one up this way takes a fortieth of the time
+    that making a Stream object does."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _on_current_device(index: int, what: str):
@@ -561,8 +570,8 @@ def _on_current_device(index: int, what: str):
 
 
 def _dtype_of(tensors, what: str, kinds) -> int:
-    """The one dtype of a list's non-empty tensors, as a ZERO_DTYPE number."""
-    seen = {t.dtype for t in tensors if t.numel() > 0} or {t.dtype for t in tensors}
+    """The one dtype of a list of tensors, as a ZERO_DTYPE number."""
+    seen = {t.dtype for t in tensors}
     if len(seen) > 1:
         raise ValueError(f"{what}: the tensors have different dtypes")
     for d in seen:
@@ -572,8 +581,23 @@ def _dtype_of(tensors, what: str, kinds) -> int:
     return DTYPE_NONE
 
 
+def _addresses(tensors, what: str, sizes, dev: int) -> list:
+    """Device addresses of contiguous tensors of the given sizes on device `dev`.
+    Lists run to tens of thousands: the checks pass over them whole, and only a
+    failed one looks for its tensor."""
+    if len(tensors) != len(sizes):
+        raise ValueError(f"{what} has {len(tensors)} tensors, the set {len(sizes)}")
+    for bad, why in (([t.get_device() != dev for t in tensors], f"is not on cuda:{dev}, the current device"),
+                     ([not t.is_contiguous() for t in tensors], "must be contiguous"),
+                     ([t.numel() != n for t, n in zip(tensors, sizes)], "has another size than the set's tensor needs")):
+        if any(bad):
+            raise ValueError(f"{what}[{bad.index(True)}] {why}")
+    return [t.data_ptr() for t in tensors]
+
+
 _BITS16 = {torch.float16: DTYPE_FP16, torch.int16: DTYPE_FP16, torch.bfloat16: DTYPE_BF16}
 _GRAD_DTYPES = {**_BITS16, torch.float32: DTYPE_FP32}
+_SCALE_DTYPES = {torch.uint8: DTYPE_MXFP8, torch.float8_e8m0fnu: DTYPE_MXFP8}
 _STATE_DTYPES = {torch.float32: DTYPE_FP32, torch.uint8: DTYPE_MXFP8, torch.float8_e4m3fn: DTYPE_MXFP8}
 
 
@@ -590,13 +614,14 @@ class TensorSet:
       out      fp16 (or int16) or bf16 copies that a step writes
       groups   each tensor's parameter group (default 0)
       seed     of the random rounding of 8-bit variances
+      grad_dtype   of gradients that bind_grads will bring, when grads is not given
 
     Lists that an operator does not need may be left out: grad_sumsq needs
     grads, adamw_step p, grads, m and v, states_from m and v.  The tensors'
     storage must not be moved or resized while the set is in use."""
 
     def __init__(self, p=None, grads=None, m=None, v=None, m_scale=None, v_scale=None, out=None,
-                 groups=None, seed: int = 0, stream=None):
+                 groups=None, seed: int = 0, grad_dtype=None, stream=None):
         self._h = None
         lists = dict(p=p, grad=grads, m=m, v=v, m_scale=m_scale, v_scale=v_scale, out=out)
         lists = {k: list(x) for k, x in lists.items() if x is not None}
@@ -608,6 +633,10 @@ class TensorSet:
         n = len(self._numels)
         self._dev = _current_device()
         self._grad_type = _dtype_of(lists.get("grad", []), "grads", _GRAD_DTYPES)
+        if "grad" not in lists and grad_dtype is not None:
+            if grad_dtype not in _GRAD_DTYPES:
+                raise ValueError(f"grad_dtype {grad_dtype} is not supported")
+            self._grad_type = _GRAD_DTYPES[grad_dtype]
         state_type = _dtype_of(lists.get("m", []), "m", _STATE_DTYPES)
         if state_type != _dtype_of(lists.get("v", []), "v", _STATE_DTYPES):
             raise ValueError("m and v have different dtypes")
@@ -616,27 +645,21 @@ class TensorSet:
         mx = state_type == DTYPE_MXFP8
         if ("m_scale" in lists, "v_scale" in lists) != (mx, mx):
             raise ValueError("m_scale and v_scale come with states in 8 bits, and only with them")
-        width = dict(p=4, grad=4 if self._grad_type == DTYPE_FP32 else 2, m=1 if mx else 4,
-                     v=1 if mx else 4, m_scale=1, v_scale=1, out=2)
         if groups is not None and len(groups) != n:
             raise ValueError(f"groups has {len(groups)} entries, the set {n} tensors")
-        recs = (TensorC * max(1, n))()
         blocks = [-(-k // STATE_BLOCK) for k in self._numels]
+        recs = np.zeros(max(1, n), dtype=np.dtype(TensorC))
+        recs["numel"][:n] = self._numels
+        if groups is not None:
+            recs["group"][:n] = [int(g) for g in groups]
         for name, lst in lists.items():
             sizes = blocks if name in ("m_scale", "v_scale") else self._numels
-            if len(lst) != n:
-                raise ValueError(f"{name} has {len(lst)} tensors, the set {n}")
-            for i, (t, k) in enumerate(zip(lst, sizes)):
-                if t.numel() != k:
-                    raise ValueError(f"{name}[{i}] has {t.numel()} elements, expected {k}")
-                if k:
-                    setattr(recs[i], name, _dev_ptr(t, f"{name}[{i}]", width[name], self._dev))
-        for i, k in enumerate(self._numels):
-            recs[i].numel = k
-            recs[i].group = 0 if groups is None else int(groups[i])
+            if name in ("m_scale", "v_scale"):
+                _dtype_of(lst, name, _SCALE_DTYPES)
+            recs[name][:n] = _addresses(lst, name, sizes, self._dev)
         h = ctypes.c_void_p()
-        _check(lib.zero_tensor_set_create(recs, n, self._grad_type, state_type, out_type,
-                                          int(seed) & 0xFFFFFFFF, _stream_ptr(stream), _ref(h)))
+        _check(lib.zero_tensor_set_create(recs.ctypes.data, n, self._grad_type, state_type, out_type,
+                                          int(seed) & 0xFFFFFFFF, _raw_stream(stream, self._dev), _ref(h)))
         self._h = h
         self._keep = lists
         self._work_elems = lib.zero_grad_sumsq_work_bytes(h) // 8
@@ -656,18 +679,11 @@ class TensorSet:
     def bind_grads(self, grads, stream=None):
         """Replace the gradient tensors (same sizes and dtype)."""
         grads = list(grads)
-        if len(grads) != len(self._numels):
-            raise ValueError(f"grads has {len(grads)} tensors, the set {len(self._numels)}")
         kind = _dtype_of(grads, "grads", _GRAD_DTYPES)
-        if any(self._numels) and kind != self._grad_type:
+        if grads and kind != self._grad_type:
             raise ValueError("the set's gradients have another dtype")
-        w = 4 if kind == DTYPE_FP32 else 2
-        ptrs = (ctypes.c_void_p * max(1, len(grads)))()
-        for i, (t, k) in enumerate(zip(grads, self._numels)):
-            if t.numel() != k:
-                raise ValueError(f"grads[{i}] has {t.numel()} elements, expected {k}")
-            ptrs[i] = _dev_ptr(t, f"grads[{i}]", w, self._dev) if k else None
-        _check(lib.zero_tensor_set_bind_grads(self._h, ptrs, _stream_ptr(stream)))
+        ptrs = np.array(_addresses(grads, "grads", self._numels, self._dev) or [0], dtype=np.uint64)
+        _check(lib.zero_tensor_set_bind_grads(self._h, ptrs.ctypes.data, _raw_stream(stream, self._dev)))
         self._keep["grad"] = grads
 
     def grad_sumsq(self, out, accumulate: bool = False, stream=None):
@@ -686,19 +702,19 @@ class TensorSet:
                 with torch.cuda.stream(stream):
                     work = torch.empty(self._work_elems, dtype=torch.float64, device=out.device)
         _check(lib.zero_grad_sumsq(self._h, _dev_ptr(out, "out", 8), int(bool(accumulate)),
-                                   None if work is None else work.data_ptr(), _stream_ptr(stream)))
+                                   None if work is None else work.data_ptr(), _raw_stream(stream, self._dev)))
 
     def adamw_step(self, control: "StepControl", stream=None):
         """zero_adamw_step: the step that `control` began, on every tensor."""
         if control._n_groups == 0:
             raise ValueError("the step has not begun (StepControl.begin)")
         _on_current_device(control.device_index, "the control block")
-        _check(lib.zero_adamw_step(self._h, control._ptr, control._n_groups, _stream_ptr(stream)))
+        _check(lib.zero_adamw_step(self._h, control._ptr, control._n_groups, _raw_stream(stream, self._dev)))
 
     def states_from(self, source: "TensorSet", stream=None):
         """zero_states_convert: write `source`'s states into this set's, fp32
         to 8 bits or back."""
-        _check(lib.zero_states_convert(self._h, source._h, _stream_ptr(stream)))
+        _check(lib.zero_states_convert(self._h, source._h, _raw_stream(stream, self._dev)))
 
 
 def version() -> int:

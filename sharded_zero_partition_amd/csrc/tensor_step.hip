@@ -8,8 +8,6 @@
 //   p = p - (lr wd p + step (m / (sqrt(v) rbc2 + eps)))
 // in fp32, one rounding per operation in that order, so m, v and with fp32
 // states p equal a scalar reference bit for bit.
-#include <hip/hip_ext.h>
-
 #include <type_traits>
 
 #include "tensor_set.hpp"
@@ -730,17 +728,11 @@ __global__ __launch_bounds__(kThreads) void decode_kernel(const SetLaunch dst, c
 
 dim3 tile_grid(int64_t n_tiles) { return dim3(unsigned((n_tiles + kWaves - 1) / kWaves)); }
 
-template <typename K, typename... Args>
-void launch(K kernel, dim3 grid, hipStream_t s, const KernelEvents& ev, Args... args) {
-    if (ev.start) hipExtLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, s, ev.start, ev.stop, 0, args...);
-    else hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, s, args...);
-}
-
 template <int G, int O>
 void run_adamw(const SetLaunch& a, const zero_step_control* ctl, dim3 grid, hipStream_t s, const KernelEvents& ev) {
-    if (a.state_type == ZERO_DTYPE_FP32) launch(adamw_kernel<G, O, ZERO_DTYPE_FP32>, grid, s, ev, a, ctl);
-    else if (a.staged_step) launch(adamw_staged_kernel<G, O>, grid, s, ev, a, ctl);
-    else launch(adamw_kernel<G, O, ZERO_DTYPE_MXFP8>, grid, s, ev, a, ctl);
+    if (a.state_type == ZERO_DTYPE_FP32) launch(adamw_kernel<G, O, ZERO_DTYPE_FP32>, grid, kThreads, s, ev, a, ctl);
+    else if (a.staged_step) launch(adamw_staged_kernel<G, O>, grid, kThreads, s, ev, a, ctl);
+    else launch(adamw_kernel<G, O, ZERO_DTYPE_MXFP8>, grid, kThreads, s, ev, a, ctl);
 }
 
 template <int G>
@@ -771,9 +763,9 @@ hipError_t launch_adamw(const SetLaunch& a, const zero_step_control* ctl, hipStr
 
 hipError_t launch_convert(const SetLaunch& dst, const SetLaunch& src, hipStream_t stream, const KernelEvents& ev) {
     const dim3 grid = tile_grid(dst.n_tiles);
-    if (dst.state_type == ZERO_DTYPE_FP32) launch(decode_kernel, grid, stream, ev, dst, src.rec);
-    else if (dst.staged_codes) launch(encode_kernel<true>, grid, stream, ev, dst, src.rec);
-    else launch(encode_kernel<false>, grid, stream, ev, dst, src.rec);
+    if (dst.state_type == ZERO_DTYPE_FP32) launch(decode_kernel, grid, kThreads, stream, ev, dst, src.rec);
+    else if (dst.staged_codes) launch(encode_kernel<true>, grid, kThreads, stream, ev, dst, src.rec);
+    else launch(encode_kernel<false>, grid, kThreads, stream, ev, dst, src.rec);
     return hipGetLastError();
 }
 

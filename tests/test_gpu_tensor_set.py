@@ -200,11 +200,21 @@ def test_two_sets_under_one_norm():
 def test_gradients_bound_later_and_replaced():
     t = Twin(SIZES, "bf16", "none", "fp32", seed=4)
     p = [x.clone() for x in t.view["p"]]
-    late = zp.TensorSet(p=p, grads=None, m=[x.clone() for x in t.view["m"]], v=[x.clone() for x in t.view["v"]])
+    state = dict(m=[x.clone() for x in t.view["m"]], v=[x.clone() for x in t.view["v"]])
     control = zp.StepControl()
     control.begin(hparams(HP), check=False)
-    with pytest.raises(zp.ZeroError, match="STATE"):
-        late.adamw_step(control)
+    never = zp.TensorSet(p=p, **state)
+    late = zp.TensorSet(p=p, grad_dtype=torch.bfloat16, **state)
+    for s in (never, late):
+        with pytest.raises(zp.ZeroError, match="STATE"):
+            s.adamw_step(control)
+        with pytest.raises(zp.ZeroError, match="STATE"):
+            s.grad_sumsq(control.sumsq)
+    with pytest.raises((ValueError, zp.ZeroError)):
+        never.bind_grads(t.view["g"])
+    late.bind_grads([torch.ones_like(x) for x in t.view["g"]])
+    late.grad_sumsq(control.sumsq)
+    assert control.sumsq.item() == sum(SIZES)
     with pytest.raises(ValueError):
         t.set.bind_grads([x.float() for x in t.view["g"]])
     with pytest.raises(zp.ZeroError, match="INVALID_ARG"):
