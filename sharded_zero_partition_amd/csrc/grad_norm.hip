@@ -12,7 +12,7 @@ namespace zp {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int64_t kMaxBlocks = 2048;   // 8 blocks of 4 waves on each of 256 CUs
+constexpr int64_t kMaxBlocks = 1024;   // 4 blocks of 4 waves on each of 256 CUs (2048: 1 to 2% slower)
 // Up to 64 tiles are summed by one block of 16 waves in one launch.  On the
 // device the two ways meet there (replayed from a graph 2.6 us for 16 tiles,
 // 4.4 for 64, 5.7 for 96; two launches 4.0 for any of them); called from a

@@ -62,19 +62,20 @@ __host__ __device__ inline uint32_t block_shift(const TensorRec& r) {
     return (s & 32u) <= r.spare ? s & 32u : 0u;
 }
 // Whether the whole tiles of an array of `bytes`-byte elements then fill whole
-// 64-byte sectors.
-__host__ __device__ inline bool on_sectors(const void* p, int bytes, uint32_t shift) {
-    return ((reinterpret_cast<uintptr_t>(p) - uintptr_t(bytes) * shift) & 63u) == 0;
+// lines.
+constexpr int kLine = 128;
+__host__ __device__ inline bool on_lines(const void* p, int bytes, uint32_t shift) {
+    return ((reinterpret_cast<uintptr_t>(p) - uintptr_t(bytes) * shift) & uintptr_t(kLine - 1)) == 0;
 }
 // Those of a step and of a conversion.  Sets with a tensor that is off them run
 // kernels that put such tiles' results in order through LDS first.
-__host__ __device__ inline bool step_on_sectors(const TensorRec& r) {
+__host__ __device__ inline bool step_on_lines(const TensorRec& r) {
     const uint32_t s = block_shift(r);
-    return on_sectors(r.p, 4, s) && on_sectors(r.m, 1, s) && on_sectors(r.v, 1, s) && (!r.out || on_sectors(r.out, 2, s));
+    return on_lines(r.p, 4, s) && on_lines(r.m, 1, s) && on_lines(r.v, 1, s) && (!r.out || on_lines(r.out, 2, s));
 }
-__host__ __device__ inline bool codes_on_sectors(const TensorRec& r) {
+__host__ __device__ inline bool codes_on_lines(const TensorRec& r) {
     const uint32_t s = block_shift(r);
-    return on_sectors(r.m, 1, s) && on_sectors(r.v, 1, s);
+    return on_lines(r.m, 1, s) && on_lines(r.v, 1, s);
 }
 constexpr int64_t kMaxSetTiles = int64_t(1) << 25;
 static_assert(kMaxSetTiles <= kMaxGridWaves, "one wave per tile fits one launch");
@@ -97,7 +98,7 @@ struct SetLaunch {
     int32_t grad_type;
     int32_t state_type;
     int32_t out_type;
-    bool staged_step;      // MXFP8: a tensor whose step, or conversion, is off the sectors
+    bool staged_step;      // MXFP8: a tensor whose step, or conversion, is off the lines
     bool staged_codes;
 };
 

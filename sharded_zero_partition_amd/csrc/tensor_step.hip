@@ -402,7 +402,7 @@ __device__ __forceinline__ Chain chain(const SetLaunch& a, const TileRec& tile, 
 template <typename T, typename Vec, typename One>
 __device__ __forceinline__ void store_run(uintptr_t at, const Extent& x, const Chain& link, Vec vec, One one) {
     constexpr int kSize = int(sizeof(T)), kBytes = int(kSetTile) * kSize;
-    const int mis = int(at & 63u), begins = (64 - mis) & 63;   // first sector that begins in the tile
+    const int mis = int(at & uintptr_t(kLine - 1)), begins = (kLine - mis) & (kLine - 1);   // the first line that begins in the tile
     const int lo = link.before ? begins : x.lo * kSize;
     const int to_next = begins < link.next * kSize ? begins : link.next * kSize;
     const int hi = link.after && x.hi == int(kSetTile) ? kBytes + to_next : x.hi * kSize;
@@ -589,7 +589,7 @@ __global__ __launch_bounds__(kThreads) void adamw_staged_kernel(const SetLaunch 
     if (wave_tile(a, &tile)) {
         r = a.rec[tile.tensor];
         x = extent(r, tile.tile, block_shift(r));
-        staged = x.hi > 0 && !step_on_sectors(r);
+        staged = x.hi > 0 && !step_on_lines(r);
         if (staged) step_wave<G, O, ZERO_DTYPE_MXFP8, true>(ctl, r, x, &stage);
         else if (x.hi > 0) step_wave<G, O, ZERO_DTYPE_MXFP8, false>(ctl, r, x, &stage);
     }
@@ -666,7 +666,7 @@ __global__ __launch_bounds__(kThreads) void encode_kernel(const SetLaunch dst, c
     }
     if constexpr (kStaged) {
         __shared__ CodeStage stage;
-        const bool staged = x.hi > 0 && !codes_on_sectors(to);
+        const bool staged = x.hi > 0 && !codes_on_lines(to);
         if (x.hi > 0) encode_wave(to, src[tile.tensor], x, staged ? &stage : nullptr);
         __syncthreads();
         if (!staged) return;
