@@ -477,8 +477,8 @@ typedef struct zero_tensor {
  * is used, and the set must be kept until the work that uses it has finished
  * (graphs that captured it among it).
  * Errors: INVALID_ARG, ALIGNMENT, INDEX_OVERFLOW, OUT_OF_MEMORY (more than 2^25
- * tiles of 1024 elements, each tensor's last one counting as whole), STATE,
- * HIP. */
+ * tiles of 1024 elements, each tensor's first and last one counting as whole),
+ * STATE (the stream is being captured, or another device's), HIP. */
 int zero_tensor_set_create(const zero_tensor* tensors, int64_t n, int32_t grad_type,
                            int32_t state_type, int32_t out_type, uint32_t seed, void* stream,
                            zero_tensor_set** out);
@@ -488,9 +488,10 @@ int zero_tensor_set_destroy(zero_tensor_set* set); /* NULL is accepted */
 /* Replace every gradient address (host array of n pointers, as in
  * zero_tensor_set_create).  Ordered on `stream`: calls on it that were enqueued
  * before use the old addresses, later ones (replayed graphs too) the new.
- * Waits for the upload; on an error the old addresses stay.
- * Errors: INVALID_ARG, ALIGNMENT, STATE (grad_type is NONE, or another device),
- * OUT_OF_MEMORY, HIP. */
+ * Waits for the upload; on an error the old addresses stay.  No other call on
+ * the set may run at the same time, nor work that uses it on another stream.
+ * Errors: INVALID_ARG, ALIGNMENT, STATE (grad_type is NONE, another device, or
+ * the stream is being captured), OUT_OF_MEMORY, HIP. */
 int zero_tensor_set_bind_grads(zero_tensor_set* set, const void* const* grads, void* stream);
 
 /* Sum of squares of every gradient value of the set, in fp64, into the device
@@ -528,9 +529,11 @@ typedef struct zero_step_control {
 /* Begin a step.  With S = ctl->scale, and check = 1:
  *   norm = sqrt(ctl->sumsq) / S;  c = max_norm / norm when max_norm > 0 and
  *   norm > max_norm, else 1.  The step is skipped unless norm * c < 2^62 (inf
- *   and NaN skip), S is at least 2^-24 and finite, and lr_mult is finite.
+ *   and NaN skip), S is at least 2^-24 and finite, lr_mult is finite and t is
+ *   not negative.
  *   A skipped step leaves t and every tensor as they are.
- * With check = 0 sumsq is not read, norm is 0 and c is 1; max_norm must be 0.
+ * With check = 0 sumsq is not read, norm is 0 and c is 1; max_norm must be 0,
+ * and every gradient must be finite and below 2^62 S in magnitude.
  * A taken step counts t up and sets the constants of zero_adamw_step.
  *   groups    host, n_groups hyper-parameters (1..16), read during the call
  *   scaler    host, or NULL for a constant scale: a taken step counts
@@ -555,8 +558,8 @@ int zero_step_begin(zero_step_control* ctl, const zero_adam_hparams* groups, int
  * under the root.  Several sets can follow one zero_step_begin.
  *   ctl       device, as zero_step_begin left it on this stream
  *   n_groups  as given to zero_step_begin; every tensor's group is below it
- * The set's gradients must be finite unless the step was begun with check = 1
- * and a sum over all of them.  Asynchronous on `stream`.
+ * The set's gradients are part of the sum that a step begun with check = 1 went
+ * by.  Asynchronous on `stream`.
  * Errors: INVALID_ARG, ALIGNMENT, STATE (no p, gradients or states, another
  * device), HIP. */
 int zero_adamw_step(const zero_tensor_set* set, const zero_step_control* ctl, int32_t n_groups,

@@ -102,6 +102,16 @@ int check_set_device(const zero_tensor_set* set, void* stream, const char* who) 
     return check_stream_device(stream, dev, who);
 }
 
+// Uploads wait for their stream, which one that is being captured cannot.
+int check_not_capturing(void* stream, const char* who) {
+    hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+    const hipError_t e = hipStreamIsCapturing(static_cast<hipStream_t>(stream), &status);
+    if (e != hipSuccess) return fail_hip(e, "hipStreamIsCapturing");
+    if (status != hipStreamCaptureStatusNone)
+        return fail(ZERO_ERR_STATE, std::string(who) + ": not possible while the stream is being captured");
+    return ZERO_OK;
+}
+
 SetLaunch set_launch(const zero_tensor_set* s) {
     return SetLaunch{s->d_rec, s->d_tile, s->n_tiles, s->grad_type, s->state_type, s->out_type,
                      s->staged_step, s->staged_codes};
@@ -226,7 +236,8 @@ int create(const zero_tensor* tensors, int64_t n, int32_t grad_type, int32_t sta
 
     hipError_t e = hipGetDevice(&set->device);
     if (e != hipSuccess) return fail_hip(e, "hipGetDevice");
-    const int rc = check_stream_device(stream, set->device, "zero_tensor_set_create");
+    int rc = check_stream_device(stream, set->device, "zero_tensor_set_create");
+    if (rc == ZERO_OK) rc = check_not_capturing(stream, "zero_tensor_set_create");
     if (rc != ZERO_OK) return rc;
     const size_t rec_bytes = set->rec.size() * sizeof(TensorRec), tile_bytes = tiles.size() * sizeof(TileRec);
     if (rec_bytes) {
@@ -261,7 +272,8 @@ int bind_grads(zero_tensor_set* set, const void* const* grads, void* stream) {
         if (rc != ZERO_OK) return rc;
         rec[k++].grad = grads[i];
     }
-    const int rc = check_set_device(set, stream, "zero_tensor_set_bind_grads");
+    int rc = check_set_device(set, stream, "zero_tensor_set_bind_grads");
+    if (rc == ZERO_OK) rc = check_not_capturing(stream, "zero_tensor_set_bind_grads");
     if (rc != ZERO_OK) return rc;
     if (!rec.empty()) {
         hipStream_t s = static_cast<hipStream_t>(stream);
@@ -274,7 +286,7 @@ int bind_grads(zero_tensor_set* set, const void* const* grads, void* stream) {
     return ZERO_OK;
 }
 
-// Whether two calls on the set could run: what it lacks, or NULL.
+// What the set lacks of what a call needs, or NULL.
 const char* lacks(const zero_tensor_set* s, bool p, bool grads, bool states) {
     if (s->rec.empty()) return nullptr;   // nothing to do
     if (p && !s->has_p) return "the set has no p";

@@ -249,9 +249,9 @@ static_assert(sizeof(Consts) == sizeof(zero_step_control::group) / ZERO_MAX_GROU
 // counts.
 __global__ __launch_bounds__(64) void step_begin_kernel(const BeginLaunch a) {
     zero_step_control* c = a.ctl;
-    const int64_t t = c->t + 1;
+    const int64_t t = int64_t(uint64_t(c->t) + 1u);
     const float scale = c->scale, lr_mult = c->lr_mult;
-    bool ok = scale >= ZERO_MIN_LOSS_SCALE && scale <= 3.402823466e38f && fabsf(lr_mult) <= 3.402823466e38f;
+    bool ok = t > 0 && scale >= ZERO_MIN_LOSS_SCALE && scale <= 3.402823466e38f && fabsf(lr_mult) <= 3.402823466e38f;
     double norm = 0.0, clip = 1.0;
     if (a.check) {
         norm = sqrt(c->sumsq) / double(scale);
@@ -390,8 +390,8 @@ __device__ __forceinline__ Chain chain(const SetLaunch& a, const TileRec& tile, 
 
 // A wave's tile, from the block's staged results to memory; `at` is where its
 // element 0 belongs (maybe outside the tensor).  Lane l takes the aligned 16
-// bytes l of each KiB, so a sector is written whole by one instruction; where
-// the tile's neighbours are in the block too, the wave takes the sectors that
+// bytes l of each KiB, so a line is written whole by one instruction; where
+// the tile's neighbours are in the block too, the wave takes the lines that
 // begin in its tile, and only the ends of the block's run are left unfinished.
 // (Each wave to its own ends: 648 us for 200 M elements one element off the
 // lines, and 582 us sixteen off.)  A vector is cut out of two staged ones;
@@ -576,7 +576,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const SetLaunch a, cons
     step_wave<G, O, S, false>(ctl, r, x, none);
 }
 
-// For sets with MXFP8 states of which some tensors' whole tiles leave sectors
+// For sets with MXFP8 states of which some tensors' whole tiles leave lines
 // unfinished.
 template <int G, int O>
 __global__ __launch_bounds__(kThreads) void adamw_staged_kernel(const SetLaunch a, const zero_step_control* __restrict__ ctl) {

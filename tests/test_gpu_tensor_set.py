@@ -167,7 +167,8 @@ def test_device_side_values_that_skip():
     """A scale or factor on lr that the caller left unusable, and a norm whose squares would leave fp32."""
     t = Twin([100], "fp32", "none", "fp32", seed=1)
     for name, value, std in (("scale", 0.0, 1), ("scale", float("inf"), 1), ("scale", float("nan"), 1),
-                             ("lr_mult", float("inf"), 1), ("lr_mult", float("nan"), 1), (None, 0, 2.0 ** 63)):
+                             ("lr_mult", float("inf"), 1), ("lr_mult", float("nan"), 1), ("t", -1, 1), ("t", (1 << 63) - 1, 1),
+                             (None, 0, 2.0 ** 63)):
         t.new_grads([np.full(100, std, np.float32)])
         control = zp.StepControl()
         if name:
@@ -175,7 +176,7 @@ def test_device_side_values_that_skip():
         t.set.grad_sumsq(control.sumsq)
         control.begin(hparams(HP[:1]))
         t.set.adamw_step(control)
-        assert (control.skip.item(), control.t.item(), control.skipped.item()) == (1, 0, 1), name
+        assert (control.skip.item(), control.t.item(), control.skipped.item()) == (1, value if name == "t" else 0, 1), name
         t.compare(str(name))
     control = zp.StepControl()                        # clipped, the same gradients are fine
     t.set.grad_sumsq(control.sumsq)
@@ -494,6 +495,81 @@ def test_a_tensor_past_2_31_elements():
         assert np.array_equal(x[lo:].cpu().numpy(), code) and np.array_equal(sc[lo // 32:].cpu().numpy(), scale)
     middle = slice(1 << 20, lo)                    # no gradient, no state, no decay of zeros
     assert int(torch.count_nonzero(p[middle])) == 0 and int(torch.count_nonzero(m[middle])) == 0
+
+
+def test_uploads_are_refused_while_the_stream_is_captured():
+    t = Twin([100, 200], "fp16", "none", "fp32", seed=41)
+    g = torch.ones(64, device="cuda")
+    out = torch.zeros((), dtype=torch.float64, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(zp.ZeroError, match="captured"):
+            t.set.bind_grads(t.view["g"])
+        with pytest.raises(zp.ZeroError, match="captured"):
+            zp.TensorSet(grads=[g])
+        t.set.grad_sumsq(out)                                 # the capture goes on
+    for _ in range(3):
+        out.fill_(-1.0)
+        graph.replay()
+        assert abs(out.item() - t.sumsq()) <= 301 * 2.0 ** -53 * t.sumsq()
+
+
+@pytest.mark.parametrize("n_ranks,align", [(1, 1), (3, 1), (4, 32), (7, 64)])
+def test_partitioned_steps_equal_the_whole_model_s(n_ranks, align):
+    """A ZeRO-2 step from end to end, rank after rank on one device: gradients reduced to their owner, each rank's set
+    made of the tensor pieces of its shard, one norm over all ranks, the update, and the fp16 copies in the rank's slot of
+    the gather buffer.  Each element's result hangs on no other's, so it equals the step of one set of whole tensors."""
+    rng = np.random.default_rng(n_ranks)
+    numels = [1600, 7, 50257, 1, 3000, 129, 64, 9000]
+    lists = [[torch.from_numpy((rng.standard_normal(n) * 0.5).astype(np.float16)).cuda() for n in numels] for _ in range(2)]
+    lay = zp.partition_layout(numels, n_ranks, stage=2, align=align, bucket=8192)
+    lay.bind_contributions([[x.view(torch.int16) for x in lst] for lst in lists])
+    S, psi = lay.info.shard_elems, sum(numels)
+    p0 = torch.zeros(n_ranks * S, device="cuda")
+    p0[:psi] = torch.randn(psi, device="cuda") * 0.02
+    gather = torch.zeros(n_ranks * S, dtype=torch.float16, device="cuda")
+    flat = {k: torch.zeros(n_ranks * S, device="cuda") for k in "mv"}
+    flat.update(p=p0.clone(), g=torch.zeros(n_ranks * S, dtype=torch.float16, device="cuda"), out=gather)
+    groups = [0 if n > 200 else 1 for n in numels]
+    sets = []
+    for r in range(n_ranks):
+        shard = {k: x[r * S:(r + 1) * S] for k, x in flat.items()}
+        pieces = lay.rank_segments(r)
+        cut = {}
+        for sg in pieces:                                     # a tensor's pieces of one shard, joined over bucket fills
+            lo, hi = cut.get(sg.tensor, (sg.shard_off, sg.shard_off))
+            assert hi == sg.shard_off
+            cut[sg.tensor] = (lo, hi + sg.len)
+        view = {k: [x[lo:hi] for lo, hi in cut.values()] for k, x in shard.items()}
+        sets.append(zp.TensorSet(p=view["p"], grads=view["g"], m=view["m"], v=view["v"], out=view["out"],
+                                 groups=[groups[i] for i in cut]))
+    whole = {k: [torch.zeros(n, device="cuda") for n in numels] for k in "mv"}
+    off = np.concatenate([[0], np.cumsum(numels)])
+    wp = [p0[a:b].clone() for a, b in zip(off, off[1:])]
+    total = [(a.float() + b.float()).half() for a, b in zip(*lists)]
+    ref = zp.TensorSet(p=wp, grads=total, m=whole["m"], v=whole["v"], groups=groups)
+    control, other = zp.StepControl(), zp.StepControl()
+    for _ in range(3):
+        for r, s in enumerate(sets):
+            for fill in range(lay.info.n_fills):
+                lay.reduce_to_owner(fill, r, flat["g"][r * S:(r + 1) * S].view(torch.int16))
+            s.grad_sumsq(control.sumsq, accumulate=r > 0)     # the all-reduce over ranks
+        ref.grad_sumsq(other.sumsq)
+        a, b = control.sumsq.item(), other.sumsq.item()
+        assert abs(a - b) <= (psi + n_ranks) * 2.0 ** -53 * b
+        other.sumsq.copy_(control.sumsq)
+        for c in (control, other):
+            c.begin(hparams(HP), max_norm=1.0)
+        for s in sets:
+            s.adamw_step(control)
+        ref.adamw_step(other)
+    torch.cuda.synchronize()
+    assert control.grad_mult.item() < 1.0
+    for k, want in (("p", wp), ("m", whole["m"]), ("v", whole["v"])):
+        assert torch.equal(flat[k][:psi].view(torch.int32), torch.cat(want).view(torch.int32)), k
+    assert torch.equal(gather[:psi], torch.cat(wp).half())
+    for x in (gather, flat["p"], flat["m"], flat["v"]):       # padding stays as it was
+        assert int(torch.count_nonzero(x[psi:])) == 0
 
 
 @pytest.mark.parametrize("state", ["fp32", "mx"])
