@@ -121,6 +121,10 @@ def parse_args():
     ap.add_argument("--shard-workloads", action="store_true",
                     help="instead of the default measurement: the fused step on each shard workload "
                          "(tiny, GPT-2 1.5B, 13B, 1T), K timed steps each, one JSON line")
+    ap.add_argument("--tensor-set", action="store_true",
+                    help="instead of the default measurement: the tensor-set kernels (gradient norm, "
+                         "AdamW with fp32 and MXFP8 states, state conversion) on the tensor pieces of "
+                         "the 13B rank-63 shard, K timed calls each, one JSON line")
     ap.add_argument("--no-pack", action="store_true", help="skip the bucket-pack measurement")
     ap.add_argument("--no-cpu-baseline", action="store_true", help="skip the CPU oracle timing")
     ap.add_argument("--calibration-copy", action="store_true",
@@ -233,6 +237,68 @@ def shard_workloads_main(args):
     print(json.dumps(out), flush=True)
 
 
+def tensor_set_main(args):
+    """One JSON line: the tensor-set kernels on the tensor pieces of the 13B
+    rank-63 shard, laid back to back in flat buffers (bf16 gradients and
+    copies, two parameter groups), each call's kernels timed by their events."""
+    import numpy as np
+    import torch
+
+    import sharded_zero_partition_amd as zp
+    from sharded_zero_partition_amd import workloads as W
+
+    torch.cuda.set_device(0)
+    w = W.zero3_13b()
+    lay = zp.partition_layout(w.numels, w.n_ranks, w.stage)
+    pieces = [sg.len for sg in lay.rank_segments(w.rank)]
+    n, blocks = sum(pieces), [-(-k // 32) for k in pieces]
+    p = W.master_init(w, device="cuda")
+    grad = (torch.randn(n, device="cuda") * (1e-3 * w.scale)).to(torch.bfloat16)
+    out = torch.empty(n, dtype=torch.bfloat16, device="cuda")
+    m, v = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    m8, v8 = (torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ms, vs = (torch.zeros(sum(blocks), dtype=torch.uint8, device="cuda") for _ in range(2))
+    common = dict(p=torch.split(p, pieces), grads=torch.split(grad, pieces), out=torch.split(out, pieces),
+                  groups=[0 if k > 65536 else 1 for k in pieces])
+    wide = zp.TensorSet(m=torch.split(m, pieces), v=torch.split(v, pieces), **common)
+    mx = zp.TensorSet(m=torch.split(m8, pieces), v=torch.split(v8, pieces), m_scale=torch.split(ms, blocks),
+                      v_scale=torch.split(vs, blocks), **common)
+    control = zp.StepControl(scale=w.scale)
+    hp = [zp.AdamHParams(w.lr, w.beta1, w.beta2, w.eps, wd) for wd in (0.1, 0.0)]
+    rows = []
+
+    def timed(name, call, bytes_):
+        for _ in range(args.warmup):
+            call()
+        torch.cuda.synchronize()
+        zp.set_kernel_timing(True)
+        for _ in range(args.steps):
+            call()
+        torch.cuda.synchronize()
+        t = zp.kernel_times()
+        zp.set_kernel_timing(False)
+        gbs = bytes_ / (float(np.mean(t)) * 1e-3) / 1e9
+        rows.append({"kernel": name, "ms": round(float(np.mean(t)), 4), "ms_median": round(float(np.median(t)), 4),
+                     "roofline": {"bound": "hbm", "achieved": round(gbs, 1), "peak": HBM_PEAK_GBS, "unit": "GB/s",
+                                  "frac": round(gbs / HBM_PEAK_GBS, 4)}})
+        return rows[-1]
+
+    timed("gradient norm", lambda: wide.grad_sumsq(control.sumsq), 2 * n)
+    control.begin(hp, max_norm=1.0)
+    main_row = timed("AdamW, fp32 states", lambda: wide.adamw_step(control), 28 * n)
+    timed("states to 8 bits", lambda: mx.states_from(wide), 10 * n + 2 * sum(blocks))
+    timed("AdamW, MXFP8 states", lambda: mx.adamw_step(control), 16 * n + 4 * sum(blocks))
+    timed("states to 32 bits", lambda: wide.states_from(mx), 10 * n + 2 * sum(blocks))
+    assert control.skip.item() == 0 and bool(torch.isfinite(p).all())
+    result = {"metric": METRIC, "value": round(n / (main_row["ms"] * 1e-3), 1), "unit": "elements/s",
+              "n_gpus": 1, "steps": args.steps, "warmup": args.warmup, "ms_per_step": main_row["ms"],
+              "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "f32", "data": "synthetic",
+              "config": {"workload": f"tensor set: the {len(pieces)} tensor pieces of the 13B rank-63 shard",
+                         "elements": n, "gradients": "bf16", "copies": "bf16"},
+              "roofline": main_row["roofline"], "kernels": rows}
+    print(json.dumps(result), flush=True)
+
+
 def main():
     args = parse_args()
     world = int(os.environ.get("WORLD_SIZE", "1"))
@@ -246,6 +312,9 @@ def main():
 
     if args.shard_workloads:
         shard_workloads_main(args)
+        return
+    if args.tensor_set:
+        tensor_set_main(args)
         return
 
     import numpy as np

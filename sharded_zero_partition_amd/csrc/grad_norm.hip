@@ -7,6 +7,7 @@
 // way and the blocks' sums added in a fixed order, so equal inputs give equal
 // bits; there are no atomics.
 #include "tensor_set.hpp"
+#include "timed_launch.hpp"
 
 namespace zp {
 namespace {

@@ -11,6 +11,7 @@
 #include <type_traits>
 
 #include "tensor_set.hpp"
+#include "timed_launch.hpp"
 
 #pragma clang fp contract(off)
 
@@ -301,10 +302,11 @@ __global__ __launch_bounds__(64) void step_begin_kernel(const BeginLaunch a) {
 
 // kFast (states in 8 bits): root and quotient by the hardware's approximations,
 // within 1 ulp each, which puts the update within 14 half-ulps instead of 12 of
-// the formula's; the states it came from are off by 2^-4.  IEEE's sequences cost
-// 21 of 78 instructions an element, and this kernel is bound by them as much as
-// by memory.  The approximate root takes no subnormals: v counts as 2^-126 at
-// least there.
+// the formula's; the states it came from are off by 2^-4.  With IEEE's sequences
+// (21 instructions an element more) the kernel had 78 VALU instructions an
+// element and the ALUs were busy for 400 of its 550 us at 200 M elements, which
+// nothing could be added to.  The approximate root takes no subnormals: v counts
+// as 2^-126 at least there.
 template <bool kFast>
 __device__ __forceinline__ void adamw_element(const Consts& c, float g, float& p, float& m, float& v) {
     m = c.beta1 * m + c.omb1 * g;
