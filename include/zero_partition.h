@@ -529,8 +529,8 @@ typedef struct zero_step_control {
 /* Begin a step.  With S = ctl->scale, and check = 1:
  *   norm = sqrt(ctl->sumsq) / S;  c = max_norm / norm when max_norm > 0 and
  *   norm > max_norm, else 1.  The step is skipped unless norm * c < 2^62 (inf
- *   and NaN skip), S is at least 2^-24 and finite, lr_mult is finite and t is
- *   not negative.
+ *   and NaN skip), c / S is at least 2^-126, S is at least 2^-24 and finite,
+ *   lr_mult is finite and t is not negative.
  *   A skipped step leaves t and every tensor as they are.
  * With check = 0 sumsq is not read, norm is 0 and c is 1; max_norm must be 0,
  * and every gradient must be finite and below 2^62 S in magnitude.
@@ -539,8 +539,9 @@ typedef struct zero_step_control {
  *   scaler    host, or NULL for a constant scale: a taken step counts
  *             good_steps, and at growth_interval (> 0) scale is multiplied by
  *             growth (kept when not finite) and good_steps reset; a skipped one
- *             sets scale = max(scale * backoff, min_scale), good_steps = 0.  Its
- *             own scale and good_steps are ignored.
+ *             sets scale = max(scale * backoff, min_scale) (min_scale when that
+ *             is not finite), good_steps = 0.  Its own scale and good_steps are
+ *             ignored.
  * Asynchronous on `stream`.  Errors: INVALID_ARG (as for zero_shard_step),
  * ALIGNMENT, STATE, HIP. */
 int zero_step_begin(zero_step_control* ctl, const zero_adam_hparams* groups, int32_t n_groups,

@@ -127,6 +127,7 @@ class Control:
             norm = float(np.sqrt(np.float64(self.sumsq))) / scale
             clip = max_norm / norm if max_norm > 0 and norm > max_norm else 1.0
             ok = bool(ok and norm * clip < 2.0 ** 62)
+        ok = bool(ok and clip / scale >= 2.0 ** -126)
         self.norm = float(np.float32(norm))
         self.grad_mult = float(np.float32(clip / scale)) if ok else 0.0
         self.skip = 0 if ok else 1
@@ -145,7 +146,8 @@ class Control:
             self.skipped += 1
         if scaler is not None:
             if not ok:
-                self.scale = max(float(np.float32(scale * scaler.backoff)), float(np.float32(scaler.min_scale)))
+                s = float(np.float32(scale * scaler.backoff))
+                self.scale = s if np.isfinite(s) and s >= scaler.min_scale else float(np.float32(scaler.min_scale))
                 self.good_steps = 0
             else:
                 self.good_steps += 1

@@ -6,6 +6,12 @@
 // keeps 5 digits more than fp32 has.  The tiles are dealt to blocks in a fixed
 // way and the blocks' sums added in a fixed order, so equal inputs give equal
 // bits; there are no atomics.
+//
+// Bound by reading 2 or 4 bytes an element: 71 us for 200 M bf16 values (5.7
+// TB/s, a plain copy reaches 6.05).  Non-temporal loads take 68, but the step
+// that follows then finds nothing of the gradients in the last-level cache: norm
+// and step together, 355 us with these loads and 385 with those (120 M elements,
+// states in 8 bits).
 #include "tensor_set.hpp"
 #include "timed_launch.hpp"
 

@@ -178,6 +178,12 @@ def test_device_side_values_that_skip():
         t.set.adamw_step(control)
         assert (control.skip.item(), control.t.item(), control.skipped.item()) == (1, value if name == "t" else 0, 1), name
         t.compare(str(name))
+    for scale in (float("nan"), float("inf"), 2.0 ** 127, 1.0):       # a dynamic scale comes back from any of them
+        control = zp.StepControl()
+        control.scale.fill_(scale)
+        control.sumsq.fill_(float("inf") if scale == 1.0 else 1.0)
+        control.begin(hparams(HP[:1]), scaler=zp.LossScaler.make(min_scale=0.75))
+        assert (control.skip.item(), control.scale.item()) == (1, 2.0 ** 126 if scale == 2.0 ** 127 else 0.75), scale
     control = zp.StepControl()                        # clipped, the same gradients are fine
     t.set.grad_sumsq(control.sumsq)
     control.begin(hparams(HP[:1]), max_norm=1.0)
