@@ -551,7 +551,7 @@ class StepControl:
         _on_current_device(self.device_index, "the control block")
         n = len(groups)
         arr = (AdamHParams * max(1, n))(*groups)
-        _check(lib.zero_step_begin(self._ptr, arr, n, max_norm, int(bool(check)),
+        _check(lib.zero_step_begin(self._ptr, arr, n, max_norm, bool(check),
                                    None if scaler is None else _ref(scaler),
                                    _raw_stream(stream, self.device_index)))
         self._n_groups = n
@@ -690,8 +690,8 @@ class TensorSet:
         """zero_grad_sumsq: the sum of squares of every gradient value into
         `out` (one float64 on the device, StepControl.sumsq); accumulate=True
         adds it to what is there."""
-        if out.dtype != torch.float64 or out.numel() != 1:
-            raise ValueError("out must be one float64")
+        if out.dtype != torch.float64 or out.numel() != 1 or out.get_device() != self._dev:
+            raise ValueError(f"out must be one float64 on cuda:{self._dev}")
         work = None
         if self._work_elems:
             # workspace of this call alone, from the pool of its stream: calls
@@ -701,7 +701,7 @@ class TensorSet:
             else:
                 with torch.cuda.stream(stream):
                     work = torch.empty(self._work_elems, dtype=torch.float64, device=out.device)
-        _check(lib.zero_grad_sumsq(self._h, _dev_ptr(out, "out", 8), int(bool(accumulate)),
+        _check(lib.zero_grad_sumsq(self._h, out.data_ptr(), bool(accumulate),
                                    None if work is None else work.data_ptr(), _raw_stream(stream, self._dev)))
 
     def adamw_step(self, control: "StepControl", stream=None):
