@@ -503,6 +503,31 @@ def test_a_tensor_past_2_31_elements():
     assert int(torch.count_nonzero(p[middle])) == 0 and int(torch.count_nonzero(m[middle])) == 0
 
 
+def test_a_variance_in_8_bits_follows_a_falling_gradient():
+    """v moves by 1% a step here, under half of an e4m3 step: rounded to nearest it would stay where it is.  Rounded at
+    random its mean over N elements follows the formula.  A rounding's error has mean zero and, the neighbours being v / 8
+    apart at most, variance (v / 16)^2 at most; an error of step s is multiplied by beta2^(T - s) until the end, and
+    v_s beta2^(T - s) <= v_T, so T steps add up to at most T (v_T / 16)^2, independent over the elements: 6 deviations of the
+    mean are 6 sqrt(T) / 16 / sqrt(N) of v_T."""
+    N, T1, T2 = 16384, 50, 250
+    h = T.HParams(lr=0.0, beta1=0.0, beta2=0.99)
+    g = torch.ones(N, device="cuda")
+    z = {k: [torch.zeros(N, dtype=torch.uint8, device="cuda")] for k in "mv"}
+    z.update({k: [torch.zeros(N // 32, dtype=torch.uint8, device="cuda")] for k in ("m_scale", "v_scale")})
+    s = zp.TensorSet(p=[torch.zeros(N, device="cuda")], grads=[g], seed=9, **z)
+    control, v = zp.StepControl(), 0.0
+    for step in range(T1 + T2):
+        if step == T1:
+            g.fill_(0.05)
+        control.begin(hparams([h]), check=False)
+        s.adamw_step(control)
+        v = h.beta2 * v + (1 - h.beta2) * (1.0 if step < T1 else float(np.float32(0.05)) ** 2)
+    wide = [torch.empty(N, device="cuda") for _ in range(2)]
+    zp.TensorSet(m=wide[:1], v=wide[1:]).states_from(s)
+    mean = wide[1].double().mean().item()
+    assert v < 0.05 and abs(mean - v) <= 6 * np.sqrt(T1 + T2) / 16 / np.sqrt(N) * v, (mean, v)
+
+
 def test_uploads_are_refused_while_the_stream_is_captured():
     t = Twin([100, 200], "fp16", "none", "fp32", seed=41)
     g = torch.ones(64, device="cuda")
