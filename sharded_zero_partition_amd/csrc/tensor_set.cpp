@@ -213,8 +213,8 @@ int create(const zero_tensor* tensors, int64_t n, int32_t grad_type, int32_t sta
         r.group = t.group;
         r.spare = uint32_t(tiles * kSetTile - t.numel);
         if (mx) {
-            set->staged_step |= !step_on_lines(r);
-            set->staged_codes |= !codes_on_lines(r);
+            set->staged_step |= !step_direct(r);
+            set->staged_codes |= !codes_direct(r);
         }
         set->rec.push_back(r);
     }

@@ -105,6 +105,11 @@ struct Extent {
     int64_t base;
     int lo, hi;
     __device__ __forceinline__ bool whole() const { return hi - lo == int(kSetTile); }
+    // whether the tile ends before its group h (all lanes alike)
+    template <bool kWhole>
+    __device__ __forceinline__ bool without(int h) const {
+        return !kWhole && h * 256 >= hi;
+    }
     template <bool kWhole>
     __device__ __forceinline__ Part part(uint32_t q) const {
         if (kWhole) return {0, 4};
@@ -350,7 +355,7 @@ __device__ __forceinline__ void load_tile(const TensorRec& r, const Extent& x, i
         t.m[h] = {};
         t.v[h] = {};
         t.ms[h] = t.vs[h] = 1;
-        if (n.none()) continue;
+        if (x.without<kWhole>(h) || n.none()) continue;
         t.g[h] = load4(g, q, n);
         t.p[h] = load4(p, q, n);
         t.m[h] = load4(m, q, n);
@@ -509,6 +514,7 @@ __device__ __forceinline__ void step_tile(const TensorRec& r, const Consts& c, f
     const uint32_t pair0 = uint32_t(x.base >> 1) + key;
 #pragma unroll
     for (int h = 0; h < kGroups; ++h) {
+        if (x.without<kWhole>(h)) break;
         const uint32_t q = h * 256 + 4 * lane;
         const Part n = x.part<kWhole>(q);
         float p[4] = {t.p[h].x, t.p[h].y, t.p[h].z, t.p[h].w};
@@ -586,8 +592,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const SetLaunch a, cons
     step_wave<G, O, S, false>(ctl, r, x, none);
 }
 
-// For sets with MXFP8 states of which some tensors' whole tiles leave lines
-// unfinished.
+// For sets with MXFP8 states of which some tensors' tiles are not stored
+// straight.
 template <int G, int O>
 __global__ __launch_bounds__(kThreads) void adamw_staged_kernel(const SetLaunch a, const zero_step_control* __restrict__ ctl) {
     __shared__ StepStage stage;
@@ -599,7 +605,7 @@ __global__ __launch_bounds__(kThreads) void adamw_staged_kernel(const SetLaunch 
     if (wave_tile(a, &tile)) {
         r = a.rec[tile.tensor];
         x = extent(r, tile.tile, block_shift(r));
-        staged = x.hi > 0 && !step_on_lines(r);
+        staged = x.hi > 0 && !step_direct(r);
         if (staged) step_wave<G, O, ZERO_DTYPE_MXFP8, true>(ctl, r, x, &stage);
         else if (x.hi > 0) step_wave<G, O, ZERO_DTYPE_MXFP8, false>(ctl, r, x, &stage);
     }
@@ -633,12 +639,13 @@ __device__ __forceinline__ void encode_tile(const TensorRec& to, const TensorRec
         const uint32_t q = h * 256 + 4 * lane;
         const Part n = x.part<kWhole>(q);
         m4[h] = v4[h] = {};
-        if (n.none()) continue;
+        if (x.without<kWhole>(h) || n.none()) continue;
         m4[h] = load4(wm, q, n);
         v4[h] = load4(wv, q, n);
     }
 #pragma unroll
     for (int h = 0; h < kGroups; ++h) {
+        if (x.without<kWhole>(h)) break;
         const uint32_t q = h * 256 + 4 * lane;
         const Part n = x.part<kWhole>(q);
         const float m[4] = {m4[h].x, m4[h].y, m4[h].z, m4[h].w}, v[4] = {v4[h].x, v4[h].y, v4[h].z, v4[h].w};
@@ -676,7 +683,7 @@ __global__ __launch_bounds__(kThreads) void encode_kernel(const SetLaunch dst, c
     }
     if constexpr (kStaged) {
         __shared__ CodeStage stage;
-        const bool staged = x.hi > 0 && !codes_on_lines(to);
+        const bool staged = x.hi > 0 && !codes_direct(to);
         if (x.hi > 0) encode_wave(to, src[tile.tensor], x, staged ? &stage : nullptr);
         __syncthreads();
         if (!staged) return;
@@ -711,7 +718,7 @@ __device__ __forceinline__ void decode_tile(const TensorRec& to, const TensorRec
         const uint32_t q = h * 256 + 4 * lane;
         const Part n = x.part<kWhole>(q);
         mc[h] = vc[h] = 0;
-        if (n.none()) continue;
+        if (x.without<kWhole>(h) || n.none()) continue;
         mc[h] = load4(cm, q, n);
         vc[h] = load4(cv, q, n);
     }
@@ -719,7 +726,7 @@ __device__ __forceinline__ void decode_tile(const TensorRec& to, const TensorRec
     for (int h = 0; h < kGroups; ++h) {
         const uint32_t q = h * 256 + 4 * lane;
         const Part n = x.part<kWhole>(q);
-        if (n.none()) continue;
+        if (x.without<kWhole>(h) || n.none()) continue;
         store4(wm, q, decode_across(mc[h], from.m_scale, x.base + q, n), n);
         store4(wv, q, decode_across(vc[h], from.v_scale, x.base + q, n), n);
     }
