@@ -61,28 +61,48 @@ struct Part {
     __device__ __forceinline__ bool has(int k) const { return k >= a && k < b; }
 };
 
-// Elements q + [a, b) of a tile, p being where its element 0 is (the same in all
+// Elements q .. q + 3 of a tile, p being where its element 0 is (the same in all
 // lanes; outside the array for a tile that starts before it) and q a lane's
-// first; zeros in the others' places.  Non-temporal where whole: no line is used
-// again (plain loads and stores on whole lines: 1039 against 926 us for the step
-// with fp32 states of 200 M elements, 602 against 547 us in 8 bits).  Plain where
-// not: single elements written non-temporally leave one by one (966 against
-// 648 us for a misaligned step in 8 bits).
+// first.  Non-temporal: no line is used again (plain loads and stores on whole
+// lines: 1039 against 926 us for the step with fp32 states of 200 M elements,
+// 602 against 547 us in 8 bits).
 template <typename T>
-__device__ __forceinline__ typename Four<T>::vec load4(const T* p, uint32_t q, Part n) {
+__device__ __forceinline__ typename Four<T>::vec load4(const T* p, uint32_t q) {
     typedef const typename Four<T>::at at;
-    Global<const T>* x = (Global<const T>*)((Global<const char>*)p + q * uint32_t(sizeof(T)));
-    if (n.all()) return __builtin_nontemporal_load((Global<at>*)x);
+    return __builtin_nontemporal_load((Global<at>*)((Global<const char>*)p + q * uint32_t(sizeof(T))));
+}
+
+// The same in a group of lanes of which some have elements that do not exist:
+// each lane loads four single elements, `at[k]` being element k or, where that
+// is none, one that is there.  No branch and nothing to wait for until all
+// arrays' loads are under way (with a branch for each element that exists, 12
+// tensors of up to 1600 elements took 9 us, see edge_pack).
+template <typename T>
+struct Edge {   // each in a register of its own
+    std::conditional_t<sizeof(T) == 4, T, uint32_t> e[4];
+};
+template <typename T>
+__device__ __forceinline__ Edge<T> edge_load(const T* p, const int at[4]) {
+    Edge<T> r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r.e[k] = ((Global<const T>*)p)[at[k]];
+    return r;
+}
+// ... and zeros in the places of those that are not.
+template <typename T>
+__device__ __forceinline__ typename Four<T>::vec edge_pack(const Edge<T>& x, Part n) {
     typename Four<T>::vec r = {};
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        if (n.has(k)) {
-            if constexpr (sizeof(T) == 1) r |= uint32_t(x[k]) << (8 * k);
-            else r[k] = x[k];
-        }
+    for (int k = 0; k < 4; ++k) {
+        const auto e = n.has(k) ? x.e[k] : 0;
+        if constexpr (sizeof(T) == 1) r |= uint32_t(e) << (8 * k);
+        else r[k] = T(e);
+    }
     return r;
 }
 
+// Plain where not all four exist: single elements written non-temporally leave
+// one by one (966 against 648 us for a misaligned step in 8 bits).
 template <typename T>
 __device__ __forceinline__ void store4(T* p, uint32_t q, typename Four<T>::vec v, Part n) {
     typedef typename Four<T>::at at;
@@ -105,10 +125,23 @@ struct Extent {
     int64_t base;
     int lo, hi;
     __device__ __forceinline__ bool whole() const { return hi - lo == int(kSetTile); }
-    // whether the tile ends before its group h (all lanes alike)
+    // whether the tile ends before its group h, and whether it has all of it
+    // (the same in all lanes)
     template <bool kWhole>
     __device__ __forceinline__ bool without(int h) const {
         return !kWhole && h * 256 >= hi;
+    }
+    template <bool kWhole>
+    __device__ __forceinline__ bool with(int h) const {
+        return kWhole || (lo <= h * 256 && h * 256 + 256 <= hi);
+    }
+    // elements q .. q + 3, or the nearest of the tile's
+    __device__ __forceinline__ void nearest(uint32_t q, int at[4]) const {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int e = int(q) + k;
+            at[k] = e < lo ? lo : e < hi ? e : hi - 1;
+        }
     }
     template <bool kWhole>
     __device__ __forceinline__ Part part(uint32_t q) const {
@@ -344,25 +377,39 @@ __device__ __forceinline__ void load_tile(const TensorRec& r, const Extent& x, i
     const GT* g = tile_at<GT>(r.grad, x.base);
     const float* p = tile_at<float>(r.p, x.base);
     const ST *m = tile_at<ST>(r.m, x.base), *v = tile_at<ST>(r.v, x.base);
-    const uint8_t* ms = tile_at<uint8_t>(r.m_scale, x.base / ZERO_STATE_BLOCK);
-    const uint8_t* vs = tile_at<uint8_t>(r.v_scale, x.base / ZERO_STATE_BLOCK);
+    Global<const uint8_t>* ms = (Global<const uint8_t>*)tile_at<uint8_t>(r.m_scale, x.base / ZERO_STATE_BLOCK);
+    Global<const uint8_t>* vs = (Global<const uint8_t>*)tile_at<uint8_t>(r.v_scale, x.base / ZERO_STATE_BLOCK);
 #pragma unroll
     for (int h = 0; h < kGroups; ++h) {
         const uint32_t q = h * 256 + 4 * lane;
-        const Part n = x.part<kWhole>(q);
+        int b = int(q);   // an element of the lane's block (a tile starts with a block)
         t.g[h] = {};
         t.p[h] = {};
         t.m[h] = {};
         t.v[h] = {};
         t.ms[h] = t.vs[h] = 1;
-        if (x.without<kWhole>(h) || n.none()) continue;
-        t.g[h] = load4(g, q, n);
-        t.p[h] = load4(p, q, n);
-        t.m[h] = load4(m, q, n);
-        t.v[h] = load4(v, q, n);
-        if constexpr (S == ZERO_DTYPE_MXFP8) {   // a tile starts with a block
-            t.ms[h] = ((Global<const uint8_t>*)ms)[q / ZERO_STATE_BLOCK];
-            t.vs[h] = ((Global<const uint8_t>*)vs)[q / ZERO_STATE_BLOCK];
+        if (x.without<kWhole>(h)) break;
+        if (x.with<kWhole>(h)) {
+            t.g[h] = load4(g, q);
+            t.p[h] = load4(p, q);
+            t.m[h] = load4(m, q);
+            t.v[h] = load4(v, q);
+        } else {
+            int at[4];
+            x.nearest(q, at);
+            b = at[0];
+            const Part n = x.part<kWhole>(q);
+            const Edge<GT> ge = edge_load(g, at);
+            const Edge<float> pe = edge_load(p, at);
+            const Edge<ST> me = edge_load(m, at), ve = edge_load(v, at);
+            t.g[h] = edge_pack(ge, n);
+            t.p[h] = edge_pack(pe, n);
+            t.m[h] = edge_pack(me, n);
+            t.v[h] = edge_pack(ve, n);
+        }
+        if constexpr (S == ZERO_DTYPE_MXFP8) {
+            t.ms[h] = ms[b / ZERO_STATE_BLOCK];
+            t.vs[h] = vs[b / ZERO_STATE_BLOCK];
         }
     }
 }
@@ -597,21 +644,24 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const SetLaunch a, cons
 template <int G, int O>
 __global__ __launch_bounds__(kThreads) void adamw_staged_kernel(const SetLaunch a, const zero_step_control* __restrict__ ctl) {
     __shared__ StepStage stage;
-    if (ctl->skip) return;   // the same for every wave
+    const int skip = ctl->skip;
     TileRec tile = {};
     TensorRec r = {};
     Extent x = {0, 0, 0};
+    Chain link = {};
     bool staged = false;
-    if (wave_tile(a, &tile)) {
+    const bool any = wave_tile(a, &tile);
+    if (skip) return;   // the same for every wave
+    if (any) {
         r = a.rec[tile.tensor];
         x = extent(r, tile.tile, block_shift(r));
+        link = chain(a, tile, r, x);
         staged = x.hi > 0 && !step_direct(r);
         if (staged) step_wave<G, O, ZERO_DTYPE_MXFP8, true>(ctl, r, x, &stage);
         else if (x.hi > 0) step_wave<G, O, ZERO_DTYPE_MXFP8, false>(ctl, r, x, &stage);
     }
     __syncthreads();
     if (!staged) return;
-    const Chain link = chain(a, tile, r, x);
     store_p(stage.p, r.p, x, link);
     if constexpr (O != ZERO_DTYPE_NONE) store_out<O>(stage.p, r.out, x, link);
     store_codes(stage.m, r.m, x, link);
@@ -626,23 +676,37 @@ struct CodeStage {
     Staged<1> m, v;
 };
 
+// A tile of both states.
+template <typename T, bool kWhole>
+__device__ __forceinline__ void load_states(const TensorRec& from, const Extent& x, int lane, typename Four<T>::vec m[kGroups],
+                                            typename Four<T>::vec v[kGroups]) {
+    const T *pm = tile_at<T>(from.m, x.base), *pv = tile_at<T>(from.v, x.base);
+#pragma unroll
+    for (int h = 0; h < kGroups; ++h) {
+        const uint32_t q = h * 256 + 4 * lane;
+        m[h] = v[h] = {};
+        if (x.without<kWhole>(h)) break;
+        if (x.with<kWhole>(h)) {
+            m[h] = load4(pm, q);
+            v[h] = load4(pv, q);
+        } else {
+            int at[4];
+            x.nearest(q, at);
+            const Edge<T> me = edge_load(pm, at), ve = edge_load(pv, at);
+            m[h] = edge_pack(me, x.part<kWhole>(q));
+            v[h] = edge_pack(ve, x.part<kWhole>(q));
+        }
+    }
+}
+
 template <bool kWhole>
 __device__ __forceinline__ void encode_tile(const TensorRec& to, const TensorRec& from, const Extent& x, int lane,
                                             CodeStage* stage) {
-    const float *wm = tile_at<float>(from.m, x.base), *wv = tile_at<float>(from.v, x.base);
     uint8_t *cm = tile_at<uint8_t>(to.m, x.base), *cv = tile_at<uint8_t>(to.v, x.base);
     Global<uint8_t>* ms_out = (Global<uint8_t>*)tile_at<uint8_t>(to.m_scale, x.base / ZERO_STATE_BLOCK);
     Global<uint8_t>* vs_out = (Global<uint8_t>*)tile_at<uint8_t>(to.v_scale, x.base / ZERO_STATE_BLOCK);
     f32x4 m4[kGroups], v4[kGroups];
-#pragma unroll
-    for (int h = 0; h < kGroups; ++h) {
-        const uint32_t q = h * 256 + 4 * lane;
-        const Part n = x.part<kWhole>(q);
-        m4[h] = v4[h] = {};
-        if (x.without<kWhole>(h) || n.none()) continue;
-        m4[h] = load4(wm, q, n);
-        v4[h] = load4(wv, q, n);
-    }
+    load_states<float, kWhole>(from, x, lane, m4, v4);
 #pragma unroll
     for (int h = 0; h < kGroups; ++h) {
         if (x.without<kWhole>(h)) break;
@@ -711,17 +775,8 @@ __device__ __forceinline__ f32x4 decode_across(uint32_t code, const uint8_t* sca
 template <bool kWhole>
 __device__ __forceinline__ void decode_tile(const TensorRec& to, const TensorRec& from, const Extent& x, int lane) {
     float *wm = tile_at<float>(to.m, x.base), *wv = tile_at<float>(to.v, x.base);
-    const uint8_t *cm = tile_at<uint8_t>(from.m, x.base), *cv = tile_at<uint8_t>(from.v, x.base);
     uint32_t mc[kGroups], vc[kGroups];
-#pragma unroll
-    for (int h = 0; h < kGroups; ++h) {
-        const uint32_t q = h * 256 + 4 * lane;
-        const Part n = x.part<kWhole>(q);
-        mc[h] = vc[h] = 0;
-        if (x.without<kWhole>(h) || n.none()) continue;
-        mc[h] = load4(cm, q, n);
-        vc[h] = load4(cv, q, n);
-    }
+    load_states<uint8_t, kWhole>(from, x, lane, mc, vc);
 #pragma unroll
     for (int h = 0; h < kGroups; ++h) {
         const uint32_t q = h * 256 + 4 * lane;
