@@ -99,11 +99,37 @@ __global__ __launch_bounds__(kBlock) void sumsq_kernel(const SetLaunch a, double
                     s += y * y;
                 }
         } else {
+            // groups of 64 vectors where the tensor has all of one, else of
+            // single values, the nearest in the places of those it has not
+            constexpr int kGroup = 64 * T::kWide;
             const int lo = base < 0 ? int(-base) : 0, hi = left < kSetTile ? int(left) : int(kSetTile);
-#pragma unroll 4
-            for (int e = lo + lane; e < hi; e += 64) {
-                const double y = T::wide(g[e]);
-                s += y * y;
+#pragma unroll
+            for (int h = 0; h < T::kLoads; ++h) {
+                const int first = h * kGroup;
+                if (first >= hi) break;
+                typename T::elem x[T::kWide] = {};
+                bool has[T::kWide] = {};
+                if (lo <= first && first + kGroup <= hi) {
+                    const typename T::at v = *(Global<const typename T::at>*)(g + first + lane * T::kWide);
+#pragma unroll
+                    for (int k = 0; k < T::kWide; ++k) x[k] = v[k], has[k] = true;
+                } else if (hi <= first + 64) {
+                    const int e = first + lane;
+                    has[0] = e >= lo && e < hi;
+                    x[0] = g[e < lo ? lo : e < hi ? e : hi - 1];
+                } else {
+#pragma unroll
+                    for (int k = 0; k < T::kWide; ++k) {
+                        const int e = first + k * 64 + lane;
+                        has[k] = e >= lo && e < hi;
+                        x[k] = g[e < lo ? lo : e < hi ? e : hi - 1];
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < T::kWide; ++k) {
+                    const double y = has[k] ? T::wide(x[k]) : 0.0;
+                    s += y * y;
+                }
             }
         }
     }
