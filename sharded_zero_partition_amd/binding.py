@@ -549,6 +549,8 @@ class StepControl:
         `groups` (AdamHParams, one for each parameter group).  `scaler` gives
         the rule of a dynamic loss scale; its own scale is not used."""
         _on_current_device(self.device_index, "the control block")
+        if max_norm and not ctypes.c_float(max_norm).value:
+            raise ValueError("max_norm is below fp32's range (0 means no clipping)")
         n = len(groups)
         arr = (AdamHParams * max(1, n))(*groups)
         _check(lib.zero_step_begin(self._ptr, arr, n, max_norm, bool(check),

@@ -75,6 +75,70 @@ def test_sumsq_of_special_values(value, want, where):
     assert out.item() == want or (np.isnan(want) and np.isnan(out.item()))
 
 
+def test_a_norm_past_fp32_range_is_clipped_or_skipped():
+    g = torch.full((5000,), 1e30, device="cuda")
+    p, m, v = torch.zeros(5000, device="cuda"), torch.zeros(5000, device="cuda"), torch.zeros(5000, device="cuda")
+    s, control = zp.TensorSet(p=[p], grads=[g], m=[m], v=[v]), zp.StepControl()
+    s.grad_sumsq(control.sumsq)
+    want = 5000 * float(np.float32(1e30)) ** 2
+    assert abs(control.sumsq.item() - want) <= 5001 * 2.0 ** -53 * want
+    control.begin(hparams(HP[:1]))
+    s.adamw_step(control)
+    assert control.skip.item() == 1 and int(torch.count_nonzero(p)) == 0
+    control.begin(hparams(HP[:1]), max_norm=1.0)
+    s.adamw_step(control)
+    # every value clipped to 1 / sqrt(5000), times 1 - beta1 with beta1 as fp32 has it (a difference that is exact):
+    # the factor's rounding and the two products', 3 * 2^-24
+    want = (1 - HP[0].beta1) / np.sqrt(5000)
+    assert control.skip.item() == 0 and (m.double() / want - 1).abs().max().item() <= 3.01 * 2.0 ** -24
+    assert torch.isfinite(p).all() and torch.isfinite(v).all()
+    for bad in (1e-50, -1.0, float("nan"), float("inf")):
+        with pytest.raises((ValueError, zp.ZeroError)):
+            control.begin(hparams(HP[:1]), max_norm=bad)
+
+
+def test_bit_patterns_in_int16_are_fp16():
+    """fp16 data as int16 patterns, as the rest of the library passes it."""
+    a, b = Twin(SIZES, "fp16", "fp16", "fp32", seed=50), Twin(SIZES, "fp16", "fp16", "fp32", seed=50)
+    s = zp.TensorSet(p=b.view["p"], grads=[x.view(torch.int16) for x in b.view["g"]], m=b.view["m"], v=b.view["v"],
+                     out=[x.view(torch.int16) for x in b.view["out"]], groups=b.groups)
+    for t, tensors in ((a, a.set), (b, s)):
+        control, c = zp.StepControl(scale=1024.0), T.Control(scale=1024.0)
+        tensors.grad_sumsq(control.sumsq)
+        control.begin(hparams(HP), max_norm=0.05)
+        tensors.adamw_step(control)
+        c.sumsq = t.sumsq()
+        c.begin(HP, 0.05)
+        follow(c, same_control(control, c, rel=2.0 ** -23))
+        t.expect(c)
+        t.compare()
+
+
+def test_replays_read_gradients_that_are_bound_later():
+    t = Twin(SIZES, "bf16", "none", "mx", seed=51)
+    control, c = zp.StepControl(scale=1024.0), T.Control(scale=1024.0)
+    take_step([t], control, c)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        t.set.grad_sumsq(control.sumsq)
+        control.begin(hparams(HP))
+        t.set.adamw_step(control)
+    del t.kinds["g"]                                          # the old buffer is not compared
+    for shift in (0, 1, 3):                                   # other places, at other alignments
+        t.new_grads()
+        moved = [torch.cat([x.new_zeros(shift), x])[shift:] for x in t.view["g"]]
+        for x in t.view["g"]:
+            x.fill_(float("nan"))
+        t.set.bind_grads(moved)
+        c.sumsq = t.sumsq()
+        graph.replay()
+        torch.cuda.synchronize()
+        c.begin(HP)
+        follow(c, same_control(control, c, rel=2.0 ** -23))
+        t.expect(c)
+        t.compare(f"moved by {shift}")
+
+
 @pytest.mark.parametrize("state", ["fp32", "mx"])
 @pytest.mark.parametrize("out", ["fp16", "bf16", "none"])
 @pytest.mark.parametrize("grad", ["fp16", "bf16", "fp32"])
