@@ -620,7 +620,8 @@ class TensorSet:
 
     Lists that an operator does not need may be left out: grad_sumsq needs
     grads, adamw_step p, grads, m and v, states_from m and v.  The tensors'
-    storage must not be moved or resized while the set is in use."""
+    storage must not be moved or resized while the set is in use, and a graph
+    that captured one of its calls needs the set as long as it is replayed."""
 
     def __init__(self, p=None, grads=None, m=None, v=None, m_scale=None, v_scale=None, out=None,
                  groups=None, seed: int = 0, grad_dtype=None, stream=None):
@@ -666,11 +667,21 @@ class TensorSet:
         self._keep = lists
         self._work_elems = lib.zero_grad_sumsq_work_bytes(h) // 8
 
+    _late = []   # handles whose sets went while a stream was being captured
+
     def close(self):
-        """Free the set's tables.  Work that uses them must have finished."""
+        """Free the set's tables.  Work that uses them must have finished.
+        Memory cannot be freed while a stream is being captured: a set that is
+        closed, or collected, meanwhile is freed when the next one is."""
         if self._h:
-            lib.zero_tensor_set_destroy(self._h)
+            TensorSet._late.append(self._h)
             self._h = None
+        if not torch.cuda.is_current_stream_capturing():
+            try:
+                while True:
+                    lib.zero_tensor_set_destroy(TensorSet._late.pop())
+            except IndexError:      # none left (another thread may have freed the last)
+                pass
 
     def __del__(self):
         try:

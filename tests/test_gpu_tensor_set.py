@@ -427,6 +427,23 @@ def test_captured_steps_replay_like_eager_ones(state):
             take_step([t], control, c, max_norm=0.05, scaler=rule, what="eager between")
 
 
+def test_a_set_that_goes_during_a_capture():
+    t = Twin([5000, 70], "fp16", "none", "fp32", seed=52)
+    other = zp.TensorSet(grads=[torch.ones(100, device="cuda")])
+    out = torch.zeros((), dtype=torch.float64, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        t.set.grad_sumsq(out)
+        del other                                             # collected here
+        t.set.grad_sumsq(out, accumulate=True)
+    assert len(zp.TensorSet._late) == 1
+    for _ in range(3):
+        graph.replay()
+        assert abs(out.item() - 2 * t.sumsq()) <= 6000 * 2.0 ** -53 * 2 * t.sumsq()
+    zp.TensorSet(grads=[torch.ones(3, device="cuda")]).close()
+    assert not zp.TensorSet._late
+
+
 def test_two_graphs_of_one_set_on_two_streams():
     """Sums of one set captured twice and replayed at the same time do not share a workspace."""
     g = torch.randn(3_000_000, device="cuda")
