@@ -375,7 +375,7 @@ def test_scale_byte_ends():
     code |= torch.randint(0, 2, code.shape, dtype=torch.uint8) * 0x80
     dev = [x.cuda() for x in (code, code & 0x7F, s, s.clone())]
     wide = [torch.zeros(code.numel(), device="cuda") for _ in range(2)]
-    f, e = zp.TensorSet(m=wide[:1], v=wide[1:]), zp.TensorSet(m=dev[:1], v=dev[1:2], m_scale=dev[2:3], v_scale=dev[3:])
+    f, e = zp.TensorSet(m=wide[:1], v=wide[1:]), zp.TensorSet(m=dev[:1], v=dev[1:2], m_scale=[dev[2].view(torch.float8_e8m0fnu)], v_scale=dev[3:])
     f.states_from(e)
     with np.errstate(over="ignore"):
         want = T.decode(code.numpy(), s.numpy())
@@ -534,6 +534,51 @@ def test_equal_runs_give_equal_bits_and_another_seed_does_not():
     a, b, c = run(1), run(1), run(2)
     assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
     assert not np.array_equal(a[1], c[1])
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_sets(seed):
+    """Seeded sets of any sizes, starts, types, groups and hyper-parameters, three steps each with clip, skip and
+    schedule drawn, then the states converted to the other type and back."""
+    rng = np.random.default_rng([7, seed])
+    pick = lambda *x: x[int(rng.integers(len(x)))]            # noqa: E731
+    sizes = [int(2 ** rng.uniform(0, pick(5, 9, 12, 16))) + int(rng.integers(0, 2)) * int(rng.integers(-1, 2)) for _ in range(int(rng.integers(1, 30)))]
+    grad, out, state = pick("fp16", "bf16", "fp32"), pick("fp16", "bf16", "none"), pick("fp32", "mx")
+    gaps = pick(None, [int(x) for x in rng.integers(0, 130, len(sizes))], [int(x) * 32 for x in rng.integers(0, 5, len(sizes))])
+    print(f"[random] seed {seed}: {grad} {out} {state} {len(sizes)} tensors, gaps {gaps is not None}", flush=True)
+    groups = [T.HParams(float(10 ** rng.uniform(-5, -2)), float(rng.uniform(0, 0.99)), float(rng.uniform(0.5, 0.9999)),
+                        float(10 ** rng.uniform(-10, -4)), pick(0.0, 0.1)) for _ in range(int(rng.integers(1, 17)))]
+    t = Twin(sizes, grad, out, state, seed=1000 + seed, gaps=gaps, groups=[int(rng.integers(len(groups))) for _ in sizes])
+    t0 = int(pick(0, 1, 10 ** int(rng.integers(1, 7))))
+    control, c = zp.StepControl(scale=1024.0, t=t0), T.Control(t=t0, scale=1024.0)
+    rule = zp.LossScaler.make(growth_interval=2)
+    for step in range(3):
+        t.new_grads()
+        if rng.random() < 0.2 and sum(sizes):
+            i = int(rng.choice([k for k, n in enumerate(sizes) if n]))
+            at = int(rng.integers(sizes[i]))
+            t.view["g"][i][at] = float("inf")
+            t.host["g"][i][at] = np.inf
+        c.lr_mult = float(np.float32(rng.uniform(0, 2)))
+        control.lr_mult.fill_(c.lr_mult)
+        check = rng.random() < 0.8 or np.isinf(t.sumsq())
+        take_step([t], control, c, groups=groups, max_norm=float(np.float32(pick(0.0, 0.01, 1.0))) if check else 0.0, check=check,
+                  scaler=pick(None, rule), what=f"step {step}")
+    if state == "mx":
+        wide = [[torch.empty(n + 1, device="cuda")[1:] for n in sizes] for _ in range(2)]
+        f = zp.TensorSet(m=wide[0], v=wide[1])
+        f.states_from(t.set)
+        for i in range(len(sizes)):
+            for k, s, w in (("m", "ms", wide[0]), ("v", "vs", wide[1])):
+                assert np.array_equal(bits(w[i]), T.decode(t.host[k][i], t.host[s][i]).view(np.int32)), (i, k)
+    else:
+        mx = Twin(sizes, grad, "none", "mx", seed=2000 + seed, gaps=gaps)
+        mx.set.states_from(t.set)
+        for i in range(len(sizes)):
+            for k, s in (("m", "ms"), ("v", "vs")):
+                mx.host[k][i], mx.host[s][i] = T.encode(t.host[k][i], k == "v")
+        mx.compare("to 8 bits")
+        t.compare("from 32 bits")
 
 
 def test_empty_sets_and_many_tiny_tensors():
