@@ -454,14 +454,31 @@ typedef struct zero_tensor {
  * keeps its values.  All codes zero is the zero state whatever the scales; s = 255
  * is not a scale.
  *
- * m is rounded to nearest, ties to even.  The variance is a slow average:
- * rounding it to nearest would freeze it, since a step moves it by less than
- * half a unit.  So a step rounds v to one of its two neighbours at random, up
- * with the probability (to 2^-16) that keeps the mean, and only ever to zero
- * when it is zero (a lost v would divide a surviving m by eps).  The random
- * bits are a function of the set's seed, the tensor's index, the step count
- * and the element, so a run can be repeated bit for bit.  The update of p uses
- * the new m and v before they are rounded. */
+ * A state that a step moves by less than half a unit of its code would be
+ * frozen by rounding to nearest.  The variance is such a slow average, so a
+ * step rounds v to one of its two neighbours at random, up with the probability
+ * (to 2^-16) that keeps the mean, and only ever to zero when it is zero (a lost
+ * v would divide a surviving m by eps).  m is rounded
+ *   - to nearest, ties to even, where the group's beta1 is at most
+ *     ZERO_NEAREST_BETA1.  An m without gradient then falls by a code a step
+ *     until it is below 1/14000 of its block's largest, but one that moves
+ *     towards a steady gradient stops short of it: at g = constant where
+ *     (1 - beta1) |g - m| is half a unit, for beta1 = 0.9 at 0.62 to 0.8 of g
+ *     (noise of the gradient's own size takes the mean of m on to g);
+ *   - at random, as v is but also to zero, above it: 1.125 beta1 would be
+ *     rounded back to 1.125, so an m without gradient would stay while v decays
+ *     and the update m / sqrt(v) grow without end;
+ *   - at random for every beta1 after zero_tensor_set_m_rounding(set, RANDOM),
+ *     which keeps the mean of m there too.
+ * The random bits are a function of the set's seed, the tensor's index, the
+ * step count and the element (m's others than v's), so a run can be repeated
+ * bit for bit.  The update of p uses the new m and v before they are rounded. */
+#define ZERO_NEAREST_BETA1 0.9444f /* below 17/18 = 1.0625 / 1.125 */
+
+enum {
+    ZERO_M_ROUNDING_AUTO = 0,  /* by the group's beta1, as above */
+    ZERO_M_ROUNDING_RANDOM = 1
+};
 
 /* Build a set of n tensors.
  *   grad_type   FP16, BF16 or FP32; NONE for a set that only converts states
@@ -484,6 +501,11 @@ int zero_tensor_set_create(const zero_tensor* tensors, int64_t n, int32_t grad_t
                            zero_tensor_set** out);
 
 int zero_tensor_set_destroy(zero_tensor_set* set); /* NULL is accepted */
+
+/* How steps of a set with MXFP8 states round m (ZERO_M_ROUNDING_AUTO at first).
+ * Holds for calls of zero_adamw_step from then on; a captured one keeps what it
+ * was captured with.  Errors: INVALID_ARG, STATE (other states). */
+int zero_tensor_set_m_rounding(zero_tensor_set* set, int32_t mode);
 
 /* Replace every gradient address (host array of n pointers, as in
  * zero_tensor_set_create).  Ordered on `stream`: calls on it that were enqueued

@@ -44,9 +44,16 @@ def mix32(x):
     return x ^ (x >> np.uint64(16))
 
 
-def chances(n, seed, tensor, t, start=0):
-    """16 random bits for each of elements start .. start + n of a tensor at step t."""
+# m in 8 bits is rounded to nearest up to this beta1 (as fp32 has it), at random above: 1.125 beta1 has to come below
+# 1.0625, or an m without gradient stays where it is.
+NEAREST_BETA1 = float(np.float32(0.9444))
+
+
+def chances(n, seed, tensor, t, start=0, of_m=False):
+    """16 random bits for each of elements start .. start + n of a tensor at step t, of v or of m."""
     key = mix32(mix32(mix32(seed) + np.uint64(tensor)) + np.uint64((t * 0x9E3779B9) & 0xFFFFFFFF))
+    if of_m:
+        key = mix32(key ^ np.uint64(0xFFFFFFFF))
     e = np.arange(start, start + n, dtype=np.uint64)
     h = mix32((e >> np.uint64(1)) + key)
     return np.where(e & np.uint64(1), h >> np.uint64(16), h & np.uint64(0xFFFF)).astype(np.uint32)
@@ -76,13 +83,21 @@ def encode(x, positive, chance=None):
         y = np.maximum(y, np.where(x > 0, np.float32(2.0 ** -9), np.float32(0)))
     if chance is None:
         return e4m3_nearest(y), s.astype(np.uint8)
-    # the next number below and the share of the step to the one above, in which 20 bits are added and cut off; below
-    # 2^-6 the steps are 2^-9
+    # the next number below in magnitude and the share of the step to the one above, in which 20 bits are added and cut
+    # off; below 2^-6 the steps are 2^-9
     up = (chance.astype(np.int64) << 4) | 8
-    _, e = np.frexp(np.maximum(y, np.float32(2.0 ** -6)))
+    a = np.abs(y)
+    _, e = np.frexp(np.maximum(a, np.float32(2.0 ** -6)))
     step = np.ldexp(1.0, e - 4)
-    code = e4m3_nearest(np.floor(y.astype(np.float64) / step + up / 2.0 ** 20) * step)
+    code = e4m3_nearest(np.copysign(np.floor(a.astype(np.float64) / step + up / 2.0 ** 20) * step, y))
     return code, s.astype(np.uint8)
+
+
+def encode_m(m, beta1, seed, tensor, t, always_random=False):
+    """(codes, scale bytes) of the m that a step with beta1 leaves."""
+    if always_random or beta1 > NEAREST_BETA1:
+        return encode(m, False, chances(m.size, seed, tensor, t, of_m=True))
+    return encode(m, False)
 
 
 def decode(code, s):

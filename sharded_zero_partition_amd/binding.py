@@ -15,7 +15,7 @@ Names follow the C ABI in include/zero_partition.h:
   Layout.reduce_to_owner(...)          (zero_reduce_to_owner)
   shard_step(...), PreparedStep(...)   (zero_shard_step; zero_shard_step_noalloc with noalloc=True)
   Layout.owner_step(...)               (zero_owner_step)
-  TensorSet(...)                       (zero_tensor_set_create)
+  TensorSet(...)                       (zero_tensor_set_create, zero_tensor_set_m_rounding)
   TensorSet.bind_grads(...)            (zero_tensor_set_bind_grads)
   TensorSet.grad_sumsq(...)            (zero_grad_sumsq)
   StepControl(...), StepControl.begin(...)   (zero_step_control, zero_step_begin)
@@ -152,6 +152,7 @@ SIGNATURES = {
     "zero_owner_step": (ctypes.c_int, [_P, _I32, _P, _P, _P, _P, _P, _P]),
     "zero_tensor_set_create": (ctypes.c_int, [_P, _I64, _I32, _I32, _I32, ctypes.c_uint32, _P, _P]),
     "zero_tensor_set_destroy": (ctypes.c_int, [_P]),
+    "zero_tensor_set_m_rounding": (ctypes.c_int, [_P, _I32]),
     "zero_tensor_set_bind_grads": (ctypes.c_int, [_P, _P, _P]),
     "zero_grad_sumsq_work_bytes": (ctypes.c_int64, [_P]),
     "zero_grad_sumsq": (ctypes.c_int, [_P, _P, _I32, _P, _P]),
@@ -615,7 +616,11 @@ class TensorSet:
                float8_e8m0fnu).  All zeros is the state to start from.
       out      fp16 (or int16) or bf16 copies that a step writes
       groups   each tensor's parameter group (default 0)
-      seed     of the random rounding of 8-bit variances
+      seed     of the random rounding of 8-bit states
+      m_rounding   of an 8-bit m: "auto" (to nearest up to beta1 = 0.9444, at
+               random above, where to nearest it would not decay) or "random"
+               (keeps the mean of m at any beta1: to nearest, under a steady
+               gradient, m stops at 0.62 to 0.8 of it for beta1 = 0.9)
       grad_dtype   of gradients that bind_grads will bring, when grads is not given
 
     Lists that an operator does not need may be left out: grad_sumsq needs
@@ -624,8 +629,10 @@ class TensorSet:
     that captured one of its calls needs the set as long as it is replayed."""
 
     def __init__(self, p=None, grads=None, m=None, v=None, m_scale=None, v_scale=None, out=None,
-                 groups=None, seed: int = 0, grad_dtype=None, stream=None):
+                 groups=None, seed: int = 0, grad_dtype=None, stream=None, m_rounding: str = "auto"):
         self._h = None
+        if m_rounding not in ("auto", "random"):
+            raise ValueError("m_rounding must be 'auto' or 'random'")
         lists = dict(p=p, grad=grads, m=m, v=v, m_scale=m_scale, v_scale=v_scale, out=out)
         lists = {k: list(x) for k, x in lists.items() if x is not None}
         if not lists:
@@ -646,6 +653,8 @@ class TensorSet:
         out_type = _dtype_of(lists.get("out", []), "out", _BITS16)
         _dtype_of(lists.get("p", []), "p", {torch.float32: DTYPE_FP32})
         mx = state_type == DTYPE_MXFP8
+        if m_rounding != "auto" and not mx:
+            raise ValueError("m_rounding is of states in 8 bits")
         if ("m_scale" in lists, "v_scale" in lists) != (mx, mx):
             raise ValueError("m_scale and v_scale come with states in 8 bits, and only with them")
         if groups is not None and len(groups) != n:
@@ -664,6 +673,8 @@ class TensorSet:
         _check(lib.zero_tensor_set_create(recs.ctypes.data, n, self._grad_type, state_type, out_type,
                                           int(seed) & 0xFFFFFFFF, _raw_stream(stream, self._dev), _ref(h)))
         self._h = h
+        if m_rounding == "random":
+            _check(lib.zero_tensor_set_m_rounding(h, 1))
         self._keep = lists
         self._work_elems = lib.zero_grad_sumsq_work_bytes(h) // 8
 

@@ -25,6 +25,7 @@ struct zero_tensor_set {
     bool has_grads = false;
     bool staged_step = false;
     bool staged_codes = false;
+    bool random_m = false;
     int32_t max_group = 0;
     int64_t n_tiles = 0;
     std::vector<int64_t> numel;              // as given, empty tensors too
@@ -114,7 +115,7 @@ int check_not_capturing(void* stream, const char* who) {
 
 SetLaunch set_launch(const zero_tensor_set* s) {
     return SetLaunch{s->d_rec, s->d_tile, s->n_tiles, s->grad_type, s->state_type, s->out_type,
-                     s->staged_step, s->staged_codes};
+                     s->staged_step, s->staged_codes, s->random_m};
 }
 
 // Events for a timed call; none while its stream is being captured (a graph's
@@ -314,6 +315,16 @@ extern "C" int zero_tensor_set_destroy(zero_tensor_set* set) {
     zp::clear_error();
     if (set && set->d_rec) (void)hipFree(set->d_rec);
     delete set;
+    return ZERO_OK;
+}
+
+extern "C" int zero_tensor_set_m_rounding(zero_tensor_set* set, int32_t mode) {
+    zp::clear_error();
+    if (!set) return fail(ZERO_ERR_INVALID_ARG, "zero_tensor_set_m_rounding: set is NULL");
+    if (mode != ZERO_M_ROUNDING_AUTO && mode != ZERO_M_ROUNDING_RANDOM)
+        return fail(ZERO_ERR_INVALID_ARG, "the rounding of m must be AUTO or RANDOM");
+    if (set->state_type != ZERO_DTYPE_MXFP8) return fail(ZERO_ERR_STATE, "the set's states are not MXFP8");
+    set->random_m = mode == ZERO_M_ROUNDING_RANDOM;
     return ZERO_OK;
 }
 

@@ -95,6 +95,7 @@ struct SetLaunch {
     int32_t out_type;
     bool staged_step;      // MXFP8: a tensor is not step_direct, or not codes_direct
     bool staged_codes;
+    bool random_m;         // MXFP8: m rounded at random whatever beta1
 };
 
 // Blocks of the sum-of-squares pass, each of which leaves one double in `work`

@@ -243,20 +243,30 @@ __device__ __forceinline__ uint32_t encode4(const float y[4]) {
 // those that fall below fp32's normal range.
 __device__ __forceinline__ float into_block(int s) { return number(uint32_t(254 - s) << 23); }
 
-__device__ __forceinline__ uint32_t encode_m(const float m[4], int* s) {
+// ... and to one of its two neighbours in magnitude at random: r0 holds 16 random
+// bits for each of the first two elements, r1 for the others.  The conversion
+// adds the upper 20 bits of its operand below the bits that an e4m3 has room for
+// and cuts off there, so it rounds up as often as they say, below its least
+// number too; the 16 are followed by 1000, the middle of what they leave open.
+__device__ __forceinline__ uint32_t encode4_random(const float y[4], uint32_t r0, uint32_t r1) {
+    int c = __builtin_amdgcn_cvt_sr_fp8_f32(y[0], (r0 << 16) | 0x8000u, 0, 0);
+    c = __builtin_amdgcn_cvt_sr_fp8_f32(y[1], (r0 & 0xFFFF0000u) | 0x8000u, c, 1);
+    c = __builtin_amdgcn_cvt_sr_fp8_f32(y[2], (r1 << 16) | 0x8000u, c, 2);
+    return uint32_t(__builtin_amdgcn_cvt_sr_fp8_f32(y[3], (r1 & 0xFFFF0000u) | 0x8000u, c, 3));
+}
+
+// m, to nearest or at random (an m below the least number may become zero, so
+// its mean is kept everywhere).
+template <bool kRandom>
+__device__ __forceinline__ uint32_t encode_m(const float m[4], uint32_t r0, uint32_t r1, int* s) {
     constexpr uint32_t kMag = 0x7FFFFFFFu;
     *s = scale_of(block_max(max4(bits(m[0]) & kMag, bits(m[1]) & kMag, bits(m[2]) & kMag, bits(m[3]) & kMag)));
     const float f = into_block(*s);
     const float y[4] = {m[0] * f, m[1] * f, m[2] * f, m[3] * f};
-    return encode4(y);
+    return kRandom ? encode4_random(y, r0, r1) : encode4(y);
 }
 
-// v (>= 0), to nearest, or to a neighbour at random; a value above zero gets at
-// least code 1.  At random: r0 holds 16 random bits for each of the first two
-// elements, r1 for the others.  The conversion adds the upper 20 bits of its
-// operand below the bits that an e4m3 has room for and cuts off there, so it
-// rounds up as often as they say; the 16 are followed by 1000, the middle of
-// what they leave open.
+// v (>= 0), to nearest or at random; a value above zero gets at least code 1.
 template <bool kRandom>
 __device__ __forceinline__ uint32_t encode_v(const float v[4], uint32_t r0, uint32_t r1, int* s) {
     *s = scale_of(block_max(max4(bits(v[0]), bits(v[1]), bits(v[2]), bits(v[3]))));
@@ -267,11 +277,7 @@ __device__ __forceinline__ uint32_t encode_v(const float v[4], uint32_t r0, uint
         const float x = v[k] * f, least = v[k] > 0.0f ? 0x1p-9f : 0.0f;
         y[k] = x > least ? x : least;
     }
-    if (!kRandom) return encode4(y);
-    int c = __builtin_amdgcn_cvt_sr_fp8_f32(y[0], (r0 << 16) | 0x8000u, 0, 0);
-    c = __builtin_amdgcn_cvt_sr_fp8_f32(y[1], (r0 & 0xFFFF0000u) | 0x8000u, c, 1);
-    c = __builtin_amdgcn_cvt_sr_fp8_f32(y[2], (r1 << 16) | 0x8000u, c, 2);
-    return uint32_t(__builtin_amdgcn_cvt_sr_fp8_f32(y[3], (r1 & 0xFFFF0000u) | 0x8000u, c, 3));
+    return kRandom ? encode4_random(y, r0, r1) : encode4(y);
 }
 
 // ---------------------------------------------------------------------------
@@ -546,7 +552,7 @@ struct StepStage {
 };
 struct NoStage {};
 
-template <int G, int O, int S, bool kWhole, bool kStaged, typename Stage>
+template <int G, int O, int S, bool kWhole, bool kStaged, bool kRandomM, typename Stage>
 __device__ __forceinline__ void step_tile(const TensorRec& r, const Consts& c, float mult, uint32_t key, const Extent& x,
                                           int lane, Stage* stage) {
     const uint32_t own = kStaged ? (threadIdx.x >> 6) * uint32_t(kSetTile) : 0u;   // the wave's place in the stage
@@ -558,7 +564,8 @@ __device__ __forceinline__ void step_tile(const TensorRec& r, const Consts& c, f
     uint16_t* oo = tile_at<uint16_t>(r.out, x.base);
     Global<uint8_t>* ms_out = (Global<uint8_t>*)tile_at<uint8_t>(r.m_scale, x.base / ZERO_STATE_BLOCK);
     Global<uint8_t>* vs_out = (Global<uint8_t>*)tile_at<uint8_t>(r.v_scale, x.base / ZERO_STATE_BLOCK);
-    const uint32_t pair0 = uint32_t(x.base >> 1) + key;
+    // random bits of two elements: of v, and of m by a key of its own
+    const uint32_t pair0 = uint32_t(x.base >> 1) + key, m_pair0 = uint32_t(x.base >> 1) + mix32(~key);
 #pragma unroll
     for (int h = 0; h < kGroups; ++h) {
         if (x.without<kWhole>(h)) break;
@@ -584,8 +591,9 @@ __device__ __forceinline__ void step_tile(const TensorRec& r, const Consts& c, f
                 for (int k = 0; k < 4; ++k)
                     if (!n.has(k)) m[k] = v[k] = 0.0f;
             const uint32_t r0 = mix32(pair0 + (q >> 1)), r1 = mix32(pair0 + (q >> 1) + 1);
+            const uint32_t m0 = kRandomM ? mix32(m_pair0 + (q >> 1)) : 0u, m1 = kRandomM ? mix32(m_pair0 + (q >> 1) + 1) : 0u;
             int ms, vs;
-            const uint32_t mc = encode_m(m, &ms), vc = encode_v<true>(v, r0, r1, &vs);
+            const uint32_t mc = encode_m<kRandomM>(m, m0, m1, &ms), vc = encode_v<true>(v, r0, r1, &vs);
             if (!n.none() && (lane & 7) == 0) {
                 ms_out[q / ZERO_STATE_BLOCK] = uint8_t(ms);
                 vs_out[q / ZERO_STATE_BLOCK] = uint8_t(vs);
@@ -617,15 +625,24 @@ __device__ __forceinline__ bool wave_tile(const SetLaunch& a, TileRec* tile) {
     return true;
 }
 
+// m in 8 bits is rounded to nearest where that lets it decay: the codes' worst
+// case is 1.125, which times beta1 has to come below 1.0625 to leave it.  Above,
+// at random (or everywhere, when the set says so).
 template <int G, int O, int S, bool kStaged, typename Stage>
 __device__ __forceinline__ void step_wave(const zero_step_control* __restrict__ ctl, const TensorRec& r, const Extent& x,
-                                          Stage* stage) {
+                                          bool random_m, Stage* stage) {
     const Consts c = *reinterpret_cast<const Consts*>(ctl->group[r.group]);
     const float mult = ctl->grad_mult;
     const uint32_t key = mix32(r.key + uint32_t(ctl->t) * 0x9E3779B9u);
     const int lane = threadIdx.x & 63;
-    if (x.whole()) step_tile<G, O, S, true, kStaged>(r, c, mult, key, x, lane, stage);
-    else step_tile<G, O, S, false, kStaged>(r, c, mult, key, x, lane, stage);
+    if constexpr (S == ZERO_DTYPE_MXFP8)
+        if (random_m || c.beta1 > ZERO_NEAREST_BETA1) {
+            if (x.whole()) step_tile<G, O, S, true, kStaged, true>(r, c, mult, key, x, lane, stage);
+            else step_tile<G, O, S, false, kStaged, true>(r, c, mult, key, x, lane, stage);
+            return;
+        }
+    if (x.whole()) step_tile<G, O, S, true, kStaged, false>(r, c, mult, key, x, lane, stage);
+    else step_tile<G, O, S, false, kStaged, false>(r, c, mult, key, x, lane, stage);
 }
 
 template <int G, int O, int S>
@@ -636,7 +653,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const SetLaunch a, cons
     const Extent x = extent(r, tile.tile, S == ZERO_DTYPE_MXFP8 ? block_shift(r) : tile_shift(r.p, 4, r.spare));
     if (x.hi == 0) return;   // a tile counted for another array's shift
     NoStage* none = nullptr;
-    step_wave<G, O, S, false>(ctl, r, x, none);
+    step_wave<G, O, S, false>(ctl, r, x, a.random_m, none);
 }
 
 // For sets with MXFP8 states of which some tensors' tiles are not stored
@@ -657,8 +674,8 @@ __global__ __launch_bounds__(kThreads) void adamw_staged_kernel(const SetLaunch 
         x = extent(r, tile.tile, block_shift(r));
         link = chain(a, tile, r, x);
         staged = x.hi > 0 && !step_direct(r);
-        if (staged) step_wave<G, O, ZERO_DTYPE_MXFP8, true>(ctl, r, x, &stage);
-        else if (x.hi > 0) step_wave<G, O, ZERO_DTYPE_MXFP8, false>(ctl, r, x, &stage);
+        if (staged) step_wave<G, O, ZERO_DTYPE_MXFP8, true>(ctl, r, x, a.random_m, &stage);
+        else if (x.hi > 0) step_wave<G, O, ZERO_DTYPE_MXFP8, false>(ctl, r, x, a.random_m, &stage);
     }
     __syncthreads();
     if (!staged) return;
@@ -714,7 +731,7 @@ __device__ __forceinline__ void encode_tile(const TensorRec& to, const TensorRec
         const Part n = x.part<kWhole>(q);
         const float m[4] = {m4[h].x, m4[h].y, m4[h].z, m4[h].w}, v[4] = {v4[h].x, v4[h].y, v4[h].z, v4[h].w};
         int ms, vs;
-        const uint32_t mc = encode_m(m, &ms), vc = encode_v<false>(v, 0, 0, &vs);
+        const uint32_t mc = encode_m<false>(m, 0, 0, &ms), vc = encode_v<false>(v, 0, 0, &vs);
         if (!n.none() && (lane & 7) == 0) {
             ms_out[q / ZERO_STATE_BLOCK] = uint8_t(ms);
             vs_out[q / ZERO_STATE_BLOCK] = uint8_t(vs);
