@@ -80,7 +80,7 @@ def encode(x, positive, chance=None):
     with np.errstate(under="ignore"):
         y = x * np.repeat(np.ldexp(np.float32(1), 127 - s).astype(np.float32), BLOCK)[:x.size]
     if positive:
-        y = np.maximum(y, np.where(x > 0, np.float32(2.0 ** -9), np.float32(0)))
+        y = np.maximum(y, np.where(x > 0, np.float32(2.0 ** -9), np.float32(0))) + np.float32(0)    # -0: +0
     if chance is None:
         return e4m3_nearest(y), s.astype(np.uint8)
     # the next number below in magnitude and the share of the step to the one above, in which 20 bits are added and cut

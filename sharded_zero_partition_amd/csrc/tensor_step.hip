@@ -266,10 +266,13 @@ __device__ __forceinline__ uint32_t encode_m(const float m[4], uint32_t r0, uint
     return kRandom ? encode4_random(y, r0, r1) : encode4(y);
 }
 
-// v (>= 0), to nearest or at random; a value above zero gets at least code 1.
+// v (>= 0, -0 among it), to nearest or at random; a value above zero gets at
+// least code 1.  A step's v is the sum of +0 or more and never -0; a conversion's
+// is the caller's, and -0 has the largest bits of all.
 template <bool kRandom>
 __device__ __forceinline__ uint32_t encode_v(const float v[4], uint32_t r0, uint32_t r1, int* s) {
-    *s = scale_of(block_max(max4(bits(v[0]), bits(v[1]), bits(v[2]), bits(v[3]))));
+    constexpr uint32_t kMag = kRandom ? 0xFFFFFFFFu : 0x7FFFFFFFu;
+    *s = scale_of(block_max(max4(bits(v[0]) & kMag, bits(v[1]) & kMag, bits(v[2]) & kMag, bits(v[3]) & kMag)));
     const float f = into_block(*s);
     float y[4];
 #pragma unroll

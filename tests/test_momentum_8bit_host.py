@@ -94,3 +94,10 @@ def test_m_rounding_refusals(zp):
     for name in ("nearest", None, 1):
         with pytest.raises(ValueError, match="m_rounding"):
             zp.TensorSet(m=[z], v=[z.clone()], m_rounding=name)
+
+
+def test_a_variance_of_negative_zeros_is_zero():
+    v = np.array([-0.0, 1e-6, 0.0, 3e-7] + [-0.0] * 28, np.float32)
+    code, s = T.encode(v, True)
+    same, t = T.encode(np.abs(v), True)
+    assert np.array_equal(code, same) and np.array_equal(s, t) and not (code & 128).any()
