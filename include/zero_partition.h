@@ -519,7 +519,8 @@ int zero_tensor_set_bind_grads(zero_tensor_set* set, const void* const* grads, v
 /* Sum of squares of every gradient value of the set, in fp64, into the device
  * double *sumsq (accumulate = 1: added to it).  The values are summed as they
  * are, with their loss scale.  The order of the sum is fixed by the tensors'
- * sizes: equal inputs give equal bits.  inf and NaN values give an inf or NaN.
+ * sizes and the gradients' type: equal values give equal bits, wherever the
+ * tensors are and whatever else the set has.  inf and NaN values give an inf or NaN.
  *   sumsq   device, 8-byte aligned
  *   work    device, zero_grad_sumsq_work_bytes(set) bytes, 8-byte aligned, that
  *           nothing else uses until the call's work is done; may be NULL when

@@ -3,9 +3,11 @@
 //
 // Every value is widened to fp64 before it is squared: an fp16 or bf16 square
 // is exact there, no square of an fp32 overflows, and a sum over 10^10 values
-// keeps 5 digits more than fp32 has.  The tiles are dealt to blocks in a fixed
-// way and the blocks' sums added in a fixed order, so equal inputs give equal
-// bits; there are no atomics.
+// keeps 5 digits more than fp32 has.  A tensor's tiles start with it, an element
+// goes to a lane by its number in the tensor, the tiles are dealt to blocks in a
+// fixed way and the blocks' sums added in a fixed order: equal values in tensors
+// of equal sizes give equal bits, wherever the tensors are.  There are no
+// atomics.
 //
 // Bound by reading 2 or 4 bytes an element: 71 us for 200 M bf16 values (5.7
 // TB/s, a plain copy reaches 6.05).  Non-temporal loads take 68, but the step
@@ -80,14 +82,14 @@ __global__ __launch_bounds__(kBlock) void sumsq_kernel(const SetLaunch a, double
     constexpr int kWaves = kBlock / 64;
     const int lane = threadIdx.x & 63;
     double s = 0.0;
-    for (int64_t w = int64_t(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); w < a.n_tiles;
+    for (int64_t w = int64_t(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); w < a.n_norm_tiles;
          w += int64_t(gridDim.x) * kWaves) {
-        const TileRec tile = a.tile[w];
+        const TileRec tile = a.norm_tile[w];
         const TensorRec& r = a.rec[tile.tensor];
-        const int64_t base = int64_t(tile.tile) * kSetTile - tile_shift(r.grad, int(sizeof(typename T::elem)), r.spare);
+        const int64_t base = int64_t(tile.tile) * kSetTile;
         const auto* g = (Global<const typename T::elem>*)r.grad + base;
-        const int64_t left = r.numel - base;
-        if (base >= 0 && left >= kSetTile) {
+        const int64_t left = r.numel - base;   // > 0
+        if (left >= kSetTile) {
             typename T::at x[T::kLoads];
 #pragma unroll
             for (int h = 0; h < T::kLoads; ++h) x[h] = *(Global<const typename T::at>*)(g + (h * 64 + lane) * T::kWide);
@@ -100,29 +102,29 @@ __global__ __launch_bounds__(kBlock) void sumsq_kernel(const SetLaunch a, double
                 }
         } else {
             // groups of 64 vectors where the tensor has all of one, else of
-            // single values, the nearest in the places of those it has not
+            // single values, its last in the places of those it has not
             constexpr int kGroup = 64 * T::kWide;
-            const int lo = base < 0 ? int(-base) : 0, hi = left < kSetTile ? int(left) : int(kSetTile);
+            const int hi = int(left);
 #pragma unroll
             for (int h = 0; h < T::kLoads; ++h) {
                 const int first = h * kGroup;
                 if (first >= hi) break;
                 typename T::elem x[T::kWide] = {};
                 bool has[T::kWide] = {};
-                if (lo <= first && first + kGroup <= hi) {
+                if (first + kGroup <= hi) {
                     const typename T::at v = *(Global<const typename T::at>*)(g + first + lane * T::kWide);
 #pragma unroll
                     for (int k = 0; k < T::kWide; ++k) x[k] = v[k], has[k] = true;
                 } else if (hi <= first + 64) {
                     const int e = first + lane;
-                    has[0] = e >= lo && e < hi;
-                    x[0] = g[e < lo ? lo : e < hi ? e : hi - 1];
+                    has[0] = e < hi;
+                    x[0] = g[e < hi ? e : hi - 1];
                 } else {
 #pragma unroll
                     for (int k = 0; k < T::kWide; ++k) {
                         const int e = first + k * 64 + lane;
-                        has[k] = e >= lo && e < hi;
-                        x[k] = g[e < lo ? lo : e < hi ? e : hi - 1];
+                        has[k] = e < hi;
+                        x[k] = g[e < hi ? e : hi - 1];
                     }
                 }
 #pragma unroll
@@ -148,9 +150,9 @@ __global__ __launch_bounds__(kThreads) void sumsq_join_kernel(const double* work
 
 }  // namespace
 
-int64_t sumsq_blocks(int64_t n_tiles) {
-    if (n_tiles <= kOneTiles) return 1;
-    const int64_t b = (n_tiles + kThreads / 64 - 1) / (kThreads / 64);
+int64_t sumsq_blocks(int64_t n_norm_tiles) {
+    if (n_norm_tiles <= kOneTiles) return 1;
+    const int64_t b = (n_norm_tiles + kThreads / 64 - 1) / (kThreads / 64);
     return b < kMaxBlocks ? b : kMaxBlocks;
 }
 
@@ -158,7 +160,7 @@ namespace {
 
 template <int D>
 void run_sumsq(const SetLaunch& a, double* sumsq, bool accumulate, double* work, hipStream_t s, const KernelEvents& ev) {
-    const int blocks = int(sumsq_blocks(a.n_tiles));
+    const int blocks = int(sumsq_blocks(a.n_norm_tiles));
     if (blocks == 1) {
         launch(sumsq_kernel<D, kOneThreads>, dim3(1), kOneThreads, s, ev, a, sumsq, accumulate, work);
         return;

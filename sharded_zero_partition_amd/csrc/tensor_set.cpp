@@ -28,10 +28,12 @@ struct zero_tensor_set {
     bool random_m = false;
     int32_t max_group = 0;
     int64_t n_tiles = 0;
+    int64_t n_norm_tiles = 0;
     std::vector<int64_t> numel;              // as given, empty tensors too
     std::vector<zp::TensorRec> rec;          // host copy of the device records (non-empty tensors)
-    zp::TensorRec* d_rec = nullptr;          // one allocation: the records, then the tiles
+    zp::TensorRec* d_rec = nullptr;          // one allocation: the records, the tiles, the norm's tiles
     zp::TileRec* d_tile = nullptr;
+    zp::TileRec* d_norm_tile = nullptr;      // d_tile where no tensor has one more there
     // byte ranges of the arrays that a step or a conversion writes, sorted;
     // they are disjoint
     std::vector<std::pair<uintptr_t, uintptr_t>> written;
@@ -114,7 +116,7 @@ int check_not_capturing(void* stream, const char* who) {
 }
 
 SetLaunch set_launch(const zero_tensor_set* s) {
-    return SetLaunch{s->d_rec, s->d_tile, s->n_tiles, s->grad_type, s->state_type, s->out_type,
+    return SetLaunch{s->d_rec, s->d_tile, s->n_tiles, s->d_norm_tile, s->n_norm_tiles, s->grad_type, s->state_type, s->out_type,
                      s->staged_step, s->staged_codes, s->random_m};
 }
 
@@ -187,10 +189,10 @@ int create(const zero_tensor* tensors, int64_t n, int32_t grad_type, int32_t sta
         if (t.p) shift = tile_shift(t.p, 4, any);
         if (state_type == ZERO_DTYPE_FP32) shift = std::max<int64_t>(shift, tile_shift(t.m, 4, any));
         if (mx) shift = ((reinterpret_cast<uintptr_t>(t.p) / 4) | reinterpret_cast<uintptr_t>(t.m)) & 32;
-        if (!t.p && !st && t.grad) shift = tile_shift(t.grad, dtype_bytes(grad_type), any);
         const int64_t tiles = (t.numel + shift - 1) / kSetTile + 1;
         if (tiles > kMaxSetTiles - set->n_tiles) return fail(ZERO_ERR_OUT_OF_MEMORY, "more than 2^25 tiles of 1024 elements");
         set->n_tiles += tiles;
+        set->n_norm_tiles += (t.numel - 1) / kSetTile + 1;
         set->max_group = std::max(set->max_group, t.group);
         bool ok = true;
         if (t.p) ok = ok && add_range(&set->written, t.p, t.numel, 4);
@@ -231,9 +233,13 @@ int create(const zero_tensor* tensors, int64_t n, int32_t grad_type, int32_t sta
             if (rc != ZERO_OK) return rc;
         }
     std::vector<TileRec> tiles;
-    tiles.reserve(size_t(set->n_tiles));
+    const bool own_norm_tiles = grad_type != ZERO_DTYPE_NONE && set->n_norm_tiles != set->n_tiles;
+    tiles.reserve(size_t(set->n_tiles + (own_norm_tiles ? set->n_norm_tiles : 0)));
     for (size_t k = 0; k < set->rec.size(); ++k)
         for (int64_t j = 0; j * kSetTile < set->rec[k].numel + set->rec[k].spare; ++j) tiles.push_back({uint32_t(k), uint32_t(j)});
+    if (own_norm_tiles)
+        for (size_t k = 0; k < set->rec.size(); ++k)
+            for (int64_t j = 0; j * kSetTile < set->rec[k].numel; ++j) tiles.push_back({uint32_t(k), uint32_t(j)});
 
     hipError_t e = hipGetDevice(&set->device);
     if (e != hipSuccess) return fail_hip(e, "hipGetDevice");
@@ -247,6 +253,7 @@ int create(const zero_tensor* tensors, int64_t n, int32_t grad_type, int32_t sta
         if (e != hipSuccess) return fail_hip(e, "hipMalloc (tensor set)");
         set->d_rec = static_cast<TensorRec*>(d);
         set->d_tile = reinterpret_cast<TileRec*>(static_cast<uint8_t*>(d) + rec_bytes);
+        set->d_norm_tile = set->d_tile + (own_norm_tiles ? set->n_tiles : 0);
         hipStream_t s = static_cast<hipStream_t>(stream);
         e = hipMemcpyAsync(set->d_rec, set->rec.data(), rec_bytes, hipMemcpyHostToDevice, s);
         if (e == hipSuccess) e = hipMemcpyAsync(set->d_tile, tiles.data(), tile_bytes, hipMemcpyHostToDevice, s);
@@ -339,7 +346,7 @@ extern "C" int zero_tensor_set_bind_grads(zero_tensor_set* set, const void* cons
 
 extern "C" int64_t zero_grad_sumsq_work_bytes(const zero_tensor_set* set) {
     if (!set) return 0;
-    const int64_t blocks = zp::sumsq_blocks(set->n_tiles);
+    const int64_t blocks = zp::sumsq_blocks(set->n_norm_tiles);
     return blocks > 1 ? blocks * int64_t(sizeof(double)) : 0;
 }
 

@@ -23,15 +23,16 @@ struct TensorRec {
 };
 static_assert(sizeof(TensorRec) == 80, "TensorRec layout");
 
-// A tile is kSetTile consecutive elements of one tensor; one wave takes it.
-// Tile k of a tensor starts at element k kSetTile - shift, so the first and the
-// last one may be shorter.  The shift (0 .. kAlign - 1) puts an array's whole
-// tiles on kAlign-element boundaries in memory, for 16- and 32-bit elements on
-// lines of 128 bytes.  A store that leaves a line unfinished is dear (state
-// conversion to fp32, 200 M elements: 346 us on lines, 459 us one element off
-// them), a load off its lines costs 5 to 10%.  Flat buffers of several kinds
-// mostly start on lines, so one tensor's shift is the same in all of them; where
-// it is not, only the array it was taken from gains.
+// A tile is kSetTile consecutive elements of one tensor; one wave takes it.  The
+// norm's tiles start with the tensor, so the order of its sum depends on sizes
+// alone.  In a step and a conversion tile k of a tensor starts at element
+// k kSetTile - shift, so the first and the last one may be shorter.  The shift
+// (0 .. kAlign - 1) puts an array's whole tiles on kAlign-element boundaries in
+// memory, for 16- and 32-bit elements on lines of 128 bytes.  A store that leaves
+// a line unfinished is dear (state conversion to fp32, 200 M elements: 346 us on
+// lines, 459 us one element off them), a load off its lines costs 5 to 10%.  Flat
+// buffers of several kinds mostly start on lines, so one tensor's shift is the
+// same in all of them; where it is not, only the array it was taken from gains.
 constexpr int64_t kSetTile = 1024;
 constexpr int64_t kAlign = 64;
 struct TileRec {
@@ -90,6 +91,8 @@ struct SetLaunch {
     const TensorRec* rec;    // device, one per non-empty tensor
     const TileRec* tile;     // device
     int64_t n_tiles;
+    const TileRec* norm_tile;   // device: tiles of kSetTile from each tensor's first element on
+    int64_t n_norm_tiles;
     int32_t grad_type;
     int32_t state_type;
     int32_t out_type;
@@ -100,7 +103,7 @@ struct SetLaunch {
 
 // Blocks of the sum-of-squares pass, each of which leaves one double in `work`
 // for a second launch to add up; 1: the one block writes the result itself.
-int64_t sumsq_blocks(int64_t n_tiles);
+int64_t sumsq_blocks(int64_t n_norm_tiles);
 
 hipError_t launch_sumsq(const SetLaunch& a, double* sumsq, bool accumulate, double* work, hipStream_t stream,
                         const KernelEvents& ev);
