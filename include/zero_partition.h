@@ -500,7 +500,9 @@ int zero_tensor_set_create(const zero_tensor* tensors, int64_t n, int32_t grad_t
                            int32_t state_type, int32_t out_type, uint32_t seed, void* stream,
                            zero_tensor_set** out);
 
-int zero_tensor_set_destroy(zero_tensor_set* set); /* NULL is accepted */
+/* Free a set (NULL is accepted), also while streams are being captured.  Waits
+ * for the device.  Errors: HIP (the set is still there: call again later). */
+int zero_tensor_set_destroy(zero_tensor_set* set);
 
 /* How steps of a set with MXFP8 states round m (ZERO_M_ROUNDING_AUTO at first).
  * Holds for calls of zero_adamw_step from then on; a captured one keeps what it

@@ -675,24 +675,35 @@ class TensorSet:
         self._h = h
         if m_rounding == "random":
             _check(lib.zero_tensor_set_m_rounding(h, 1))
+        TensorSet._free_late()
         self._keep = lists
         self._work_elems = lib.zero_grad_sumsq_work_bytes(h) // 8
 
-    _late = []   # handles whose sets went while a stream was being captured
+    _late = []   # handles that wait to be freed
 
     def close(self):
         """Free the set's tables.  Work that uses them must have finished.
-        Memory cannot be freed while a stream is being captured: a set that is
-        closed, or collected, meanwhile is freed when the next one is."""
+        Freeing waits for the device, which a stream that is being captured
+        cannot: a set that is closed, or collected, while its thread's current
+        stream is, or that the runtime refuses to free, is freed with the next
+        set that is made or closed.  Captures of other threads go on."""
         if self._h:
             TensorSet._late.append(self._h)
             self._h = None
-        if not torch.cuda.is_current_stream_capturing():
+        TensorSet._free_late()
+
+    @staticmethod
+    def _free_late():
+        if not TensorSet._late or torch.cuda.is_current_stream_capturing():
+            return
+        for _ in range(len(TensorSet._late)):
             try:
-                while True:
-                    lib.zero_tensor_set_destroy(TensorSet._late.pop())
-            except IndexError:      # none left (another thread may have freed the last)
-                pass
+                h = TensorSet._late.pop()
+            except IndexError:      # another thread has freed the last
+                return
+            if lib.zero_tensor_set_destroy(h):
+                TensorSet._late.append(h)
+                return
 
     def __del__(self):
         try:

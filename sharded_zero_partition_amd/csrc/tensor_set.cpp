@@ -115,6 +115,20 @@ int check_not_capturing(void* stream, const char* who) {
     return ZERO_OK;
 }
 
+// Takes the calling thread out of the capture mode in which calls that allocate,
+// free or wait are refused while any stream of the process is being captured:
+// these concern the sets' own tables alone, which no other capture holds.
+class OutsideCaptures {
+public:
+    OutsideCaptures() { (void)hipThreadExchangeStreamCaptureMode(&mode_); }
+    ~OutsideCaptures() { (void)hipThreadExchangeStreamCaptureMode(&mode_); }
+    OutsideCaptures(const OutsideCaptures&) = delete;
+    OutsideCaptures& operator=(const OutsideCaptures&) = delete;
+
+private:
+    hipStreamCaptureMode mode_ = hipStreamCaptureModeRelaxed;
+};
+
 SetLaunch set_launch(const zero_tensor_set* s) {
     return SetLaunch{s->d_rec, s->d_tile, s->n_tiles, s->d_norm_tile, s->n_norm_tiles, s->grad_type, s->state_type, s->out_type,
                      s->staged_step, s->staged_codes, s->random_m};
@@ -248,6 +262,7 @@ int create(const zero_tensor* tensors, int64_t n, int32_t grad_type, int32_t sta
     if (rc != ZERO_OK) return rc;
     const size_t rec_bytes = set->rec.size() * sizeof(TensorRec), tile_bytes = tiles.size() * sizeof(TileRec);
     if (rec_bytes) {
+        const OutsideCaptures guard;
         void* d = nullptr;
         e = hipMalloc(&d, rec_bytes + tile_bytes);
         if (e != hipSuccess) return fail_hip(e, "hipMalloc (tensor set)");
@@ -284,6 +299,7 @@ int bind_grads(zero_tensor_set* set, const void* const* grads, void* stream) {
     if (rc == ZERO_OK) rc = check_not_capturing(stream, "zero_tensor_set_bind_grads");
     if (rc != ZERO_OK) return rc;
     if (!rec.empty()) {
+        const OutsideCaptures guard;
         hipStream_t s = static_cast<hipStream_t>(stream);
         hipError_t e = hipMemcpyAsync(set->d_rec, rec.data(), rec.size() * sizeof(TensorRec), hipMemcpyHostToDevice, s);
         if (e == hipSuccess) e = hipStreamSynchronize(s);
@@ -320,7 +336,11 @@ extern "C" int zero_tensor_set_create(const zero_tensor* tensors, int64_t n, int
 
 extern "C" int zero_tensor_set_destroy(zero_tensor_set* set) {
     zp::clear_error();
-    if (set && set->d_rec) (void)hipFree(set->d_rec);
+    if (set && set->d_rec) {
+        const zp::OutsideCaptures guard;
+        const hipError_t e = hipFree(set->d_rec);
+        if (e != hipSuccess) return zp::fail_hip(e, "hipFree (tensor set)");
+    }
     delete set;
     return ZERO_OK;
 }
