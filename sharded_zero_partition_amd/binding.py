@@ -598,6 +598,17 @@ def _addresses(tensors, what: str, sizes, dev: int) -> list:
     return [t.data_ptr() for t in tensors]
 
 
+def _counted(tensors) -> list:
+    """One tensor for each version counter among these: views share their
+    base's.  A call that writes tensors raises their counters, so that a
+    backward pass that saved one of them before reports it."""
+    first = {}
+    for t in tensors:
+        base = t if t._base is None else t._base
+        first.setdefault(id(base), base)
+    return list(first.values())
+
+
 _BITS16 = {torch.float16: DTYPE_FP16, torch.int16: DTYPE_FP16, torch.bfloat16: DTYPE_BF16}
 _GRAD_DTYPES = {**_BITS16, torch.float32: DTYPE_FP32}
 _SCALE_DTYPES = {torch.uint8: DTYPE_MXFP8, torch.float8_e8m0fnu: DTYPE_MXFP8}
@@ -607,7 +618,9 @@ _STATE_DTYPES = {torch.float32: DTYPE_FP32, torch.uint8: DTYPE_MXFP8, torch.floa
 class TensorSet:
     """Owner of a zero_tensor_set: lists of device tensors, contiguous and of
     any size, one entry for each parameter (or each piece of one that a rank's
-    shard holds, Layout.rank_segments).
+    shard holds, Layout.rank_segments).  A call writes p, out and states as an
+    in-place operation does: autograd's version counters of p and out are raised
+    (of m and v by a conversion), but not by a graph's replays.
 
       p        fp32 master values
       grads    fp16 (or int16 bit patterns), bf16 or fp32
@@ -677,6 +690,8 @@ class TensorSet:
             _check(lib.zero_tensor_set_m_rounding(h, 1))
         TensorSet._free_late()
         self._keep = lists
+        self._written = _counted(lists.get("p", []) + lists.get("out", []))
+        self._converted = _counted(lists.get("m", []) + lists.get("v", []))
         self._work_elems = lib.zero_grad_sumsq_work_bytes(h) // 8
 
     _late = []   # handles that wait to be freed
@@ -745,11 +760,13 @@ class TensorSet:
             raise ValueError("the step has not begun (StepControl.begin)")
         _on_current_device(control.device_index, "the control block")
         _check(lib.zero_adamw_step(self._h, control._ptr, control._n_groups, _raw_stream(stream, self._dev)))
+        torch.autograd.graph.increment_version(self._written)
 
     def states_from(self, source: "TensorSet", stream=None):
         """zero_states_convert: write `source`'s states into this set's, fp32
         to 8 bits or back."""
         _check(lib.zero_states_convert(self._h, source._h, _raw_stream(stream, self._dev)))
+        torch.autograd.graph.increment_version(self._converted)
 
 
 def version() -> int:
