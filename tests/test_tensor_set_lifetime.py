@@ -54,7 +54,8 @@ def test_a_free_in_this_thread_s_capture_waits(monkeypatch):
 
 
 @pytest.mark.gpu
-def test_sets_come_and_go_in_one_thread_while_another_captures():
+@pytest.mark.parametrize("default_stream", [False, True])
+def test_sets_come_and_go_in_one_thread_while_another_captures(default_stream):
     """In torch's default mode, in which a plain free or a wait of any thread is refused while a stream is captured."""
     g = torch.randn(200_000, device="cuda")
     other = [torch.ones(5000, device="cuda") for _ in range(3)]
@@ -62,7 +63,7 @@ def test_sets_come_and_go_in_one_thread_while_another_captures():
     s.grad_sumsq(out)
     want, errors, sums = out.item(), [], torch.zeros(8, dtype=torch.float64, device="cuda")
     begun, done = threading.Event(), threading.Event()
-    st = torch.cuda.Stream()
+    st = torch.cuda.default_stream() if default_stream else torch.cuda.Stream()
 
     def work():
         try:
