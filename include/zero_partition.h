@@ -526,7 +526,8 @@ int zero_tensor_set_bind_grads(zero_tensor_set* set, const void* const* grads, v
  *   sumsq   device, 8-byte aligned
  *   work    device, zero_grad_sumsq_work_bytes(set) bytes, 8-byte aligned, that
  *           nothing else uses until the call's work is done; may be NULL when
- *           that is 0
+ *           that is 0.  Neither may overlap the other, an array of the set that
+ *           a step writes, or (unchecked) a gradient.
  * Asynchronous on `stream`.  Errors: INVALID_ARG, ALIGNMENT, STATE (no
  * gradients, another device), HIP. */
 int64_t zero_grad_sumsq_work_bytes(const zero_tensor_set* set);

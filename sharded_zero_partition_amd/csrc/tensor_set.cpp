@@ -376,7 +376,13 @@ extern "C" int zero_grad_sumsq(const zero_tensor_set* set, double* sumsq, int32_
     if (accumulate != 0 && accumulate != 1) return fail(ZERO_ERR_INVALID_ARG, "accumulate must be 0 or 1");
     if (!zp::is_aligned(sumsq, 8) || !zp::is_aligned(work, 8))
         return fail(ZERO_ERR_ALIGNMENT, "sumsq or work is not 8-byte aligned");
-    if (!work && zero_grad_sumsq_work_bytes(set) > 0) return fail(ZERO_ERR_INVALID_ARG, "work is NULL");
+    const uintptr_t work_bytes = uintptr_t(zero_grad_sumsq_work_bytes(set));
+    if (!work && work_bytes > 0) return fail(ZERO_ERR_INVALID_ARG, "work is NULL");
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(sumsq), wlo = reinterpret_cast<uintptr_t>(work);
+    if (zp::meets(set->written, lo, lo + sizeof(*sumsq)) || (work_bytes > 0 && zp::meets(set->written, wlo, wlo + work_bytes)))
+        return fail(ZERO_ERR_INVALID_ARG, "sumsq or work overlaps an array of the set");
+    if (lo < wlo + work_bytes && wlo < lo + sizeof(*sumsq) && work_bytes > 0)
+        return fail(ZERO_ERR_INVALID_ARG, "sumsq is inside work");
     if (const char* what = zp::lacks(set, false, true, false)) return fail(ZERO_ERR_STATE, what);
     const int rc = zp::check_set_device(set, stream, "zero_grad_sumsq");
     if (rc != ZERO_OK) return rc;
