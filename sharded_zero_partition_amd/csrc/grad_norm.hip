@@ -9,8 +9,9 @@
 // of equal sizes give equal bits, wherever the tensors are.  There are no
 // atomics.
 //
-// Bound by reading 2 or 4 bytes an element: 71 us for 200 M bf16 values (5.7
-// TB/s, a plain copy reaches 6.05).  Non-temporal loads take 68, but the step
+// Bound by reading 2 or 4 bytes an element: 69 to 72 us for 200 M bf16 values
+// (5.7 TB/s, a plain copy reaches 6.05), on 128-byte lines or off them.
+// Non-temporal loads take 68, but the step
 // that follows then finds nothing of the gradients in the last-level cache: norm
 // and step together, 355 us with these loads and 385 with those (120 M elements,
 // states in 8 bits).
@@ -30,6 +31,7 @@ constexpr int kOneThreads = 1024;
 constexpr int64_t kOneTiles = 64;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 
 template <typename T>
@@ -76,6 +78,34 @@ __device__ __forceinline__ double block_sum(double x) {
 
 __device__ __forceinline__ void put(double* sumsq, double s, bool accumulate) { *sumsq = accumulate ? *sumsq + s : s; }
 
+// A whole tile's vectors, element 8 (64 h + lane) on (4 for fp32) in x[h].
+template <typename T>
+__device__ __forceinline__ void load_tile(const Global<const typename T::elem>* g, int lane, typename T::at x[T::kLoads]) {
+#pragma unroll
+    for (int h = 0; h < T::kLoads; ++h) x[h] = *(Global<const typename T::at>*)(g + (h * 64 + lane) * T::kWide);
+}
+
+// The same for 16-bit values at an odd element, g[-1] being one of the tensor's:
+// words from one value before on, so that loads are 4-byte aligned, and the
+// eighth value from the next lane's.  (One tensor of 200 M bf16 values one
+// element in: 77 us, and 88 by loads that are 2-byte aligned.)
+template <typename T>
+__device__ __forceinline__ void load_odd_tile(const Global<const typename T::elem>* g, int lane, typename T::at x[T::kLoads]) {
+    typedef u32x4 at4 __attribute__((aligned(4)));
+    u32x4 w[T::kLoads];
+#pragma unroll
+    for (int h = 0; h < T::kLoads; ++h) w[h] = *(Global<const at4>*)(g - 1 + (h * 64 + lane) * T::kWide);
+    const uint32_t last = g[kSetTile - 1];
+#pragma unroll
+    for (int h = 0; h < T::kLoads; ++h) {
+        const uint32_t after = h + 1 < T::kLoads ? uint32_t(__builtin_amdgcn_readfirstlane(int(w[h + 1].x))) : last;
+        const uint32_t next = uint32_t(__shfl_down(int(w[h].x), 1, 64)), w4 = lane == 63 ? after : next;
+        const u32x4 v = {__builtin_amdgcn_alignbit(w[h].y, w[h].x, 16), __builtin_amdgcn_alignbit(w[h].z, w[h].y, 16),
+                         __builtin_amdgcn_alignbit(w[h].w, w[h].z, 16), __builtin_amdgcn_alignbit(w4, w[h].w, 16)};
+        x[h] = __builtin_bit_cast(u16x8, v);
+    }
+}
+
 template <int D, int kBlock>
 __global__ __launch_bounds__(kBlock) void sumsq_kernel(const SetLaunch a, double* sumsq, bool accumulate, double* work) {
     typedef Grad<D> T;
@@ -91,8 +121,12 @@ __global__ __launch_bounds__(kBlock) void sumsq_kernel(const SetLaunch a, double
         const int64_t left = r.numel - base;   // > 0
         if (left >= kSetTile) {
             typename T::at x[T::kLoads];
-#pragma unroll
-            for (int h = 0; h < T::kLoads; ++h) x[h] = *(Global<const typename T::at>*)(g + (h * 64 + lane) * T::kWide);
+            bool odd = false;
+            if constexpr (sizeof(typename T::elem) == 2) {
+                odd = (reinterpret_cast<uintptr_t>(r.grad) & 2u) != 0 && base > 0;
+                if (odd) load_odd_tile<T>(g, lane, x);
+            }
+            if (!odd) load_tile<T>(g, lane, x);
 #pragma unroll
             for (int h = 0; h < T::kLoads; ++h)
 #pragma unroll
