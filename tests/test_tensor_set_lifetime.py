@@ -115,3 +115,20 @@ def test_a_set_deferred_in_a_capture_goes_with_the_next_one_made():
     for _ in range(3):
         graph.replay()
         assert out.item() == 100.0
+
+
+@pytest.mark.gpu
+def test_the_abi_frees_a_set_while_its_own_thread_captures():
+    """As a C program may; the binding waits for the capture's end."""
+    g = torch.ones(100, device="cuda")
+    s, gone = zp.TensorSet(grads=[g]), zp.TensorSet(grads=[g])
+    h, gone._h = gone._h, None
+    out = torch.zeros((), dtype=torch.float64, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.grad_sumsq(out)
+        assert zp.lib.zero_tensor_set_destroy(h) == 0
+        s.grad_sumsq(out, accumulate=True)
+    for _ in range(3):
+        graph.replay()
+        assert out.item() == 200.0
