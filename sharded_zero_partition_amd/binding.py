@@ -598,17 +598,6 @@ def _addresses(tensors, what: str, sizes, dev: int) -> list:
     return [t.data_ptr() for t in tensors]
 
 
-def _counted(tensors) -> list:
-    """One tensor for each version counter among these: views share their
-    base's.  A call that writes tensors raises their counters, so that a
-    backward pass that saved one of them before reports it."""
-    first = {}
-    for t in tensors:
-        base = t if t._base is None else t._base
-        first.setdefault(id(base), base)
-    return list(first.values())
-
-
 _BITS16 = {torch.float16: DTYPE_FP16, torch.int16: DTYPE_FP16, torch.bfloat16: DTYPE_BF16}
 _GRAD_DTYPES = {**_BITS16, torch.float32: DTYPE_FP32}
 _SCALE_DTYPES = {torch.uint8: DTYPE_MXFP8, torch.float8_e8m0fnu: DTYPE_MXFP8}
@@ -690,8 +679,7 @@ class TensorSet:
             _check(lib.zero_tensor_set_m_rounding(h, 1))
         TensorSet._free_late()
         self._keep = lists
-        self._written = _counted(lists.get("p", []) + lists.get("out", []))
-        self._converted = _counted(lists.get("m", []) + lists.get("v", []))
+        self._counted = {}   # lists written by a call -> their version counters' tensors
         self._work_elems = lib.zero_grad_sumsq_work_bytes(h) // 8
 
     _late = []   # handles that wait to be freed
@@ -725,6 +713,18 @@ class TensorSet:
             self.close()
         except Exception:
             pass
+
+    def _wrote(self, *names):
+        """Raise the version counters of lists that a call wrote, so that a
+        backward pass that saved one of their tensors before reports it.  Views
+        share their base's, so a flat buffer is counted once; which tensors
+        these are is looked up at the first such call."""
+        if names not in self._counted:
+            tensors = [t for name in names for t in self._keep.get(name, ())]
+            bases = [t._base for t in tensors]
+            views = {id(b): b for b in bases if b is not None}
+            self._counted[names] = list(views.values()) + [t for t, b in zip(tensors, bases) if b is None]
+        torch.autograd.graph.increment_version(self._counted[names])
 
     def bind_grads(self, grads, stream=None):
         """Replace the gradient tensors (same sizes and dtype)."""
@@ -760,13 +760,13 @@ class TensorSet:
             raise ValueError("the step has not begun (StepControl.begin)")
         _on_current_device(control.device_index, "the control block")
         _check(lib.zero_adamw_step(self._h, control._ptr, control._n_groups, _raw_stream(stream, self._dev)))
-        torch.autograd.graph.increment_version(self._written)
+        self._wrote("p", "out")
 
     def states_from(self, source: "TensorSet", stream=None):
         """zero_states_convert: write `source`'s states into this set's, fp32
         to 8 bits or back."""
         _check(lib.zero_states_convert(self._h, source._h, _raw_stream(stream, self._dev)))
-        torch.autograd.graph.increment_version(self._converted)
+        self._wrote("m", "v")
 
 
 def version() -> int:

@@ -48,7 +48,7 @@ def test_counters_of_tensors_and_views():
     before = flat._version, own._version, other._version
     step(s)
     assert flat._version > before[0] and own._version > before[1] and other._version == before[2]
-    assert len(s._written) == 2                               # one for the flat buffer's two views
+    assert len(s._counted["p", "out"]) == 2                   # one for the flat buffer's two views
 
 
 def test_a_conversion_raises_the_states_counters():
