@@ -484,7 +484,7 @@ enum {
  *   grad_type   FP16, BF16 or FP32; NONE for a set that only converts states
  *   state_type  FP32 or MXFP8; NONE for a set that only sums squares
  *   out_type    FP16, BF16, or NONE (no 16-bit copies)
- *   seed        of the random rounding of MXFP8 variances
+ *   seed        of the random rounding of MXFP8 states
  * Of the non-empty tensors, all or none have p, and all or none have grad (none:
  * zero_tensor_set_bind_grads comes first); m and v are set when state_type is
  * not NONE, the scales when it is MXFP8, out when out_type is not NONE, and are

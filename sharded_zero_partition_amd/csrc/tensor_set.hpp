@@ -29,10 +29,11 @@ static_assert(sizeof(TensorRec) == 80, "TensorRec layout");
 // k kSetTile - shift, so the first and the last one may be shorter.  The shift
 // (0 .. kAlign - 1) puts an array's whole tiles on kAlign-element boundaries in
 // memory, for 16- and 32-bit elements on lines of 128 bytes.  A store that leaves
-// a line unfinished is dear (state conversion to fp32, 200 M elements: 346 us on
-// lines, 459 us one element off them), a load off its lines costs 5 to 10%.  Flat
-// buffers of several kinds mostly start on lines, so one tensor's shift is the
-// same in all of them; where it is not, only the array it was taken from gains.
+// a line unfinished is dear (state conversion to fp32, 200 M elements, tiles that
+// start with the tensor: 348 us on lines, 469 us one element off them); loads off
+// their lines cost little (the norm: nothing).  Flat buffers of several kinds
+// mostly start on lines, so one tensor's shift is the same in all of them; where
+// it is not, only the array it was taken from gains.
 constexpr int64_t kSetTile = 1024;
 constexpr int64_t kAlign = 64;
 struct TileRec {

@@ -64,8 +64,8 @@ struct Part {
 // Elements q .. q + 3 of a tile, p being where its element 0 is (the same in all
 // lanes; outside the array for a tile that starts before it) and q a lane's
 // first.  Non-temporal: no line is used again (plain loads and stores on whole
-// lines: 1039 against 926 us for the step with fp32 states of 200 M elements,
-// 602 against 547 us in 8 bits).
+// lines: 1038 against 934 us for the step with fp32 states of 200 M elements,
+// 607 against 546 us in 8 bits).
 template <typename T>
 __device__ __forceinline__ typename Four<T>::vec load4(const T* p, uint32_t q) {
     typedef const typename Four<T>::at at;
@@ -456,7 +456,7 @@ __device__ __forceinline__ Chain chain(const SetLaunch& a, const TileRec& tile, 
 }
 
 // The step of 200 M elements in 8 bits reads 3 and writes 0.2% more than it must
-// this way and takes 558 to 582 us against 540 on lines; six blocks of 24 KB of
+// this way and takes 556 to 588 us against 546 on lines; six blocks of 24 KB of
 // LDS fit a CU, as many waves as the registers allow.
 //
 // A wave's tile, from the block's staged results to memory; `at` is where its
@@ -630,7 +630,8 @@ __device__ __forceinline__ bool wave_tile(const SetLaunch& a, TileRec* tile) {
 
 // m in 8 bits is rounded to nearest where that lets it decay: the codes' worst
 // case is 1.125, which times beta1 has to come below 1.0625 to leave it.  Above,
-// at random (or everywhere, when the set says so).
+// at random (or everywhere, when the set says so), which costs no time: 13B
+// share, 200 M elements, 557 us either way.
 template <int G, int O, int S, bool kStaged, typename Stage>
 __device__ __forceinline__ void step_wave(const zero_step_control* __restrict__ ctl, const TensorRec& r, const Extent& x,
                                           bool random_m, Stage* stage) {
