@@ -601,18 +601,145 @@ int zero_adamw_step(const zero_tensor_set* set, const zero_step_control* ctl, in
 int zero_states_convert(const zero_tensor_set* dst, const zero_tensor_set* src, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Activation checkpoints in 8 bits, and the gradients made from them        */
+/* ------------------------------------------------------------------------ */
+
+/* What a rank keeps of its forward pass for the backward one, a byte and a
+ * thirty-second a value, and the parameter gradients that it makes from it:
+ *
+ *   zero_checkpoint_store, _load    a matrix to MXFP8 and back
+ *   zero_activation, _grad          an activation that stores the checkpoint of
+ *                                   its input in the same pass, and its gradient
+ *   zero_weight_grad                the weight and bias gradient of a linear
+ *                                   layer from the checkpoint of its input
+ *   zero_embedding_lookup, _grad    rows of a table, and the table's gradient
+ *
+ * Gradients come in fp16, bf16 or fp32, the types that tensor sets read.  The
+ * calls are asynchronous on `stream`, hold no state of their own and can be
+ * captured into a graph.  Equal inputs give equal bits. */
+
+/* A matrix in device memory: row r's element c is data[r * stride + c].  Only
+ * element alignment is required.  A matrix that is read may have any stride >= 0
+ * (0: every row the same); one that is written needs stride >= cols.  Pointers
+ * of an empty matrix are ignored. */
+typedef struct zero_matrix {
+    void* data;
+    int64_t rows;
+    int64_t cols;
+    int64_t stride;     /* elements from a row to the next */
+    int32_t type;       /* ZERO_DTYPE_FP16, BF16 or FP32 */
+    int32_t reserved;
+} zero_matrix;
+
+/* A matrix in 8 bits (MXFP8, as for states): blocks of 32 neighbouring values of
+ * a row, the last of a row maybe shorter.  Element c of row r with scale byte
+ * s = scale[r * B + c / 32] stands for e4m3(code[r * 32 B + c]) * 2^(s - 127), B
+ * being ceil(cols / 32).  Storing takes the least s >= 1 that brings the block's
+ * largest magnitude to 448 or below, rounds to nearest, ties to even (what is
+ * beyond 1.875 2^127 to that), and pads rows of codes with zeros.  A block with an inf or NaN gets s = 255 and codes
+ * 0x7F: all of it reads back as NaN.  Other bytes than those that a store writes
+ * are not a checkpoint. */
+typedef struct zero_checkpoint {
+    uint8_t* code;      /* rows * 32 B bytes, 16-byte aligned */
+    uint8_t* scale;     /* rows * B bytes */
+    int64_t rows;
+    int64_t cols;
+} zero_checkpoint;
+
+/* Bytes of a checkpoint's codes and scales; either pointer may be NULL.
+ * Errors: INVALID_ARG (negative), INDEX_OVERFLOW (more than 2^48 codes, or 2^31
+ * columns). */
+int zero_checkpoint_bytes(int64_t rows, int64_t cols, int64_t* code_bytes, int64_t* scale_bytes);
+
+/* Store x, and read a checkpoint back (exact in every type but for what leaves
+ * its range: fp16 beyond 65504 becomes inf).  Shapes are equal and neither
+ * overlaps the other.  Errors: INVALID_ARG, ALIGNMENT, INDEX_OVERFLOW, STATE (the
+ * stream is another device's), HIP. */
+int zero_checkpoint_store(const zero_matrix* x, const zero_checkpoint* c, void* stream);
+int zero_checkpoint_load(const zero_checkpoint* c, const zero_matrix* out, void* stream);
+
+enum {
+    ZERO_ACT_RELU = 0,       /* z > 0 ? z : 0 (a NaN stays) */
+    ZERO_ACT_SILU = 1,       /* z / (1 + exp(-z)) */
+    ZERO_ACT_GELU = 2,       /* z (1 + erf(z / sqrt 2)) / 2 */
+    ZERO_ACT_GELU_TANH = 3   /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+};
+
+/* out = act(x), or act(x) * up where `up` is given (a gated layer), computed in
+ * fp32 and rounded once; and in the same pass the checkpoints that the backward
+ * pass needs: of x, of up where it is given, and of out (as rounded) where
+ * `c_out` is, for the weight gradient of the layer that reads it.  c_x may be
+ * NULL when nothing is kept (then c_up is NULL too).  x, up and out have one
+ * type.  out may be x or up itself (the same place and stride); nothing else may
+ * overlap what is written.  Errors: as for zero_checkpoint_store. */
+int zero_activation(int32_t kind, const zero_matrix* x, const zero_matrix* up, const zero_matrix* out,
+                    const zero_checkpoint* c_x, const zero_checkpoint* c_up, const zero_checkpoint* c_out,
+                    void* stream);
+
+/* The gradients of x and up from those of out, with x and up as the checkpoints
+ * hold them:
+ *   dx = dy * act'(x)    or, gated,    dx = dy * up * act'(x),  dup = dy * act(x)
+ * in fp32, rounded once.  c_up and dup come together.  dy, dx and dup have one
+ * type; dx or dup may be dy itself.  Errors: as for zero_checkpoint_store. */
+int zero_activation_grad(int32_t kind, const zero_matrix* dy, const zero_checkpoint* c_x,
+                         const zero_checkpoint* c_up, const zero_matrix* dx, const zero_matrix* dup,
+                         void* stream);
+
+/* Gradients of a linear layer y[t, n] = sum_k x[t, k] w[n, k] + b[n] from the
+ * gradient of y and the checkpoint of x:
+ *   dw[n, k] = sum_t dy[t, n] x[t, k]        bias[n] = sum_t dy[t, n]
+ * added to what is there when accumulate is 1.  Products are exact and sums in
+ * fp32, in an order fixed by the sizes; results are rounded once.
+ *   dy          fp16, bf16 or fp32, T rows
+ *   dw          fp16, bf16 or fp32, n by k; with transposed = 1 it is k by n (for a
+ *               weight kept as inputs by outputs)
+ *   bias        n values of dw's type, or NULL
+ *   work        device, zero_weight_grad_work_bytes() bytes, 16-byte aligned, that
+ *               nothing else uses until the call's work is done; may be NULL
+ *               when that is 0
+ * With T = 0 the sums are zero.  Nothing written may overlap anything else.
+ * Errors: as for zero_checkpoint_store. */
+int64_t zero_weight_grad_work_bytes(int64_t T, int64_t n, int64_t k, int32_t dy_type);
+int zero_weight_grad(const zero_matrix* dy, const zero_checkpoint* x, const zero_matrix* dw, int32_t transposed,
+                     void* bias, int32_t accumulate, void* work, void* stream);
+
+/* out[i] = scale * table[tokens[i] - first], in fp32, rounded once.  A token that
+ * names no row (tokens[i] - first outside 0 .. rows - 1) gives zeros: padding,
+ * or another rank's part of a table cut by rows.
+ *   tokens       device, out->rows of them, int32 or int64 (token_bytes 4 or 8)
+ * out may not overlap the others.  Errors: as for zero_checkpoint_store. */
+int zero_embedding_lookup(const zero_matrix* table, const void* tokens, int32_t token_bytes, int64_t first,
+                          float scale, const zero_matrix* out, void* stream);
+
+/* The table's gradient:
+ *   dtable[r] = scale * (sum of dy[i] over the i with tokens[i] - first == r)
+ * added to what is there when accumulate is 1 (rows without a token are not
+ * touched then, and are zeros otherwise).  Tokens are sorted, each row's sum is
+ * taken in fp32 in an order fixed by how often it is named, and rounded once.
+ *   dy           one row for each token, at most 2^30
+ *   dtable       at most 2^30 rows
+ *   work         device, zero_embedding_grad_work_bytes() bytes, 16-byte aligned,
+ *                as for zero_weight_grad
+ * Nothing written may overlap anything else.
+ * Errors: as for zero_checkpoint_store. */
+int64_t zero_embedding_grad_work_bytes(int64_t tokens, int64_t rows, int64_t cols);
+int zero_embedding_grad(const zero_matrix* dy, const void* tokens, int32_t token_bytes, int64_t first, float scale,
+                        const zero_matrix* dtable, int32_t accumulate, void* work, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Kernel timing (profiling aid)                                            */
 /* ------------------------------------------------------------------------ */
 
 /* Per calling thread.  While enabled (enable != 0), zero_shard_step,
  * zero_owner_step, zero_pack_bucket, zero_reduce_to_owner, zero_grad_sumsq,
- * zero_adamw_step and zero_states_convert time their kernels with a pair of
+ * zero_adamw_step, zero_states_convert and the calls on checkpoints and
+ * embeddings time their kernels with a pair of
  * HIP events that the launch itself records at the
  * start of their first kernel and at the end of their last (for
  * zero_shard_step: the fused pass, or the check and update passes in place;
  * for zero_owner_step: the pass, without the one-thread flag hand-over).
- * zero_grad_sumsq, zero_adamw_step and zero_states_convert are not timed on a
- * stream that is being captured.
+ * Those from zero_grad_sumsq on are not timed on a stream that is being
+ * captured.
  * The pairs go into a ring of 4096 per thread, so calls can be timed back to
  * back without waiting on the events; enabling or disabling clears it.
  * zero_last_kernel_ms waits for the most recent pair's end event and returns
@@ -637,7 +764,7 @@ int zero_last_hip_error(void);         /* hipError_t of the last ZERO_ERR_HIP */
 
 /* sizeof of the ABI structs, for binding checks: 0 layout_info, 1 segment,
  * 2 shard_state, 3 adam_hparams, 4 loss_scaler, 5 arena_plan, 6 tensor,
- * 7 step_control; -1 otherwise. */
+ * 7 step_control, 8 matrix, 9 checkpoint; -1 otherwise. */
 int64_t zero_abi_struct_size(int32_t which);
 
 /* Architecture of the current device as a number (gfx950 -> 950) and its

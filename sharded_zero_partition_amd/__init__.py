@@ -11,7 +11,8 @@ generators; `build` compiles the library.
 
 __all__ = ["partition_layout", "Layout", "ShardState", "shard_step", "PreparedStep", "AdamHParams",
            "LossScaler", "ZeroError", "version", "device_info", "set_kernel_timing",
-           "last_kernel_ms", "kernel_times", "carve_arena", "ArenaPlan", "TensorSet", "StepControl"]
+           "last_kernel_ms", "kernel_times", "carve_arena", "ArenaPlan", "TensorSet", "StepControl",
+           "Checkpoint", "activation", "activation_grad", "weight_grad", "embedding_lookup", "embedding_grad"]
 
 
 def __getattr__(name):

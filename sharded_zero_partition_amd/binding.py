@@ -21,6 +21,10 @@ Names follow the C ABI in include/zero_partition.h:
   StepControl(...), StepControl.begin(...)   (zero_step_control, zero_step_begin)
   TensorSet.adamw_step(...)            (zero_adamw_step)
   TensorSet.states_from(...)           (zero_states_convert)
+  Checkpoint(...), .store, .load       (zero_checkpoint, zero_checkpoint_store, zero_checkpoint_load)
+  activation(...), activation_grad(...)   (zero_activation, zero_activation_grad)
+  weight_grad(...)                     (zero_weight_grad)
+  embedding_lookup(...), embedding_grad(...)   (zero_embedding_lookup, zero_embedding_grad)
   set_kernel_timing, last_kernel_ms, kernel_times   (kernel timing)
 """
 
@@ -127,8 +131,18 @@ class StepControlC(ctypes.Structure):
                 ("group", (ctypes.c_float * 8) * MAX_GROUPS)]
 
 
+class MatrixC(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("stride", ctypes.c_int64), ("type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class CheckpointC(ctypes.Structure):
+    _fields_ = [("code", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64)]
+
+
 ABI_STRUCTS = [LayoutInfo, Segment, ShardStateC, AdamHParams, LossScaler, ArenaPlan, TensorC,
-               StepControlC]
+               StepControlC, MatrixC, CheckpointC]
 
 # exported symbol -> (restype, argtypes)
 _P = ctypes.c_void_p
@@ -159,6 +173,16 @@ SIGNATURES = {
     "zero_step_begin": (ctypes.c_int, [_P, _P, _I32, ctypes.c_float, _I32, _P, _P]),
     "zero_adamw_step": (ctypes.c_int, [_P, _P, _I32, _P]),
     "zero_states_convert": (ctypes.c_int, [_P, _P, _P]),
+    "zero_checkpoint_bytes": (ctypes.c_int, [_I64, _I64, _P, _P]),
+    "zero_checkpoint_store": (ctypes.c_int, [_P, _P, _P]),
+    "zero_checkpoint_load": (ctypes.c_int, [_P, _P, _P]),
+    "zero_activation": (ctypes.c_int, [_I32, _P, _P, _P, _P, _P, _P, _P]),
+    "zero_activation_grad": (ctypes.c_int, [_I32, _P, _P, _P, _P, _P, _P]),
+    "zero_weight_grad_work_bytes": (ctypes.c_int64, [_I64, _I64, _I64, _I32]),
+    "zero_weight_grad": (ctypes.c_int, [_P, _P, _P, _I32, _P, _I32, _P, _P]),
+    "zero_embedding_lookup": (ctypes.c_int, [_P, _P, _I32, _I64, ctypes.c_float, _P, _P]),
+    "zero_embedding_grad_work_bytes": (ctypes.c_int64, [_I64, _I64, _I64]),
+    "zero_embedding_grad": (ctypes.c_int, [_P, _P, _I32, _I64, ctypes.c_float, _P, _I32, _P, _P]),
     "zero_set_kernel_timing": (ctypes.c_int, [_I32]),
     "zero_last_kernel_ms": (ctypes.c_int, [_P]),
     "zero_kernel_times": (ctypes.c_int, [_P, _I64, _P]),
@@ -767,6 +791,188 @@ class TensorSet:
         to 8 bits or back."""
         _check(lib.zero_states_convert(self._h, source._h, _raw_stream(stream, self._dev)))
         self._wrote("m", "v")
+
+
+# ---------------------------------------------------------------------------
+# activation checkpoints in 8 bits, and the gradients made from them
+# ---------------------------------------------------------------------------
+
+def _matrix(t, what: str, dev: int) -> MatrixC:
+    """A tensor as a matrix: its last dimension's values neighbours, the others
+    its rows, equally far apart."""
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is not on cuda:{dev}, the current device")
+    kind = _GRAD_DTYPES.get(t.dtype)
+    if kind is None:
+        raise ValueError(f"{what}: dtype {t.dtype} is not supported")
+    if t.dim() != 2:
+        if t.dim() == 0:
+            raise ValueError(f"{what} must have a last dimension")
+        try:
+            t = t.view(t.numel() // t.shape[-1] if t.shape[-1] else 0, t.shape[-1])
+        except RuntimeError:
+            raise ValueError(f"{what}: its rows are not equally far apart") from None
+    rows, cols = t.shape
+    stride, step = t.stride()
+    if step != 1 and cols > 1 and rows > 0:
+        raise ValueError(f"{what}: the values of a row must be neighbours")
+    return MatrixC(t.data_ptr(), rows, cols, stride, kind, 0)
+
+
+def _wrote(*tensors):
+    """Raise autograd's version counters of what a call wrote."""
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+
+
+def _workspace(nbytes: int, like, stream):
+    """Memory of one call alone, from the pool of its stream: calls on other
+    streams and captured graphs get their own."""
+    if not nbytes:
+        return None
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+
+
+def _tokens(t, n: int, dev: int):
+    """(address, bytes of one) of a contiguous tensor of n tokens."""
+    if t.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"tokens: dtype {t.dtype} is not supported")
+    if t.get_device() != dev:
+        raise ValueError(f"tokens are not on cuda:{dev}, the current device")
+    if t.numel() != n:
+        raise ValueError(f"{t.numel()} tokens for {n} rows")
+    if not t.is_contiguous():
+        raise ValueError("tokens must be contiguous")
+    return t.data_ptr(), t.element_size()
+
+
+class Checkpoint:
+    """A matrix of activations kept in 8 bits (a zero_checkpoint, MXFP8): `code`
+    holds rows of e4m3 codes, padded to whole blocks of 32, and `scale` a byte for
+    each block.  Made empty from its sizes, or from tensors that hold one
+    (`code` [rows, 32 ceil(cols / 32)], `scale` [rows, ceil(cols / 32)], uint8 or
+    the float8 types, both contiguous, `code` 16-byte aligned; rows of a larger
+    checkpoint are one)."""
+
+    def __init__(self, rows: int = None, cols: int = None, code=None, scale=None, device=None):
+        if cols is None or cols < 0 or (code is None) != (scale is None) or (code is None) == (rows is None):
+            raise ValueError("a checkpoint takes rows and cols, or code, scale and cols")
+        blocks = -(-int(cols) // STATE_BLOCK)
+        if code is None:
+            if rows < 0:
+                raise ValueError("rows must not be negative")
+            dev = torch.device("cuda", _current_device()) if device is None else torch.device(device)
+            code = torch.empty(int(rows), STATE_BLOCK * blocks, dtype=torch.uint8, device=dev)
+            scale = torch.empty(int(rows), blocks, dtype=torch.uint8, device=dev)
+        if not code.is_cuda or code.device != scale.device:
+            raise ValueError("code and scale live on one GPU")
+        if code.dtype not in (torch.uint8, torch.float8_e4m3fn) or scale.dtype not in _SCALE_DTYPES:
+            raise ValueError(f"code and scale: dtypes {code.dtype} and {scale.dtype} are not supported")
+        if code.dim() != 2 or tuple(code.shape) != (code.shape[0], STATE_BLOCK * blocks) \
+                or tuple(scale.shape) != (code.shape[0], blocks):
+            raise ValueError(f"code and scale must have rows of {STATE_BLOCK * blocks} and {blocks}")
+        if not (code.is_contiguous() and scale.is_contiguous()):
+            raise ValueError("code and scale must be contiguous")
+        self.rows, self.cols, self.code, self.scale = code.shape[0], int(cols), code, scale
+        self.device_index = code.device.index
+        self._c = CheckpointC(code.data_ptr(), scale.data_ptr(), self.rows, self.cols)
+
+    def _on(self, dev: int):
+        if self.device_index != dev:
+            raise ValueError(f"a checkpoint is on cuda:{self.device_index}, the current device is another")
+        return _ref(self._c)
+
+    def store(self, x, stream=None):
+        """zero_checkpoint_store: keep x (fp16, bf16 or fp32)."""
+        dev = _current_device()
+        _check(lib.zero_checkpoint_store(_ref(_matrix(x, "x", dev)), self._on(dev), _raw_stream(stream, dev)))
+        _wrote(self.code, self.scale)
+
+    def load(self, out, stream=None):
+        """zero_checkpoint_load: read it back into `out`."""
+        dev = _current_device()
+        _check(lib.zero_checkpoint_load(self._on(dev), _ref(_matrix(out, "out", dev)), _raw_stream(stream, dev)))
+        _wrote(out)
+
+
+ACTIVATIONS = {"relu": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
+
+
+def _kind(name: str) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {name!r}: one of {', '.join(ACTIVATIONS)}")
+    return ACTIVATIONS[name]
+
+
+def activation(kind: str, x, out, checkpoint: Checkpoint = None, up=None, up_checkpoint: Checkpoint = None,
+               out_checkpoint: Checkpoint = None, stream=None):
+    """zero_activation: out = act(x), or act(x) * up, with the checkpoints of x
+    and up that activation_grad reads, and of out for weight_grad of the layer
+    that comes next.  `kind`: "relu", "silu", "gelu" (erf) or "gelu_tanh".  out
+    may be x or up."""
+    dev = _current_device()
+    kept = [None if c is None else c._on(dev) for c in (checkpoint, up_checkpoint, out_checkpoint)]
+    _check(lib.zero_activation(_kind(kind), _ref(_matrix(x, "x", dev)), None if up is None else _ref(_matrix(up, "up", dev)),
+                               _ref(_matrix(out, "out", dev)), *kept, _raw_stream(stream, dev)))
+    _wrote(out, *(t for c in (checkpoint, up_checkpoint, out_checkpoint) if c is not None for t in (c.code, c.scale)))
+
+
+def activation_grad(kind: str, dy, checkpoint: Checkpoint, dx, up_checkpoint: Checkpoint = None, dup=None, stream=None):
+    """zero_activation_grad: the gradients of x (and up) from that of the
+    activation's result, x and up being read from their checkpoints.  dx or dup
+    may be dy."""
+    dev = _current_device()
+    _check(lib.zero_activation_grad(_kind(kind), _ref(_matrix(dy, "dy", dev)), checkpoint._on(dev),
+                                    None if up_checkpoint is None else up_checkpoint._on(dev),
+                                    _ref(_matrix(dx, "dx", dev)), None if dup is None else _ref(_matrix(dup, "dup", dev)),
+                                    _raw_stream(stream, dev)))
+    _wrote(dx, dup)
+
+
+def weight_grad(dy, checkpoint: Checkpoint, dw, bias=None, accumulate: bool = False, stream=None):
+    """zero_weight_grad: dw[n, k] = sum of dy[t, n] x[t, k] over the tokens t, x
+    being read from its checkpoint, and bias[n] = sum of dy[t, n]; accumulate=True
+    adds to what is there.  dw may be the transpose of a tensor (`w.grad.t()` for
+    a weight that is kept as inputs by outputs)."""
+    dev = _current_device()
+    m = _matrix(dy, "dy", dev)
+    if dw.dim() != 2 or tuple(dw.shape) != (m.cols, checkpoint.cols):
+        raise ValueError(f"dw must be {m.cols} by {checkpoint.cols}")
+    transposed = dw.stride(1) != 1 and dw.shape[1] > 1
+    if bias is not None and (bias.dtype != dw.dtype or bias.get_device() != dev or not bias.is_contiguous()
+                             or bias.numel() != m.cols):
+        raise ValueError(f"bias must be {m.cols} neighbouring values of dw's dtype on cuda:{dev}")
+    work = _workspace(lib.zero_weight_grad_work_bytes(m.rows, m.cols, checkpoint.cols, m.type), dw, stream)
+    _check(lib.zero_weight_grad(_ref(m), checkpoint._on(dev), _ref(_matrix(dw.t() if transposed else dw, "dw", dev)),
+                                transposed, None if bias is None else bias.data_ptr(), bool(accumulate),
+                                None if work is None else work.data_ptr(), _raw_stream(stream, dev)))
+    _wrote(dw, bias)
+
+
+def embedding_lookup(table, tokens, out, scale: float = 1.0, first: int = 0, stream=None):
+    """zero_embedding_lookup: out's rows are scale times the table's rows
+    tokens - first; zeros where that is no row (padding, or another rank's)."""
+    dev = _current_device()
+    m = _matrix(out, "out", dev)
+    at, size = _tokens(tokens, m.rows, dev)
+    _check(lib.zero_embedding_lookup(_ref(_matrix(table, "table", dev)), at, size, first, scale, _ref(m),
+                                     _raw_stream(stream, dev)))
+    _wrote(out)
+
+
+def embedding_grad(dy, tokens, dtable, scale: float = 1.0, first: int = 0, accumulate: bool = False, stream=None):
+    """zero_embedding_grad: row r of dtable is scale times the sum of dy's rows
+    whose token is first + r; accumulate=True adds that to what is there (other
+    rows stay as they are)."""
+    dev = _current_device()
+    m, d = _matrix(dy, "dy", dev), _matrix(dtable, "dtable", dev)
+    at, size = _tokens(tokens, m.rows, dev)
+    work = _workspace(lib.zero_embedding_grad_work_bytes(m.rows, d.rows, d.cols), dtable, stream)
+    _check(lib.zero_embedding_grad(_ref(m), at, size, first, scale, _ref(d), bool(accumulate),
+                                   None if work is None else work.data_ptr(), _raw_stream(stream, dev)))
+    _wrote(dtable)
 
 
 def version() -> int:

@@ -22,7 +22,8 @@ LIB = os.path.join(PKG, "libzero_partition.so")
 PROBE_LIB = os.path.join(PKG, "libzero_probe.so")
 
 SOURCES = ["layout.cpp", "capi.cpp", "pack.hip", "shard_step.hip", "reduce_owner.hip", "noalloc.hip",
-           "tensor_set.cpp", "tensor_step.hip", "grad_norm.hip"]
+           "tensor_set.cpp", "tensor_step.hip", "grad_norm.hip", "activations.cpp", "checkpoint.hip",
+           "weight_grad.hip", "embedding.hip"]
 PROBE_SOURCES = ["stream_probe.hip"]
 
 ARCH = "gfx950"

@@ -643,6 +643,8 @@ extern "C" int64_t zero_abi_struct_size(int32_t which) {
         case 5: return int64_t(sizeof(zero_arena_plan));
         case 6: return int64_t(sizeof(zero_tensor));
         case 7: return int64_t(sizeof(zero_step_control));
+        case 8: return int64_t(sizeof(zero_matrix));
+        case 9: return int64_t(sizeof(zero_checkpoint));
         default: return -1;
     }
 }

@@ -1,0 +1,559 @@
+// embedding.hip -- rows of a table by tokens, and the table's gradient (gfx950).
+//
+// The gradient adds up rows of dy that have the same token.  Atomic adds would
+// take an order of their own each time; here the tokens are sorted (stable, so a
+// row's summands come as the tokens do), the sorted list is cut into tiles of
+// equal length, and one wave sums a tile's rows of dy for 512 columns.  Tokens
+// are as uneven as text is (the most frequent one has several per cent), and
+// equal tiles make the waves' work equal.  A run of equal tokens inside a tile
+// is a finished row; one that crosses tiles leaves a partial sum for each, which
+// a last kernel adds in order.  Rows that no token names are filled with zeros by
+// the same launch that sums the tiles.
+#include <type_traits>
+
+#include "octets.hpp"
+#include "timed_launch.hpp"
+
+#pragma clang fp contract(off)
+
+namespace zp {
+namespace {
+
+constexpr int kThreads = 256;
+
+// ---------------------------------------------------------------------------
+// lookup
+// ---------------------------------------------------------------------------
+
+// Row of the table that token i names, or -1.
+template <typename I>
+__device__ __forceinline__ int64_t named_row(const void* tokens, int64_t i, int64_t first, int64_t rows) {
+    const uint64_t r = uint64_t(int64_t(((Global<const I>*)tokens)[i])) - uint64_t(first);
+    return r < uint64_t(rows) ? int64_t(r) : -1;
+}
+
+struct LookupArgs {
+    EmbedLaunch e;
+    Divisor per_row;   // octets of a row
+    int64_t octets;
+};
+
+template <int DI, int DO, typename I>
+__global__ __launch_bounds__(kThreads) void lookup_kernel(const LookupArgs a) {
+    const int64_t base = int64_t(blockIdx.x) * (kThreads * kRowOctets);
+    int64_t row;
+    uint32_t rest;
+    divide(base, a.per_row, &row, &rest);
+    int64_t i[kRowOctets], col[kRowOctets], left[kRowOctets], r[kRowOctets];
+#pragma unroll
+    for (int u = 0; u < kRowOctets; ++u) {
+        const uint32_t k = threadIdx.x + u * kThreads;
+        const uint32_t q = divide(rest + k, a.per_row);
+        i[u] = row + q;
+        col[u] = int64_t(rest + k - q * a.per_row.g) * kOctet;
+        left[u] = base + k < a.octets ? a.e.cols - col[u] : 0;
+        r[u] = left[u] > 0 ? named_row<I>(a.e.tokens, i[u], a.e.first, a.e.rows) : -1;
+    }
+    Octet<DI> x[kRowOctets];
+#pragma unroll
+    for (int u = 0; u < kRowOctets; ++u)
+        x[u] = load_octet<DI>(place<DI>(a.e.in, r[u], a.e.s_in, col[u]), r[u] < 0 ? 0 : left[u]);
+#pragma unroll
+    for (int u = 0; u < kRowOctets; ++u) {
+        Octet<DO> y;
+#pragma unroll
+        for (int k = 0; k < kOctet; ++k) y.set(k, r[u] < 0 ? 0.0f : x[u].get(k) * a.e.scale);
+        store_octet<DO>(place<DO>(a.e.out, i[u], a.e.s_out, col[u]), left[u], y);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// sorting: (row, place) pairs, rows ascending, places ascending in a row; tokens
+// that name no row count as row `rows` and come last
+// ---------------------------------------------------------------------------
+
+struct SortArgs {
+    const void* tokens;
+    int64_t n, first, rows;
+    uint32_t* key;      // sorted rows
+    uint32_t* order;    // and their places
+};
+
+template <typename I>
+__device__ __forceinline__ uint32_t key_of(const SortArgs& a, int64_t i) {
+    const int64_t r = named_row<I>(a.tokens, i, a.first, a.rows);
+    return r < 0 ? uint32_t(a.rows) : uint32_t(r);
+}
+
+// Few tokens: each one's place is how many keys are smaller, or equal and before
+// it.  8 threads count for a token, 32 tokens a block; n^2 comparisons, but one
+// launch (8192 tokens: measured below at its launch), where digit by digit takes four.
+constexpr int64_t kRankMost = 8192;
+constexpr int kRankTokens = kThreads / 8;
+template <typename I>
+__global__ __launch_bounds__(kThreads) void rank_kernel(const SortArgs a) {
+    __shared__ uint32_t keys[kRankMost];
+    const int n = int(a.n), tid = int(threadIdx.x);
+    for (int j = tid; j < n; j += kThreads) keys[j] = key_of<I>(a, j);
+    __syncthreads();
+    const int i = int(blockIdx.x) * kRankTokens + (tid >> 3);
+    const int part = tid & 7;
+    const uint32_t mine = i < n ? keys[i] : 0;
+    int rank = 0;
+    for (int j = part; j < n; j += 8) {
+        const uint32_t k = keys[j];
+        rank += (k < mine || (k == mine && j < i)) ? 1 : 0;
+    }
+    rank += __shfl_xor(rank, 1);
+    rank += __shfl_xor(rank, 2);
+    rank += __shfl_xor(rank, 4);
+    if (part == 0 && i < n) {
+        a.key[rank] = mine;
+        a.order[rank] = uint32_t(i);
+    }
+}
+
+// Many: digits of at most 9 bits, lowest first.  A block counts the digits of its
+// part of the list; then each block, knowing all counts, puts its elements where
+// the lower digits, the earlier blocks, its earlier waves and its wave's earlier
+// elements leave off.
+constexpr int kDigitBits = 9;
+constexpr int kMaxDigits = 1 << kDigitBits;
+constexpr int kSortWaves = kThreads / 64;
+constexpr int64_t kMaxSortBlocks = 256;
+struct DigitArgs {
+    SortArgs s;
+    const uint32_t* in_key;     // NULL in the first pass: from the tokens
+    const uint32_t* in_order;
+    uint32_t* count;            // blocks x digits
+    int64_t part;               // elements of a block, a multiple of kThreads
+    int32_t blocks, shift, digits;   // digits: a power of two
+};
+
+template <typename I>
+__device__ __forceinline__ uint32_t digit_key(const DigitArgs& a, int64_t i) {
+    return a.in_key ? ((Global<const uint32_t>*)a.in_key)[i] : key_of<I>(a.s, i);
+}
+
+template <typename I>
+__global__ __launch_bounds__(kThreads) void digit_count_kernel(const DigitArgs a) {
+    __shared__ uint32_t count[kMaxDigits];
+    for (int d = threadIdx.x; d < a.digits; d += kThreads) count[d] = 0;
+    __syncthreads();
+    const int64_t lo = int64_t(blockIdx.x) * a.part, hi = lo + a.part < a.s.n ? lo + a.part : a.s.n;
+    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads)
+        atomicAdd(&count[(digit_key<I>(a, i) >> a.shift) & (a.digits - 1)], 1u);
+    __syncthreads();
+    for (int d = threadIdx.x; d < a.digits; d += kThreads) a.count[int64_t(blockIdx.x) * a.digits + d] = count[d];
+}
+
+template <typename I>
+__global__ __launch_bounds__(kThreads) void digit_move_kernel(const DigitArgs a) {
+    __shared__ uint32_t next[kSortWaves][kMaxDigits];   // where a wave's next element with the digit goes
+    __shared__ uint32_t total[kMaxDigits];
+    const int tid = int(threadIdx.x), wave = tid >> 6, lane = tid & 63;
+    const int64_t quarter = a.part / kSortWaves;
+    const int64_t lo = int64_t(blockIdx.x) * a.part + wave * quarter;
+    const int64_t hi = lo + quarter < a.s.n ? lo + quarter : a.s.n;
+    for (int d = tid; d < a.digits; d += kThreads) {
+        uint32_t before = 0, all = 0;
+        for (int b = 0; b < a.blocks; ++b) {
+            const uint32_t c = a.count[int64_t(b) * a.digits + d];
+            before += b < int(blockIdx.x) ? c : 0;
+            all += c;
+        }
+        total[d] = all;
+#pragma unroll
+        for (int w = 0; w < kSortWaves; ++w) next[w][d] = w == 0 ? before : 0;
+    }
+    __syncthreads();
+    // each wave's counts, for the waves after it
+    for (int64_t i = lo + lane; i < hi; i += 64) {
+        const uint32_t d = (digit_key<I>(a, i) >> a.shift) & (a.digits - 1);
+        for (int w = wave + 1; w < kSortWaves; ++w) atomicAdd(&next[w][d], 1u);
+    }
+    // sums of the lower digits, by one wave: 64 digits at a time
+    __syncthreads();
+    if (wave == 0) {
+        uint32_t below = 0;
+        for (int d0 = 0; d0 < a.digits; d0 += 64) {
+            const int d = d0 + lane;
+            const uint32_t own = d < a.digits ? total[d] : 0;
+            uint32_t x = own;
+#pragma unroll
+            for (int h = 1; h < 64; h *= 2) {
+                const uint32_t y = __shfl_up(x, h);
+                if (lane >= h) x += y;
+            }
+            if (d < a.digits) total[d] = below + x - own;
+            below += __shfl(x, 63);
+        }
+    }
+    __syncthreads();
+    for (int d = tid; d < a.digits; d += kThreads) {
+        const uint32_t first = total[d] + next[0][d];
+#pragma unroll
+        for (int w = 1; w < kSortWaves; ++w) next[w][d] += first;
+        next[0][d] = first;
+    }
+    __syncthreads();
+    for (int64_t i0 = lo; i0 < hi; i0 += 64) {   // wave-uniform bounds
+        const int64_t i = i0 + lane;
+        const bool there = i < hi;
+        const uint32_t key = there ? digit_key<I>(a, i) : 0;
+        const uint32_t d = (key >> a.shift) & (a.digits - 1);
+        // lanes with the same digit
+        uint64_t same = __ballot(there);
+        for (int bit = 1; bit < a.digits; bit *= 2) {
+            const uint64_t with = __ballot((d & bit) != 0);
+            same &= (d & bit) ? with : ~with;
+        }
+        uint32_t to = 0;
+        const int before = __popcll(same & ((uint64_t(1) << lane) - 1));
+        if (there) to = next[wave][d] + before;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (there && (same >> lane) == 1) next[wave][d] += before + 1;   // the last of them
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (there) {
+            a.s.key[to] = key;
+            a.s.order[to] = a.in_order ? a.in_order[i] : uint32_t(i);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// sums
+// ---------------------------------------------------------------------------
+
+constexpr int kChunk = 64 * kOctet;   // columns of a wave
+constexpr int kAhead = 8;             // rows of dy loaded at once
+constexpr int kZeroRows = 16;         // table rows that a block looks through for unnamed ones
+
+struct SumArgs {
+    EmbedLaunch e;
+    const uint32_t* key;      // n sorted rows
+    const uint32_t* order;
+    float* part;              // [tiles][2][chunks * kChunk]: of the run that enters a tile, and of the one that leaves it
+    int64_t tiles;
+    int32_t tile;             // length: a multiple of 64
+    int32_t chunks;
+    int64_t tile_blocks;      // blocks that sum tiles; those after them fill rows with zeros
+};
+
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return uint32_t(__builtin_amdgcn_readfirstlane(int(x))); }
+
+template <int DO>
+__device__ __forceinline__ void finish_row(const EmbedLaunch& e, uint32_t row, int64_t col, int64_t left,
+                                           const float acc[kOctet]) {
+    if (left <= 0) return;
+    char* at = place<DO>(e.out, row, e.s_out, col);
+    Octet<DO> y;
+    if (e.accumulate) {
+        y = load_octet<DO>(at, left);
+#pragma unroll
+        for (int k = 0; k < kOctet; ++k) y.set(k, y.get(k) + e.scale * acc[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < kOctet; ++k) y.set(k, e.scale * acc[k]);
+    }
+    store_octet<DO>(at, left, y);
+}
+
+// The 512 columns of tile t of the sorted list.
+template <int DI, int DO>
+__device__ __forceinline__ void sum_tile(const SumArgs& a, int64_t t, int chunk) {
+    const int lane = int(threadIdx.x) & 63;
+    const int64_t col = int64_t(chunk) * kChunk + lane * kOctet, left = a.e.cols - col;
+    const int64_t lo = t * a.tile, hi = lo + a.tile < a.e.n ? lo + a.tile : a.e.n;
+    const uint32_t none = uint32_t(a.e.rows);
+    float acc[kOctet] = {};
+    uint32_t run = uniform(a.key[lo]);   // the row that acc is of
+    bool enters = lo > 0 && uniform(a.key[lo > 0 ? lo - 1 : 0]) == run;
+    float* mine = a.part + t * 2 * a.chunks * kChunk + col;
+
+    const auto flush = [&](bool leaves) {
+        if (run == none) return;
+        if (enters || leaves) {
+            float* at = mine + (enters ? 0 : a.chunks * kChunk);
+            ((Global<f32x4>*)at)[0] = f32x4{acc[0], acc[1], acc[2], acc[3]};
+            ((Global<f32x4>*)at)[1] = f32x4{acc[4], acc[5], acc[6], acc[7]};
+        } else {
+            finish_row<DO>(a.e, run, col, left, acc);
+        }
+    };
+    for (int64_t p0 = lo; p0 < hi; p0 += 64) {
+        const int64_t p = p0 + lane;
+        const uint32_t keys = p < hi ? a.key[p] : none, places = p < hi ? a.order[p] : 0;
+        const int m = int(hi - p0 < 64 ? hi - p0 : 64);
+        for (int j0 = 0; j0 < m; j0 += kAhead) {
+            Octet<DI> x[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                x[j].zero();
+                const uint32_t r = uint32_t(__builtin_amdgcn_readlane(int(keys), j0 + j));   // none behind hi
+                const uint32_t i = uint32_t(__builtin_amdgcn_readlane(int(places), j0 + j));
+                if (r != none) x[j] = load_octet<DI>(place<DI>(a.e.in, i, a.e.s_in, col), left);
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                if (j0 + j >= m) break;
+                const uint32_t r = uint32_t(__builtin_amdgcn_readlane(int(keys), j0 + j));
+                if (r != run) {
+                    flush(false);
+                    run = r;
+                    enters = false;
+#pragma unroll
+                    for (int k = 0; k < kOctet; ++k) acc[k] = 0.0f;
+                }
+#pragma unroll
+                for (int k = 0; k < kOctet; ++k) acc[k] += x[j].get(k);
+            }
+        }
+    }
+    flush(hi < a.e.n && uniform(a.key[hi < a.e.n ? hi : 0]) == run);
+}
+
+// First place of the sorted list whose row is not below r: 64 probes at a time.
+__device__ __forceinline__ int64_t lower_bound(const uint32_t* key, int64_t n, uint32_t r) {
+    const int lane = int(threadIdx.x) & 63;
+    int64_t lo = 0, len = n;   // the answer is in [lo, lo + len]
+    while (len > 0) {
+        const int64_t step = (len + 63) / 64;
+        const int64_t p = lo + step * lane;
+        const bool below = step * lane < len && key[p] < r;
+        const int c = __popcll(__ballot(below));   // probes 0 .. c - 1 are below
+        if (c == 0) return lo;
+        const int64_t end = lo + len;
+        lo += step * (c - 1) + 1;
+        len = step - 1 < end - lo ? step - 1 : end - lo;
+    }
+    return lo;
+}
+
+template <int DI, int DO>
+__global__ __launch_bounds__(kThreads) void tile_sum_kernel(const SumArgs a) {
+    const int wave = int(threadIdx.x) >> 6;
+    if (int64_t(blockIdx.x) < a.tile_blocks) {
+        const int64_t w = int64_t(blockIdx.x) * (kThreads / 64) + wave;
+        const int64_t t = w / a.chunks;
+        if (t < a.tiles) sum_tile<DI, DO>(a, t, int(w - t * a.chunks));
+        return;
+    }
+    // zeros into the unnamed ones of kZeroRows rows
+    __shared__ uint32_t named;
+    const int64_t r0 = (int64_t(blockIdx.x) - a.tile_blocks) * kZeroRows;
+    const int64_t r1 = r0 + kZeroRows < a.e.rows ? r0 + kZeroRows : a.e.rows;
+    if (threadIdx.x == 0) named = 0;
+    __syncthreads();
+    const int64_t begin = lower_bound(a.key, a.e.n, uint32_t(r0));
+    for (int64_t p = begin + threadIdx.x; p < a.e.n; p += kThreads) {
+        const uint32_t k = a.key[p];
+        if (k >= r1) break;
+        atomicOr(&named, 1u << (k - uint32_t(r0)));
+    }
+    __syncthreads();
+    const uint32_t there = uniform(named);
+    Octet<DO> zero;
+    zero.zero();
+    for (int64_t r = r0; r < r1; ++r) {
+        if (there >> (r - r0) & 1) continue;
+        for (int64_t c = int64_t(threadIdx.x) * kOctet; c < a.e.cols; c += kThreads * kOctet)
+            store_octet<DO>(place<DO>(a.e.out, r, a.e.s_out, c), a.e.cols - c, zero);
+    }
+}
+
+// Adds up the partial sums of a run that crosses tiles: a wave for each tile that
+// such a run leaves from where it began, and 512 columns.
+template <int DO>
+__global__ __launch_bounds__(kThreads) void join_kernel(const SumArgs a) {
+    const int lane = int(threadIdx.x) & 63;
+    const int64_t w = int64_t(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6);
+    const int64_t t = w / a.chunks;
+    if (t + 1 >= a.tiles) return;
+    const int64_t end = (t + 1) * a.tile;   // below n
+    const uint32_t run = uniform(a.key[end]);
+    if (run == uint32_t(a.e.rows) || uniform(a.key[end - 1]) != run) return;
+    const int64_t lo = t * a.tile;
+    if (lo > 0 && uniform(a.key[lo]) == run && uniform(a.key[lo - 1]) == run) return;   // began earlier
+    // the tiles after t that the run enters
+    int64_t last = t + 1;
+    for (;;) {
+        const int64_t p = (last + 1 + lane) * a.tile;
+        const uint64_t on = __ballot(p < a.e.n && a.key[p < a.e.n ? p : 0] == run && a.key[p < a.e.n ? p - 1 : 0] == run);
+        const int c = on == ~uint64_t(0) ? 64 : __ffsll((unsigned long long)~on) - 1;
+        last += c;
+        if (c < 64) break;
+    }
+    const int64_t col = int64_t(w - t * a.chunks) * kChunk + lane * kOctet;
+    const int64_t half = int64_t(a.chunks) * kChunk;
+    float acc[kOctet];
+    const auto load = [&](int64_t tile, bool leaving, f32x4 v[2]) {
+        const float* p = a.part + (tile * 2 + (leaving ? 1 : 0)) * half + col;
+        v[0] = ((Global<const f32x4>*)p)[0];
+        v[1] = ((Global<const f32x4>*)p)[1];
+    };
+    f32x4 v[2];
+    load(t, true, v);   // the run began in t, at its first place or after it
+#pragma unroll
+    for (int k = 0; k < kOctet; ++k) acc[k] = v[k >> 2][k & 3];
+    for (int64_t u = t + 1; u <= last; u += kAhead) {
+        f32x4 x[kAhead][2];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) load(u + j <= last ? u + j : last, false, x[j]);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (u + j <= last)
+#pragma unroll
+                for (int k = 0; k < kOctet; ++k) acc[k] += x[j][k >> 2][k & 3];
+    }
+    finish_row<DO>(a.e, run, col, a.e.cols - col, acc);
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+
+// Tiles long enough that the most frequent token has few of them, short enough
+// that all CUs have some.
+int tile_length(int64_t n) {
+    int t = 64;
+    while (t < 512 && n / t > 2048) t *= 2;
+    return t;
+}
+
+struct Plan {
+    int64_t tiles, part;        // part: elements of a sorting block
+    int32_t tile, chunks, blocks, passes, digits;
+    int64_t lists;              // bytes of a list of n numbers
+    int64_t off_key[2], off_order[2], off_count, off_part, bytes;
+};
+Plan plan_for(int64_t n, int64_t rows, int64_t cols) {
+    Plan p = {};
+    p.tile = tile_length(n);
+    p.tiles = (n + p.tile - 1) / p.tile;
+    p.chunks = int32_t((cols + kChunk - 1) / kChunk);
+    int bits = 1;   // rows is a key too
+    while ((int64_t(1) << bits) <= rows) ++bits;
+    p.passes = n <= kRankMost ? 0 : (bits + kDigitBits - 1) / kDigitBits;
+    p.digits = p.passes ? 1 << ((bits + p.passes - 1) / p.passes) : 0;
+    p.part = (n + kMaxSortBlocks - 1) / kMaxSortBlocks;
+    p.part = p.part > 1024 ? (p.part + 1023) / 1024 * 1024 : 1024;
+    p.blocks = int32_t((n + p.part - 1) / p.part);
+    const auto take = [&](int64_t bytes) {
+        const int64_t at = p.bytes;
+        p.bytes += (bytes + 255) / 256 * 256;
+        return at;
+    };
+    for (int i = 0; i < (p.passes > 1 ? 2 : 1); ++i) {
+        p.off_key[i] = take(4 * n);
+        p.off_order[i] = take(4 * n);
+    }
+    if (p.passes) p.off_count = take(4 * int64_t(p.blocks) * p.digits);
+    p.off_part = take(p.tiles > 1 ? p.tiles * 2 * p.chunks * kChunk * 4 : 0);
+    return p;
+}
+
+template <int DI, int DO>
+void run_sum(const SumArgs& a, int64_t blocks, hipStream_t s, const KernelEvents& ev) {
+    const bool join = a.tiles > 1;
+    KernelEvents one = {ev.start, join ? nullptr : ev.stop};
+    launch(tile_sum_kernel<DI, DO>, dim3(uint32_t(blocks)), kThreads, s, one, a);
+    if (!join) return;
+    one = {nullptr, ev.stop};
+    const int64_t waves = (a.tiles - 1) * a.chunks;
+    launch(join_kernel<DO>, dim3(uint32_t((waves + 3) / 4)), kThreads, s, one, a);
+}
+
+template <int DI, int DO>
+void run_lookup(const LookupArgs& a, hipStream_t s, const KernelEvents& ev) {
+    constexpr int64_t per = kThreads * kRowOctets;
+    const dim3 grid(uint32_t((a.octets + per - 1) / per));
+    if (a.e.token_bytes == 8) launch(lookup_kernel<DI, DO, int64_t>, grid, kThreads, s, ev, a);
+    else launch(lookup_kernel<DI, DO, int32_t>, grid, kThreads, s, ev, a);
+}
+
+// f<in type, out type>() for the dtype numbers.
+template <typename F>
+void for_types(int32_t in, int32_t out, const F& f) {
+    const auto with_in = [&](auto di) {
+        if (out == ZERO_DTYPE_FP16) f(di, std::integral_constant<int, ZERO_DTYPE_FP16>{});
+        else if (out == ZERO_DTYPE_BF16) f(di, std::integral_constant<int, ZERO_DTYPE_BF16>{});
+        else f(di, std::integral_constant<int, ZERO_DTYPE_FP32>{});
+    };
+    if (in == ZERO_DTYPE_FP16) with_in(std::integral_constant<int, ZERO_DTYPE_FP16>{});
+    else if (in == ZERO_DTYPE_BF16) with_in(std::integral_constant<int, ZERO_DTYPE_BF16>{});
+    else with_in(std::integral_constant<int, ZERO_DTYPE_FP32>{});
+}
+
+}  // namespace
+
+hipError_t launch_lookup(const EmbedLaunch& e, hipStream_t s, const KernelEvents& ev) {
+    LookupArgs a;
+    a.e = e;
+    const int64_t per_row = (e.cols + kOctet - 1) / kOctet;
+    a.per_row = divisor(uint32_t(per_row < 2 ? 2 : per_row));   // a second octet of nothing where there is one
+    a.octets = e.n * a.per_row.g;
+    for_types(e.type, e.out_type, [&](auto di, auto d_o) { run_lookup<decltype(di)::value, decltype(d_o)::value>(a, s, ev); });
+    return hipGetLastError();
+}
+
+int64_t embedding_work(int64_t n, int64_t rows, int64_t cols) { return plan_for(n, rows, cols).bytes; }
+
+bool embedding_fits(int64_t n, int64_t rows, int64_t cols) {
+    const Plan p = plan_for(n, rows, cols);
+    return (p.tiles * p.chunks + 3) / 4 + (rows + kZeroRows - 1) / kZeroRows < int64_t(1) << 24;
+}
+
+hipError_t launch_embedding_grad(const EmbedLaunch& e, hipStream_t s, const KernelEvents& ev) {
+    const Plan p = plan_for(e.n, e.rows, e.cols);
+    char* work = static_cast<char*>(e.work);
+    const auto list = [&](int64_t off) { return reinterpret_cast<uint32_t*>(work + off); };
+    SumArgs a = {};
+    a.e = e;
+    a.tile = p.tile;
+    a.tiles = p.tiles;
+    a.chunks = p.chunks;
+    a.part = reinterpret_cast<float*>(work + p.off_part);
+    const int last = p.passes ? (p.passes - 1) & 1 : 0;   // the lists that the last pass writes
+    a.key = list(p.off_key[last]);
+    a.order = list(p.off_order[last]);
+
+    SortArgs so = {e.tokens, e.n, e.first, e.rows, list(p.off_key[0]), list(p.off_order[0])};
+    KernelEvents one = {ev.start, nullptr};
+    const bool wide = e.token_bytes == 8;
+    if (p.passes == 0 && e.n > 0) {
+        const dim3 grid(uint32_t((e.n + kRankTokens - 1) / kRankTokens));
+        if (wide) launch(rank_kernel<int64_t>, grid, kThreads, s, one, so);
+        else launch(rank_kernel<int32_t>, grid, kThreads, s, one, so);
+        one.start = nullptr;
+    }
+    for (int k = 0; k < p.passes; ++k) {
+        DigitArgs d = {};
+        d.s = so;
+        d.s.key = list(p.off_key[k & 1]);
+        d.s.order = list(p.off_order[k & 1]);
+        d.in_key = k ? list(p.off_key[(k - 1) & 1]) : nullptr;
+        d.in_order = k ? list(p.off_order[(k - 1) & 1]) : nullptr;
+        d.count = list(p.off_count);
+        d.part = p.part;
+        d.blocks = p.blocks;
+        d.digits = p.digits;
+        d.shift = k * __builtin_ctz(uint32_t(p.digits));
+        const KernelEvents none;
+        if (wide) {
+            launch(digit_count_kernel<int64_t>, dim3(p.blocks), kThreads, s, one, d);
+            launch(digit_move_kernel<int64_t>, dim3(p.blocks), kThreads, s, none, d);
+        } else {
+            launch(digit_count_kernel<int32_t>, dim3(p.blocks), kThreads, s, one, d);
+            launch(digit_move_kernel<int32_t>, dim3(p.blocks), kThreads, s, none, d);
+        }
+        one.start = nullptr;
+    }
+    a.tile_blocks = (p.tiles * p.chunks + 3) / 4;
+    const int64_t zero_blocks = e.accumulate ? 0 : (e.rows + kZeroRows - 1) / kZeroRows;
+    for_types(e.type, e.out_type,
+              [&](auto di, auto d_o) { run_sum<decltype(di)::value, decltype(d_o)::value>(a, a.tile_blocks + zero_blocks, s, {one.start, ev.stop}); });
+    return hipGetLastError();
+}
+
+}  // namespace zp

@@ -1,0 +1,107 @@
+// octets.hpp -- eight neighbouring values of a matrix's row, at any element's
+// address (device translation units only).
+#pragma once
+
+#include "activations.hpp"
+#include "mxfp8.hpp"
+
+namespace zp {
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+template <typename T>
+using Global = __attribute__((address_space(1))) T;
+
+// x / d.g for x < 2^31: m = magic is (2^(31 + l) + e) / g with 0 < e <= g <= 2^l,
+// so x m / 2^(31 + l) is x / g and less than 1 / g more.
+__device__ __forceinline__ uint32_t divide(uint32_t x, const Divisor& d) { return __umulhi(x, d.magic) >> d.shift; }
+
+// x = q d.g + r for x < 2^52: the product is within 1 of the quotient.
+__device__ __forceinline__ void divide(int64_t x, const Divisor& d, int64_t* q, uint32_t* r) {
+    int64_t a = int64_t(double(x) * d.inv);
+    int64_t b = x - a * int64_t(d.g);
+    if (b < 0) { b += d.g; a -= 1; }
+    if (b >= int64_t(d.g)) { b -= d.g; a += 1; }
+    *q = a;
+    *r = uint32_t(b);
+}
+
+// Eight values as they are in memory.
+template <int D>
+struct Octet {   // 16-bit types
+    u16x8 v;
+    __device__ __forceinline__ void zero() { v = u16x8{}; }
+    __device__ __forceinline__ void load(const void* p) {
+        typedef u16x8 at __attribute__((aligned(2)));
+        v = *(Global<const at>*)p;
+    }
+    __device__ __forceinline__ void store(void* p) const {
+        typedef u16x8 at __attribute__((aligned(2)));
+        *(Global<at>*)p = v;
+    }
+    __device__ __forceinline__ float get(int i) const { return Type<D>::wide(v[i]); }
+    __device__ __forceinline__ void set(int i, float x) { v[i] = Type<D>::narrow(x); }
+};
+template <>
+struct Octet<ZERO_DTYPE_FP32> {
+    f32x4 v[2];
+    __device__ __forceinline__ void zero() { v[0] = v[1] = f32x4{}; }
+    __device__ __forceinline__ void load(const void* p) {
+        typedef f32x4 at __attribute__((aligned(4)));
+        v[0] = ((Global<const at>*)p)[0];
+        v[1] = ((Global<const at>*)p)[1];
+    }
+    __device__ __forceinline__ void store(void* p) const {
+        typedef f32x4 at __attribute__((aligned(4)));
+        ((Global<at>*)p)[0] = v[0];
+        ((Global<at>*)p)[1] = v[1];
+    }
+    __device__ __forceinline__ float get(int i) const { return v[i >> 2][i & 3]; }
+    __device__ __forceinline__ void set(int i, float x) { v[i >> 2][i & 3] = x; }
+};
+
+// The octet at p of which `n` values exist (8 or more: all; 0 or less: none);
+// the others are zero.
+template <int D>
+__device__ __forceinline__ Octet<D> load_octet(const void* p, int64_t n) {
+    typedef typename Type<D>::elem E;
+    Octet<D> x;
+    if (n >= kOctet) {
+        x.load(p);
+        return x;
+    }
+    x.zero();
+#pragma unroll
+    for (int i = 0; i < kOctet; ++i)
+        if (i < n) {
+            const E e = ((Global<const E>*)p)[i];
+            if constexpr (D == ZERO_DTYPE_FP32) x.set(i, e);
+            else x.v[i] = e;
+        }
+    return x;
+}
+template <int D>
+__device__ __forceinline__ void store_octet(void* p, int64_t n, const Octet<D>& x) {
+    typedef typename Type<D>::elem E;
+    if (n >= kOctet) {
+        x.store(p);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < kOctet; ++i)
+        if (i < n) {
+            if constexpr (D == ZERO_DTYPE_FP32) ((Global<E>*)p)[i] = x.get(i);
+            else ((Global<E>*)p)[i] = x.v[i];
+        }
+}
+
+// Where the value at (row, col) of a matrix is.
+template <int D>
+__device__ __forceinline__ char* place(const void* p, int64_t row, int64_t stride, int64_t col) {
+    return (char*)p + (row * stride + col) * int64_t(sizeof(typename Type<D>::elem));
+}
+
+}  // namespace zp

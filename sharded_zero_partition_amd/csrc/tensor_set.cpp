@@ -41,6 +41,24 @@ struct zero_tensor_set {
 };
 
 namespace zp {
+
+// Events for a timed call; none while its stream is being captured (a graph's
+// nodes carry no events of one call).
+hipError_t set_events(hipStream_t s, KernelEvents* ev, bool* timed) {
+    *timed = false;
+    hipError_t e = timing_events(ev);
+    if (e != hipSuccess || !ev->start) return e;
+    hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+    e = hipStreamIsCapturing(s, &status);
+    if (e != hipSuccess) return e;
+    if (status != hipStreamCaptureStatusNone) {
+        *ev = KernelEvents();   // the pair stays open: the next timed call takes it
+        return hipSuccess;
+    }
+    *timed = true;
+    return hipSuccess;
+}
+
 namespace {
 
 int dtype_bytes(int32_t t) {
@@ -132,23 +150,6 @@ private:
 SetLaunch set_launch(const zero_tensor_set* s) {
     return SetLaunch{s->d_rec, s->d_tile, s->n_tiles, s->d_norm_tile, s->n_norm_tiles, s->grad_type, s->state_type, s->out_type,
                      s->staged_step, s->staged_codes, s->random_m};
-}
-
-// Events for a timed call; none while its stream is being captured (a graph's
-// nodes carry no events of one call).
-hipError_t set_events(hipStream_t s, KernelEvents* ev, bool* timed) {
-    *timed = false;
-    hipError_t e = timing_events(ev);
-    if (e != hipSuccess || !ev->start) return e;
-    hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
-    e = hipStreamIsCapturing(s, &status);
-    if (e != hipSuccess) return e;
-    if (status != hipStreamCaptureStatusNone) {
-        *ev = KernelEvents();   // the pair stays open: the next timed call takes it
-        return hipSuccess;
-    }
-    *timed = true;
-    return hipSuccess;
 }
 
 int create(const zero_tensor* tensors, int64_t n, int32_t grad_type, int32_t state_type, int32_t out_type,

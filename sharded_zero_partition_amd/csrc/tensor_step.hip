@@ -10,6 +10,7 @@
 // states p equal a scalar reference bit for bit.
 #include <type_traits>
 
+#include "mxfp8.hpp"
 #include "tensor_set.hpp"
 #include "timed_launch.hpp"
 
@@ -162,31 +163,6 @@ __device__ __forceinline__ T* tile_at(const void* p, int64_t base) {
     return reinterpret_cast<T*>(reinterpret_cast<uintptr_t>(p) + uintptr_t(base * int64_t(sizeof(T))));
 }
 
-// Types behind the ABI's dtype numbers.
-template <int D>
-struct Type;
-template <>
-struct Type<ZERO_DTYPE_FP16> {
-    typedef uint16_t elem;
-    static __device__ __forceinline__ float wide(uint16_t x) { return float(__builtin_bit_cast(_Float16, x)); }
-    static __device__ __forceinline__ uint16_t narrow(float x) { return __builtin_bit_cast(uint16_t, _Float16(x)); }
-};
-template <>
-struct Type<ZERO_DTYPE_BF16> {
-    typedef uint16_t elem;
-    static __device__ __forceinline__ float wide(uint16_t x) { return __builtin_bit_cast(float, uint32_t(x) << 16); }
-    static __device__ __forceinline__ uint16_t narrow(float x) { return __builtin_bit_cast(uint16_t, __bf16(x)); }
-};
-template <>
-struct Type<ZERO_DTYPE_FP32> {
-    typedef float elem;
-    static __device__ __forceinline__ float wide(float x) { return x; }
-};
-template <>
-struct Type<ZERO_DTYPE_MXFP8> {
-    typedef uint8_t elem;
-};
-
 // ---------------------------------------------------------------------------
 // MXFP8 states: a block of 32 elements is 8 neighbouring lanes with 4 each
 // ---------------------------------------------------------------------------
@@ -206,23 +182,6 @@ __device__ __forceinline__ uint32_t max4(uint32_t a, uint32_t b, uint32_t c, uin
     const uint32_t x = a > b ? a : b, y = c > d ? c : d;
     return x > y ? x : y;
 }
-__device__ __forceinline__ uint32_t bits(float x) { return __builtin_bit_cast(uint32_t, x); }
-__device__ __forceinline__ float number(uint32_t x) { return __builtin_bit_cast(float, x); }
-
-// The scale byte of a block whose largest magnitude has the bits `top`: the
-// least s >= 1 with top 2^(127 - s) <= 448 = 1.75 2^8.  The exponent of top less
-// 8, and one more when its fraction is above 1.75.
-__device__ __forceinline__ int scale_of(uint32_t top) {
-    const int e = int((top + 0x1FFFFFu) >> 23) - 8;
-    return e > 1 ? e : 1;
-}
-
-// 2^(s - 127).  s = 0 is 2^-127, below the normal range.
-__device__ __forceinline__ float scale_value(int s) {
-    const uint32_t b = uint32_t(s) << 23;
-    return number(b > 0x00400000u ? b : 0x00400000u);
-}
-
 __device__ __forceinline__ void decode4(uint32_t code, int s, float x[4]) {
     const float f = scale_value(s);
     const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(int(code), false);
@@ -238,10 +197,6 @@ __device__ __forceinline__ uint32_t encode4(const float y[4]) {
     const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
     return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true));
 }
-
-// The multiplier into a block's range, 2^(127 - s), exact for any value but
-// those that fall below fp32's normal range.
-__device__ __forceinline__ float into_block(int s) { return number(uint32_t(254 - s) << 23); }
 
 // ... and to one of its two neighbours in magnitude at random: r0 holds 16 random
 // bits for each of the first two elements, r1 for the others.  The conversion

@@ -291,6 +291,9 @@ int check_stream_device(void* stream, int dev, const char* what);
 // and timing_done closes the pair once the launches are enqueued.
 hipError_t timing_events(KernelEvents* ev);
 void timing_done();
+// timing_events for a call that may be captured, where it is not timed; *timed:
+// close the pair with timing_done.
+hipError_t set_events(hipStream_t s, KernelEvents* ev, bool* timed);
 
 // Blocks per CU of the grid-stride kernels (the in-place check pass and the
 // slot restore), read once from ZERO_BLOCKS_PER_CU when set.
