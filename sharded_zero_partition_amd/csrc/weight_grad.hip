@@ -2,6 +2,7 @@
 // checkpoint of its input (gfx950):
 //   dw[n, k] = sum_t dy[t, n] x[t, k]        bias[n] = sum_t dy[t, n]
 #include <type_traits>
+#include <utility>
 
 #include "octets.hpp"
 #include "timed_launch.hpp"
@@ -42,7 +43,8 @@ struct Config {
     static constexpr int a_chunks = STEP * BM / 16 / threads;   // of 16 values, a thread's
     static constexpr int b_chunks = STEP * BN / 16 / threads;
     static constexpr int a_bytes = STEP * BM * 2, b_bytes = STEP * BN * 2;
-    static constexpr int stage = a_bytes + P * b_bytes;
+    static constexpr int stage = a_bytes + P * b_bytes, lds_bytes = 2 * stage;
+    static constexpr int G = MI * NI > 16 ? 1 : 2;   // fragments of n that leave at a time
     static_assert(a_chunks * threads * 16 == STEP * BM && b_chunks * threads * 16 == STEP * BN, "loads");
     static_assert(2 * stage <= 160 * 1024, "LDS");
 };
@@ -92,14 +94,16 @@ struct Chunk {
 struct Codes {
     u32x4 code;
     uint32_t scale;
-    // as bf16 pairs, exactly: an e4m3 number has 4 bits
-    __device__ __forceinline__ void decode(u32x4 to[2]) const {
+    // half h as bf16 pairs, exactly: an e4m3 number has 4 bits
+    __device__ __forceinline__ u32x4 decode(int h) const {
         const float f = number(scale << 23);
+        u32x4 to;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            to[w >> 1][(2 * w) & 3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code[w], f, false));
-            to[w >> 1][(2 * w + 1) & 3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code[w], f, true));
+        for (int w = 0; w < 2; ++w) {
+            to[2 * w] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code[2 * h + w], f, false));
+            to[2 * w + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code[2 * h + w], f, true));
         }
+        return to;
     }
 };
 
@@ -113,29 +117,70 @@ __device__ __forceinline__ bf16x8 fragment(uint32_t at, int row_bytes) {
     return __builtin_bit_cast(bf16x8, v);
 }
 
+// Where a block's results go: dw, or the fp32 sums of a split.
+struct Target {
+    char* p;
+    int64_t rows, cols, ld;   // elements
+    bool accumulate;
+};
+
+// Four neighbouring values of a row.
 template <int DO>
-__device__ __forceinline__ void put(const GemmArgs& a, int64_t n, int64_t k, f32x4 v) {
+struct Four {
     typedef typename Type<DO>::elem E;
-    if (n >= a.w.n) return;
-    E* p = static_cast<E*>(a.w.dw);
-    const int64_t step = a.w.transposed ? a.w.s_dw : 1;
-    p += a.w.transposed ? k * a.w.s_dw + n : n * a.w.s_dw + k;
-    float old[4] = {};
-    if (a.w.accumulate)
+    typedef E vec __attribute__((ext_vector_type(4)));
+    typedef vec at __attribute__((aligned(sizeof(E))));
+    static __device__ __forceinline__ float wide(E e) {
+        if constexpr (DO == ZERO_DTYPE_FP32) return e;
+        else return Type<DO>::wide(e);
+    }
+    static __device__ __forceinline__ E narrow(float x) {
+        if constexpr (DO == ZERO_DTYPE_FP32) return x;
+        else return Type<DO>::narrow(x);
+    }
+};
+
+// Writes the R x N values that a wave has in LDS, rows of `pitch` floats, to the rows and
+// columns from (row, col) on.
+template <int DO, int R, int N, int kPitch>
+__device__ __forceinline__ void store_rows(const Target& t, const float* stage, int64_t row, int64_t col) {
+    typedef Four<DO> F;
+    typedef typename F::E E;
+    constexpr int fours = N / 4, per = 64 / fours, count = R / per, batch = count < 8 ? count : 8;   // rows a load, loads
+    static_assert(64 % fours == 0 && R % per == 0 && count % batch == 0, "whole rows");
+    const int lane = int(threadIdx.x) & 63, r0 = lane / fours, c = lane % fours * 4;
+    const float* from = stage + r0 * kPitch + c;
+    Global<E>* p = (Global<E>*)t.p + (row + r0) * t.ld + col + c;
+    const int64_t step = per * t.ld;
+    if (row + R <= t.rows && col + N <= t.cols) {   // all there
+#pragma unroll 1
+        for (int x = 0; x < count; x += batch) {
+            f32x4 v[batch];
+            typename F::vec y[batch];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (k + i < a.w.k) {
-                const E e = ((Global<const E>*)p)[i * step];
-                if constexpr (DO == ZERO_DTYPE_FP32) old[i] = e;
-                else old[i] = Type<DO>::wide(e);
+            for (int i = 0; i < batch; ++i) v[i] = *reinterpret_cast<const f32x4*>(from + (x + i) * per * kPitch);
+            if (t.accumulate)
+#pragma unroll
+                for (int i = 0; i < batch; ++i) y[i] = *(Global<typename F::at>*)(p + i * step);
+#pragma unroll
+            for (int i = 0; i < batch; ++i) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[i][k] = F::narrow(t.accumulate ? F::wide(y[i][k]) + v[i][k] : v[i][k]);
+                *(Global<typename F::at>*)(p + i * step) = y[i];
             }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (k + i < a.w.k) {
-            const float x = old[i] + v[i];
-            if constexpr (DO == ZERO_DTYPE_FP32) ((Global<E>*)p)[i * step] = x;
-            else ((Global<E>*)p)[i * step] = Type<DO>::narrow(x);
+            p += batch * step;
         }
+        return;
+    }
+#pragma unroll 1
+    for (int x = 0; x < count; ++x) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(from + x * per * kPitch);
+        const int64_t left = row + r0 + x * per < t.rows ? t.cols - col - c : 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < left) p[k] = F::narrow(t.accumulate ? F::wide(p[k]) + v[k] : v[k]);
+        p += step;
+    }
 }
 
 template <int DO>
@@ -146,6 +191,95 @@ __device__ __forceinline__ void put_bias(const GemmArgs& a, int64_t n, float v) 
     else *p = Type<DO>::narrow(a.w.accumulate ? Type<DO>::wide(*p) + v : v);
 }
 
+// Which outputs and tokens a block has.  Blocks go round the 8 XCDs, so those of
+// one XCD take neighbouring tiles, 4 n-tiles wide: the 32 that run there at a time
+// are 8 by 4 and read 12 slabs from its L2 instead of up to 33.
+constexpr int kGroup = 4;
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return uint32_t(__builtin_amdgcn_readfirstlane(int(x))); }
+struct Part {
+    int64_t k0, n0, t_begin, t_end;
+    uint32_t split;
+};
+template <typename C>
+__device__ __forceinline__ Part part_of(const GemmArgs& a) {
+    const uint32_t total = gridDim.x, id = blockIdx.x, xcd = id & 7, q8 = total >> 3, r8 = total & 7;
+    uint32_t tile = xcd * q8 + (xcd < r8 ? xcd : r8) + (id >> 3);
+    const uint32_t tiles = uint32_t(a.tiles_k) * uint32_t(a.tiles_n);
+    Part p;
+    p.split = uniform(tile / tiles);
+    tile -= p.split * tiles;
+    const uint32_t group = uniform(tile / (kGroup * a.tiles_k)), rest = tile - group * (kGroup * a.tiles_k);
+    const uint32_t wide = a.tiles_n - group * kGroup < kGroup ? a.tiles_n - group * kGroup : kGroup;
+    const uint32_t tile_k = uniform(rest / wide);
+    p.k0 = int64_t(tile_k) * C::BM;
+    p.n0 = int64_t(group * kGroup + rest - tile_k * wide) * C::BN;
+    p.t_begin = int64_t(p.split) * a.per_split * C::STEP;
+    p.t_end = p.t_begin + a.per_split * C::STEP < a.w.T ? p.t_begin + a.per_split * C::STEP : a.w.T;
+    return p;
+}
+
+// Writes a block's products: the result, or its part of one that the tokens are
+// split for.  They go through LDS, `G` fragments of n at a time, so that a row's
+// neighbours leave together whichever way round dw is, and the code for its types
+// is there once.
+template <typename C>
+__device__ __forceinline__ void finish(const GemmArgs& a, const Part& part, char* lds,
+                                       const f32x4 (&acc)[C::MI][C::NI]) {
+    constexpr int G = C::G, K = C::MI * 16, N = 16 * G;
+    constexpr int pitch_k = K + 4, pitch_n = N + 4;   // floats; 4 more spread the rows over the banks
+    constexpr int bytes = 4 * (N * pitch_k > K * pitch_n ? N * pitch_k : K * pitch_n);
+    static_assert(bytes * C::WM * C::WN <= C::lds_bytes, "LDS");
+    const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6;
+    const int wm = wave / C::WN, wn = wave % C::WN;
+    float* stage = reinterpret_cast<float*>(lds + wave * bytes);
+    const int64_t k_wave = part.k0 + wm * K, n_wave = part.n0 + wn * (C::NI * 16);
+    const int k_lane = 4 * (lane >> 4), n_lane = lane & 15;
+    const bool parts = a.splits > 1;
+    const Target to = {parts ? reinterpret_cast<char*>(a.part + part.split * a.part_size) : static_cast<char*>(a.w.dw),
+                       a.w.transposed ? a.w.k : a.w.n, a.w.transposed ? a.w.n : a.w.k, parts ? a.ld_part : a.w.s_dw,
+                       !parts && a.w.accumulate};
+    const int type = parts ? int(ZERO_DTYPE_FP32) : a.w.out_type;
+    __syncthreads();   // every wave has read its last fragments
+#pragma unroll
+    for (int g = 0; g < C::NI; g += G) {
+        const auto store = [&](auto d) {
+            constexpr int DO = decltype(d)::value;
+            if (a.w.transposed) store_rows<DO, K, N, pitch_n>(to, stage, k_wave, n_wave + 16 * g);
+            else store_rows<DO, N, K, pitch_k>(to, stage, n_wave + 16 * g, k_wave);
+        };
+        if (!a.w.transposed) {
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+#pragma unroll
+                for (int m = 0; m < C::MI; ++m)
+                    *reinterpret_cast<f32x4*>(stage + (16 * i + n_lane) * pitch_k + 16 * m + k_lane) = acc[m][g + i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+#pragma unroll
+                for (int m = 0; m < C::MI; ++m)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) stage[(16 * m + k_lane + j) * pitch_n + 16 * i + n_lane] = acc[m][g + i][j];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (type == ZERO_DTYPE_FP16) store(std::integral_constant<int, ZERO_DTYPE_FP16>{});
+        else if (type == ZERO_DTYPE_BF16) store(std::integral_constant<int, ZERO_DTYPE_BF16>{});
+        else store(std::integral_constant<int, ZERO_DTYPE_FP32>{});
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+}
+
+// The sum over dy of a wave's 16 columns from n on.
+__device__ __forceinline__ void finish_bias(const GemmArgs& a, const Part& part, int64_t n, float sum) {
+    const int lane = int(threadIdx.x) & 63;
+    n += lane;
+    if (lane >= 16 || n >= a.w.n) return;
+    if (a.splits > 1) ((Global<float>*)a.part_bias)[part.split * a.w.n + n] = sum;
+    else if (a.w.out_type == ZERO_DTYPE_FP16) put_bias<ZERO_DTYPE_FP16>(a, n, sum);
+    else if (a.w.out_type == ZERO_DTYPE_BF16) put_bias<ZERO_DTYPE_BF16>(a, n, sum);
+    else put_bias<ZERO_DTYPE_FP32>(a, n, sum);
+}
+
 template <typename C>
 __global__ __launch_bounds__(C::threads) void weight_grad_kernel(const GemmArgs a) {
     constexpr int D = C::D, P = C::P;
@@ -153,15 +287,8 @@ __global__ __launch_bounds__(C::threads) void weight_grad_kernel(const GemmArgs 
     const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6;
     const int wm = wave / C::WN, wn = wave % C::WN;
 
-    // neighbouring tiles on one XCD (blocks go round the 8 of them)
-    const uint32_t total = gridDim.x, id = blockIdx.x, xcd = id & 7, q8 = total >> 3, r8 = total & 7;
-    uint32_t tile = xcd * q8 + (xcd < r8 ? xcd : r8) + (id >> 3);
-    const uint32_t tiles = uint32_t(a.tiles_k) * uint32_t(a.tiles_n);
-    const uint32_t split = tile / tiles;
-    tile -= split * tiles;
-    const int64_t k0 = int64_t(tile % a.tiles_k) * C::BM, n0 = int64_t(tile / a.tiles_k) * C::BN;
-    const int64_t t_begin = int64_t(split) * a.per_split * C::STEP;
-    const int64_t t_end = t_begin + a.per_split * C::STEP < a.w.T ? t_begin + a.per_split * C::STEP : a.w.T;
+    const Part part = part_of<C>(a);
+    const int64_t k0 = part.k0, n0 = part.n0, t_begin = part.t_begin, t_end = part.t_end;
 
     Codes ra[C::a_chunks];
     Chunk<D> rb[C::b_chunks];
@@ -190,10 +317,8 @@ __global__ __launch_bounds__(C::threads) void weight_grad_kernel(const GemmArgs 
         for (int j = 0; j < C::a_chunks; ++j) {
             const int c = tid + j * C::threads;
             u32x4* to = reinterpret_cast<u32x4*>(base + pair_at<C::BM>(c / (C::BM / 16), c % (C::BM / 16)));
-            u32x4 v[2];
-            ra[j].decode(v);
-            to[0] = v[0];
-            to[1] = v[1];
+            to[0] = ra[j].decode(0);
+            to[1] = ra[j].decode(1);
         }
 #pragma unroll
         for (int j = 0; j < C::b_chunks; ++j) {
@@ -266,43 +391,242 @@ __global__ __launch_bounds__(C::threads) void weight_grad_kernel(const GemmArgs 
         __syncthreads();
     }
 
-    const int64_t k_lane = k0 + wm * (C::MI * 16) + 4 * (lane >> 4), n_lane = n0 + wn * (C::NI * 16) + (lane & 15);
-    if (a.splits > 1) {
-        float* part = a.part + split * a.part_size;
+    finish<C>(a, part, lds, acc);
+    if (bias)
 #pragma unroll
-        for (int i = 0; i < C::NI; ++i)
+        for (int i = 0; i < C::NI; ++i) finish_bias(a, part, n0 + (wn * C::NI + i) * 16, sum[i][0]);
+}
+
+// The same for a dy of bf16 that is aligned to 16 bytes: four waves of 128 x 128
+// outputs, one to a SIMD.
+//
+// A phase is 32 tokens: 64 products of a wave, 16 cycles each on its matrix unit,
+// in which the wave can issue up to three other instructions each.  Loads bring dy,
+// codes and scales straight into LDS, where they are rings; what a phase does besides
+// its own products is
+//   - the codes of the phase after the next are decoded, from and to LDS,
+//   - the fragments of the next phase are read,
+//   - dy four phases ahead and codes five ahead are sent for.
+// With loads through registers the compiler would wait for the newest of them at each use;
+// so it knows of none, and one wait a phase leaves those of the last two phases under way.
+// The loop holds ten phases, so that all places in the rings are constants.
+template <int... I, typename F>
+__device__ __forceinline__ void each(std::integer_sequence<int, I...>, const F& f) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+
+struct Fast {
+    static constexpr int BM = 256, BN = 256, WM = 2, WN = 2, STEP = 64, MI = 8, NI = 8, threads = 256, G = 4;
+    static constexpr int rows = 32;                               // of a phase
+    static constexpr int a_bytes = rows * BM * 2, b_bytes = rows * BN * 2, code_bytes = rows * BM, scale_bytes = rows * 8 * 4;
+    static constexpr int a_ring = 2, b_ring = 5, code_ring = 5, turn = 10;
+    static constexpr int b_at = a_ring * a_bytes, code_at = b_at + b_ring * b_bytes, scale_at = code_at + code_ring * code_bytes;
+    static constexpr int lds_bytes = scale_at + code_ring * scale_bytes;
+    static constexpr int b_loads = b_bytes / 4096, code_loads = code_bytes / 4096, loads = b_loads + code_loads + 1;   // a wave's
+    static_assert(lds_bytes <= 160 * 1024 && loads == 7, "LDS, and the waits below");
+};
+
+// Loads into LDS, the lanes' 16 bytes, or bytes as words, one after the other from
+// `to` + kOffset on (m0).
+template <int kOffset>
+__device__ __forceinline__ void load16(uint32_t to, uint32_t from, u32x4 buffer) {
+    asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds" ::"s"(to), "i"(kOffset), "v"(from), "s"(buffer) : "scc");
+}
+template <int kOffset>
+__device__ __forceinline__ void load1(uint32_t to, uint32_t from, u32x4 buffer) {
+    asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_ubyte %2, %3, 0 offen lds" ::"s"(to), "i"(kOffset), "v"(from), "s"(buffer) : "scc");
+}
+
+// c += a b, in place.
+__device__ __forceinline__ void multiply_v(f32x4& c, const bf16x8& a, const bf16x8& b) {
+    asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
+}
+
+template <int kSums>
+__global__ __launch_bounds__(256, 1) void weight_grad_fast_kernel(const GemmArgs a) {
+    typedef Fast C;
+    __shared__ __attribute__((aligned(1024))) char lds[C::lds_bytes];
+    const int tid = int(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / C::WN, wn = wave % C::WN;
+    const Part part = part_of<C>(a);
+    const int64_t k0 = part.k0, n0 = part.n0, t_begin = part.t_begin;
+    const int tokens = int(part.t_end - part.t_begin), phases = (tokens + C::rows - 1) / C::rows;
+    const uint32_t lds0 = uint32_t(reinterpret_cast<uintptr_t>((Shared<char>*)lds));
+
+    // Loads.  Beyond a buffer's size they give zeros: rows behind the last token, codes
+    // behind a row's end.  Load j of dy fills two rows of a tile, a lane's 16 bytes
+    // coming from where the exchanged pairs put them; load j of the codes four.
+    uint32_t from_b[C::b_loads], from_code[C::code_loads], from_scale;
 #pragma unroll
-            for (int m = 0; m < C::MI; ++m) {
-                const int64_t n = n_lane + 16 * i, k = k_lane + 16 * m;
-                if (n >= a.w.n) continue;
-                if (!a.w.transposed) {
-                    if (k < a.w.k) *(Global<f32x4>*)(part + n * a.ld_part + k) = acc[m][i];   // rows padded to 4
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (k + j < a.w.k) ((Global<float>*)part)[(k + j) * a.ld_part + n] = acc[m][i][j];
-                }
-            }
-        if (bias && lane < 16)
-#pragma unroll
-            for (int i = 0; i < C::NI; ++i)
-                if (n_lane + 16 * i < a.w.n) ((Global<float>*)a.part_bias)[split * a.w.n + n_lane + 16 * i] = sum[i][0];
-        return;
+    for (int j = 0; j < C::b_loads; ++j) {
+        const int r = 2 * (wave * C::b_loads + j) + (lane >> 5), c = lane & 31;
+        from_b[j] = uint32_t(r) * uint32_t(a.w.s_dy) * 2 + ((((c >> 1) ^ (r & 7)) * 2 + (c & 1)) << 4);
     }
-    const auto write = [&](auto d) {
-        constexpr int DO = decltype(d)::value;
 #pragma unroll
-        for (int i = 0; i < C::NI; ++i)
-#pragma unroll
-            for (int m = 0; m < C::MI; ++m) put<DO>(a, n_lane + 16 * i, k_lane + 16 * m, acc[m][i]);
-        if (bias && lane < 16)
-#pragma unroll
-            for (int i = 0; i < C::NI; ++i)
-                if (n_lane + 16 * i < a.w.n) put_bias<DO>(a, n_lane + 16 * i, sum[i][0]);
+    for (int j = 0; j < C::code_loads; ++j) {
+        const int r = 4 * (wave * C::code_loads + j) + (lane >> 4), c = lane & 15;
+        from_code[j] = uint32_t(r * a.pitch + 16 * c) | (k0 + 16 * c < a.pitch ? 0 : 0x80000000u);
+    }
+    from_scale = uint32_t((8 * wave + (lane >> 3)) * a.blocks + (lane & 7));
+    // What is left of a matrix from the next phase on that is loaded: its address and bytes.
+    struct Source {
+        uint64_t p;
+        uint32_t bytes;
+        __device__ __forceinline__ u32x4 buffer() const { return {uint32_t(p), uint32_t(p >> 32), bytes, 0x00020000u}; }
+        __device__ __forceinline__ void advance(uint32_t step) {
+            p += step;
+            // what is left, or 0 (the compiler would take a vector instruction for it)
+            asm("s_sub_u32 %0, %0, %1\n\ts_cselect_b32 %0, 0, %0" : "+s"(bytes) : "s"(step) : "scc");
+        }
     };
-    if (a.w.out_type == ZERO_DTYPE_FP16) write(std::integral_constant<int, ZERO_DTYPE_FP16>{});
-    else if (a.w.out_type == ZERO_DTYPE_BF16) write(std::integral_constant<int, ZERO_DTYPE_BF16>{});
-    else write(std::integral_constant<int, ZERO_DTYPE_FP32>{});
+    const auto source = [](const void* base, int64_t offset, int64_t bytes) {
+        return Source{(reinterpret_cast<uint64_t>(base) + uint64_t(offset)) & 0xFFFFFFFFFFFFull, uint32_t(bytes)};
+    };
+    // (dy's stride is n at least, a row of codes no shorter than its part from k0 on)
+    Source dy = source(a.w.dy, (t_begin * a.w.s_dy + n0) * 2, ((tokens - 1) * a.w.s_dy + a.w.n - n0) * 2);
+    Source codes = source(a.w.code, t_begin * a.pitch + k0, tokens * a.pitch - k0);
+    Source scales = source(a.w.scale, t_begin * a.blocks + (k0 >> 5), tokens * a.blocks - (k0 >> 5));
+    const uint32_t step_b = uint32_t(C::rows * a.w.s_dy * 2), step_code = uint32_t(C::rows * a.pitch), step_scale = uint32_t(C::rows * a.blocks);
+    // Where a wave's loads go in slot 0 of each ring.
+    const uint32_t to_b = lds0 + C::b_at + wave * C::b_loads * 1024, to_code = lds0 + C::code_at + wave * C::code_loads * 1024,
+                   to_scale = lds0 + C::scale_at + wave * 256;
+
+    // Codes: a thread decodes pair q of rows t and t + 16.  Lanes whose place has bit 2
+    // set take their second half first, so that eight lanes' stores meet all banks.
+    const int ta = tid >> 4, qa = tid & 15;
+    const uint32_t swap = ((qa ^ ta) >> 2) & 1;
+    const uint32_t code_from = lds0 + C::code_at + tid * 16 + 8 * swap, scale_from = lds0 + C::scale_at + (ta * 8 + (qa >> 1)) * 4;
+    const uint32_t code_to = lds0 + pair_at<C::BM>(ta, qa) + 16 * swap;
+    const auto raw = [&](int j, int h, int slot) {
+        return *(Shared<const u32x2>*)uintptr_t((code_from ^ (8 * h)) + slot * C::code_bytes + j * 4096);
+    };
+    const auto raw_scale = [&](int j, int slot) {
+        return *(Shared<const uint32_t>*)uintptr_t(scale_from + slot * C::scale_bytes + j * 512);
+    };
+    const auto decoded = [&](u32x2 code, uint32_t scale) {
+        const float f = number(scale << 23);
+        return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code.x, f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code.x, f, true)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code.y, f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code.y, f, true))};
+    };
+    const auto place_codes = [&](u32x4 v, int j, int h, int buf) {
+        *(Shared<u32x4>*)uintptr_t((code_to ^ (16 * h)) + buf * C::a_bytes + j * 16 * 512) = v;
+    };
+
+    const int row = 4 * (lane >> 4) + ((lane & 15) >> 2);
+    uint32_t at_a[8], at_b[8];
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+        const uint32_t at = lds0 + pair_at<256>(row, m) + (lane & 3) * 8;
+        at_a[m] = at + wm * 256;
+        at_b[m] = at + C::b_at + wn * 256;
+    }
+    struct Frags { bf16x8 a[C::MI], b[C::NI]; };
+    const auto read = [&](Frags& f, int i, int buf, int slot) {   // its 16 fragments, in the order of their use
+        if (i < 8) f.a[i] = fragment(at_a[i] + buf * C::a_bytes, 512);
+        else f.b[i - 8] = fragment(at_b[i - 8] + slot * C::b_bytes, 512);
+    };
+
+    f32x4 acc[C::MI][C::NI];
+#pragma unroll
+    for (int i = 0; i < C::NI; ++i)
+#pragma unroll
+        for (int m = 0; m < C::MI; ++m) acc[m][i] = f32x4{};
+    const auto multiply = [&](const Frags& f, int j) {   // in place: the compiler's own would move sums about
+        asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc[j & 7][j >> 3]) : "v"(f.a[j & 7]), "v"(f.b[j >> 3]));
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    // The bias: the waves that have the same columns of dy (two in each k-tile) share
+    // their 8 fragments, kSums for one, and multiply them with ones.  A wave behind
+    // the last share takes the last one too and drops it.
+    const int share = (int(k0 / C::BM) * 2 + wm) * kSums, first = min(share, C::NI - kSums);
+    f32x4 sum[kSums + 1];
+    bf16x8 ones, fb[kSums + 1];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ones[i] = __bf16(1.0f);
+    uint32_t at_sum[kSums + 1];
+#pragma unroll
+    for (int i = 0; i < kSums; ++i) {
+        sum[i] = f32x4{};
+        at_sum[i] = lds0 + C::b_at + pair_at<256>(row, wn * 8 + first + i) + (lane & 3) * 8;
+    }
+    Frags f0, f1;
+    // The Q-th phase of a turn with its fragments in f; those of the next go to g.
+    const auto phase = [&](auto turn, const Frags& f, Frags& g) __attribute__((always_inline)) {
+        constexpr int Q = decltype(turn)::value;
+        u32x2 raws[2][2];
+        uint32_t rs[2];
+        u32x4 d;
+        each(std::make_integer_sequence<int, 64>{}, [&](auto at) __attribute__((always_inline)) {
+            constexpr int j = decltype(at)::value;
+            multiply(f, j);
+            if constexpr (j < 2) {
+                raws[j][0] = raw(j, 0, (Q + 2) % C::code_ring);
+                raws[j][1] = raw(j, 1, (Q + 2) % C::code_ring);
+                rs[j] = raw_scale(j, (Q + 2) % C::code_ring);
+            }
+            if constexpr (j >= 2 && j < 50 && j % 3 == 2) read(g, (j - 2) / 3, (Q + 1) % 2, (Q + 1) % C::b_ring);
+            if constexpr (j >= 16 && j < 40 && j % 6 == 4) d = decoded(raws[(j - 16) / 12][(j - 16) / 6 % 2], rs[(j - 16) / 12]);
+            if constexpr (j >= 16 && j < 40 && j % 6 == 0) place_codes(d, (j - 16) / 12, (j - 16) / 6 % 2, Q % 2);
+            if constexpr (j >= 40 && j < 52 && j % 3 == 1) load16<(Q + 4) % C::b_ring * C::b_bytes + (j - 40) / 3 * 1024>(to_b, from_b[(j - 40) / 3], dy.buffer());
+            if constexpr (j == 52 || j == 55) load16<Q % C::code_ring * C::code_bytes + (j - 52) / 3 * 1024>(to_code, from_code[(j - 52) / 3], codes.buffer());
+            if constexpr (j == 58) load1<Q % C::code_ring * C::scale_bytes>(to_scale, from_scale, scales.buffer());
+            if constexpr (j == 54) dy.advance(step_b);
+            if constexpr (j == 60) codes.advance(step_code);
+            if constexpr (j == 61) scales.advance(step_scale);
+            if constexpr (j >= 12 && j < 12 + 4 * kSums && j % 4 == 0)
+                fb[(j - 12) / 4] = fragment(at_sum[(j - 12) / 4] + Q % C::b_ring * C::b_bytes, 512);
+            if constexpr (j >= 44 && j < 44 + 4 * kSums && j % 4 == 0)
+                multiply_v(sum[(j - 44) / 4], ones, fb[(j - 44) / 4]);
+        });
+        __builtin_amdgcn_s_waitcnt(0x0F70 | 14);   // all loads but the last two phases'
+        __syncthreads();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    // before the first phase: dy of phases 0 .. 3, codes of 0 .. 4, and those of 0 and 1 decoded
+    each(std::make_integer_sequence<int, 5>{}, [&](auto at) {
+        constexpr int p = decltype(at)::value;
+        if constexpr (p < 4) {
+            each(std::make_integer_sequence<int, C::b_loads>{}, [&](auto i) {
+                constexpr int j = decltype(i)::value;
+                load16<p * C::b_bytes + j * 1024>(to_b, from_b[j], dy.buffer());
+            });
+            dy.advance(step_b);
+        }
+        load16<p * C::code_bytes>(to_code, from_code[0], codes.buffer());
+        load16<p * C::code_bytes + 1024>(to_code, from_code[1], codes.buffer());
+        load1<p * C::scale_bytes>(to_scale, from_scale, scales.buffer());
+        codes.advance(step_code);
+        scales.advance(step_scale);
+    });
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) place_codes(decoded(raw(j, h, p), raw_scale(j, p)), j, h, p);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) read(f0, i, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    for (int p = 0; p < phases; p += C::turn) {   // phases behind the last multiply zeros
+        each(std::make_integer_sequence<int, C::turn>{}, [&](auto turn) __attribute__((always_inline)) {
+            if constexpr (decltype(turn)::value % 2 == 0) phase(turn, f0, f1);
+            else phase(turn, f1, f0);
+        });
+        if (p + C::turn >= phases) asm volatile("s_nop 15\n\ts_nop 15");   // the last products are written before anything reads them
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // no load comes into what follows
+    finish<C>(a, part, lds, acc);
+#pragma unroll
+    for (int i = 0; i < kSums; ++i)
+        if (share < C::NI) finish_bias(a, part, n0 + (wn * 8 + first + i) * 16, sum[i][0]);
 }
 
 // Adds up the splits' sums, in order: four neighbouring elements a thread.
@@ -365,6 +689,14 @@ Cut cut_for(int64_t T, int64_t n, int64_t k, int bn, int step) {
     return c;
 }
 
+// Whether the loads of the fast kernel reach everything: 16 bytes of dy at a time,
+// whole words up to the last value, offsets of 31 bits inside a split's `tokens`.
+bool fast(const WeightGradLaunch& w, int64_t tokens) {
+    constexpr int64_t most = int64_t(1) << 31;
+    return tokens > 0 && tokens < most && reinterpret_cast<uintptr_t>(w.dy) % 16 == 0 && w.s_dy % 8 == 0 && w.s_dy >= w.n && w.n % 2 == 0 &&
+           w.s_dy < most / 64 && tokens * w.s_dy < most / 2 && w.k < most / 64 && tokens * (w.k + 32) < most;
+}
+
 template <typename C>
 hipError_t run(const WeightGradLaunch& w, hipStream_t s, const KernelEvents& ev) {
     const Cut c = cut_for(w.T, w.n, w.k, C::BN, C::STEP);
@@ -381,7 +713,13 @@ hipError_t run(const WeightGradLaunch& w, hipStream_t s, const KernelEvents& ev)
     a.part = w.work;
     a.part_bias = c.splits > 1 ? w.work + c.splits * c.part_size : nullptr;
     KernelEvents one = {ev.start, c.splits > 1 ? nullptr : ev.stop};
-    launch(weight_grad_kernel<C>, dim3(uint32_t(int64_t(c.tiles_k) * c.tiles_n * c.splits)), C::threads, s, one, a);
+    const dim3 blocks(uint32_t(int64_t(c.tiles_k) * c.tiles_n * c.splits));
+    if (C::D == ZERO_DTYPE_BF16 && fast(w, c.per_split * C::STEP)) {
+        if (!w.bias) launch(weight_grad_fast_kernel<0>, blocks, Fast::threads, s, one, a);
+        else if (c.tiles_k >= 4) launch(weight_grad_fast_kernel<1>, blocks, Fast::threads, s, one, a);
+        else if (c.tiles_k >= 2) launch(weight_grad_fast_kernel<2>, blocks, Fast::threads, s, one, a);
+        else launch(weight_grad_fast_kernel<4>, blocks, Fast::threads, s, one, a);
+    } else launch(weight_grad_kernel<C>, blocks, C::threads, s, one, a);
     if (c.splits > 1) {
         one = {nullptr, ev.stop};
         const int64_t rows = w.transposed ? w.k : w.n;
