@@ -12,8 +12,8 @@
 namespace zp {
 namespace {
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -30,13 +30,76 @@ __device__ __forceinline__ uint32_t pair_at(int t, int q) {
     return uint32_t(t * (W * 2) + ((q ^ (t & 7)) << 5));
 }
 
-// A dy value as the sum of bf16 numbers, exactly: 1 for bf16, 2 for fp16 (11
-// bits), 3 for fp32 (24 bits).
-constexpr int parts_of(int d) { return d == ZERO_DTYPE_BF16 ? 1 : d == ZERO_DTYPE_FP16 ? 2 : 3; }
+// The products are of 16-bit numbers, exact in fp32, and what they are made from is
+// there whole:
+//   bf16   dy as it is, x in bf16: an e4m3 number has 4 bits, and every scale is in range
+//   fp32   dy as three bf16 numbers (24 bits) whose sum it is, x in bf16
+//   fp16   dy as it is, x in fp16, which needs a common scale to be in range: each 32
+//          columns' largest, over the tokens of the block, is brought to 57344 at most, and
+//          the sums are brought back.  Blocks down to 2^-22 of the largest keep all
+//          bits, and so does any x that was stored from fp16 (multiples of 2^-24) up to
+//          57344.  Of smaller ones the low bits are rounded, at 2^-41 of the largest.
+//          (As two bf16 numbers dy took twice the products: 242 us for 16384 tokens,
+//          1600 x 1600 in the kernel below, and 32 KB more LDS.)
+constexpr int parts_of(int d) { return d == ZERO_DTYPE_FP32 ? 3 : 1; }
+constexpr int kTop = 134;   // the largest scale's byte in fp16 products: 448 2^7 = 57344
 
-template <int D_, int BN_, int WM_, int WN_, int STEP_>
+template <int D>
+struct Op {   // fp16
+    static constexpr bool kScaled = true;
+    static constexpr short one = 0x3C00;
+    static __device__ __forceinline__ uint32_t pair(uint32_t code, float f, bool high) {
+        return high ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(code, f, true))
+                    : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(code, f, false));
+    }
+    static __device__ __forceinline__ f32x4 multiply(s16x8 a, s16x8 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    }
+    // c += a b in place: the compiler's own would move sums about.  A sum may be read 16
+    // wait states later.
+    static __device__ __forceinline__ void multiply_a(f32x4& c, s16x8 a, s16x8 b) {
+        asm("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+    }
+    static __device__ __forceinline__ void multiply_v(f32x4& c, s16x8 a, s16x8 b) {
+        asm("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
+    }
+};
+struct OpBf16 {
+    static constexpr bool kScaled = false;
+    static constexpr short one = 0x3F80;
+    static __device__ __forceinline__ uint32_t pair(uint32_t code, float f, bool high) {
+        return high ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code, f, true))
+                    : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code, f, false));
+    }
+    static __device__ __forceinline__ f32x4 multiply(s16x8 a, s16x8 b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ void multiply_a(f32x4& c, s16x8 a, s16x8 b) {
+        asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+    }
+    static __device__ __forceinline__ void multiply_v(f32x4& c, s16x8 a, s16x8 b) {
+        asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
+    }
+};
+template <>
+struct Op<ZERO_DTYPE_BF16> : OpBf16 {};
+template <>
+struct Op<ZERO_DTYPE_FP32> : OpBf16 {};
+
+// Two pairs of codes with scale byte `s`, `top` being the columns' largest.
+template <int D>
+__device__ __forceinline__ u32x4 decode(u32x2 code, uint32_t s, uint32_t top) {
+    // beyond either end: what has no bits left is zero, and 255's codes are NaN
+    if (Op<D>::kScaled) s = uint32_t(max(min(int(s) - int(top) + kTop, 255), 0));
+    const float f = number(s << 23);
+    return u32x4{Op<D>::pair(code.x, f, false), Op<D>::pair(code.x, f, true), Op<D>::pair(code.y, f, false), Op<D>::pair(code.y, f, true)};
+}
+
+// Tiles of 256 x 256 outputs, steps of STEP tokens.
+constexpr int kTile = 256;
+template <int D_, int STEP_>
 struct Config {
-    static constexpr int D = D_, BM = 256, BN = BN_, WM = WM_, WN = WN_, STEP = STEP_;
+    static constexpr int D = D_, BM = kTile, BN = kTile, WM = 2, WN = 4, STEP = STEP_;
     static constexpr int P = parts_of(D);
     static constexpr int threads = 64 * WM * WN;
     static constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
@@ -44,7 +107,7 @@ struct Config {
     static constexpr int b_chunks = STEP * BN / 16 / threads;
     static constexpr int a_bytes = STEP * BM * 2, b_bytes = STEP * BN * 2;
     static constexpr int stage = a_bytes + P * b_bytes, lds_bytes = 2 * stage;
-    static constexpr int G = MI * NI > 16 ? 1 : 2;   // fragments of n that leave at a time
+    static constexpr int G = 1;   // fragments of n that leave at a time
     static_assert(a_chunks * threads * 16 == STEP * BM && b_chunks * threads * 16 == STEP * BN, "loads");
     static_assert(2 * stage <= 160 * 1024, "LDS");
 };
@@ -53,12 +116,16 @@ struct GemmArgs {
     WeightGradLaunch w;
     int64_t pitch;       // of the codes
     int64_t blocks;      // scale bytes of a row
-    int32_t tiles_k, tiles_n, splits;
-    int64_t per_split;   // steps
-    float* part;         // splits > 1: [splits][n][k], or [splits][k][n] transposed, rows of ld_part
-    float* part_bias;    // [splits][n]
-    int64_t ld_part, part_size;
+    int32_t tiles_k, tiles_n;
+    int32_t whole;       // tiles that one block has for all tokens, the first ones; each of the others has
+    int32_t splits;      // `splits` blocks (1: all are whole)
+    int64_t per_split;   // tokens of a split, a multiple of kUnit
+    float* part;         // sums of tile whole + i and split j: kTile x kTile at (i splits + j) kPart, as dw has them,
+                         // then kTile of dy's columns
+    int32_t shares;      // whose the bias is: 0: the first k-tile's, else k-tile i / 2's for fragments i shares on of each 8
 };
+constexpr int64_t kPart = kTile * kTile + kTile;
+constexpr int64_t kUnit = 64;
 
 // 16 values of dy.
 template <int D>
@@ -68,13 +135,13 @@ struct Chunk {
         o[0] = load_octet<D>(p, left);
         o[1] = load_octet<D>(p + sizeof(typename Type<D>::elem) * 8, left - 8);
     }
-    // part j of the values, as bf16 pairs
+    // part j of the values, as pairs
     __device__ __forceinline__ void split(u32x4 to[parts_of(D)][2]) const {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if constexpr (D == ZERO_DTYPE_BF16) {
+                if constexpr (D != ZERO_DTYPE_FP32) {
                     to[0][h][i] = uint32_t(o[h].v[2 * i]) | uint32_t(o[h].v[2 * i + 1]) << 16;
                 } else {
                     float a = o[h].get(2 * i), b = o[h].get(2 * i + 1);
@@ -94,27 +161,15 @@ struct Chunk {
 struct Codes {
     u32x4 code;
     uint32_t scale;
-    // half h as bf16 pairs, exactly: an e4m3 number has 4 bits
-    __device__ __forceinline__ u32x4 decode(int h) const {
-        const float f = number(scale << 23);
-        u32x4 to;
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            to[2 * w] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code[2 * h + w], f, false));
-            to[2 * w + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code[2 * h + w], f, true));
-        }
-        return to;
-    }
 };
 
 // A fragment of 16 columns by 32 rows: the lane has column lane & 15 of rows
 // 4 (lane / 16) + 0 .. 3 and 16 more.  (Which of the 32 rows come where does not
 // matter as long as both operands have the same.)
-__device__ __forceinline__ bf16x8 fragment(uint32_t at, int row_bytes) {
+__device__ __forceinline__ s16x8 fragment(uint32_t at, int row_bytes) {
     const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Shared<s16x4>*)uintptr_t(at));
     const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((Shared<s16x4>*)uintptr_t(at + 16 * row_bytes));
-    const s16x8 v = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    return __builtin_bit_cast(bf16x8, v);
+    return s16x8{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 }
 
 // Where a block's results go: dw, or the fp32 sums of a split.
@@ -198,33 +253,85 @@ constexpr int kGroup = 4;
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return uint32_t(__builtin_amdgcn_readfirstlane(int(x))); }
 struct Part {
     int64_t k0, n0, t_begin, t_end;
-    uint32_t split;
+    int64_t slot;   // of its sums in `part`; -1: it has all tokens
 };
-template <typename C>
+__device__ __forceinline__ uint32_t in_order(uint32_t id, uint32_t total) {
+    const uint32_t xcd = id & 7, q8 = total >> 3, r8 = total & 7;
+    return xcd * q8 + (xcd < r8 ? xcd : r8) + (id >> 3);
+}
 __device__ __forceinline__ Part part_of(const GemmArgs& a) {
-    const uint32_t total = gridDim.x, id = blockIdx.x, xcd = id & 7, q8 = total >> 3, r8 = total & 7;
-    uint32_t tile = xcd * q8 + (xcd < r8 ? xcd : r8) + (id >> 3);
-    const uint32_t tiles = uint32_t(a.tiles_k) * uint32_t(a.tiles_n);
+    const uint32_t id = blockIdx.x, whole = uint32_t(a.whole);
     Part p;
-    p.split = uniform(tile / tiles);
-    tile -= p.split * tiles;
+    uint32_t tile;
+    if (id < whole) {
+        tile = in_order(id, whole);
+        p.slot = -1;
+        p.t_begin = 0;
+        p.t_end = a.w.T;
+    } else {
+        const uint32_t tiles = uint32_t(a.tiles_k) * uint32_t(a.tiles_n) - whole;
+        const uint32_t i = in_order(id - whole, gridDim.x - whole), split = uniform(i / tiles);
+        tile = whole + i - split * tiles;
+        p.slot = int64_t(tile - whole) * a.splits + split;
+        p.t_begin = int64_t(split) * a.per_split;
+        p.t_end = p.t_begin + a.per_split < a.w.T ? p.t_begin + a.per_split : a.w.T;
+    }
     const uint32_t group = uniform(tile / (kGroup * a.tiles_k)), rest = tile - group * (kGroup * a.tiles_k);
     const uint32_t wide = a.tiles_n - group * kGroup < kGroup ? a.tiles_n - group * kGroup : kGroup;
     const uint32_t tile_k = uniform(rest / wide);
-    p.k0 = int64_t(tile_k) * C::BM;
-    p.n0 = int64_t(group * kGroup + rest - tile_k * wide) * C::BN;
-    p.t_begin = int64_t(p.split) * a.per_split * C::STEP;
-    p.t_end = p.t_begin + a.per_split * C::STEP < a.w.T ? p.t_begin + a.per_split * C::STEP : a.w.T;
+    p.k0 = int64_t(tile_k) * kTile;
+    p.n0 = int64_t(group * kGroup + rest - tile_k * wide) * kTile;
     return p;
+}
+
+// The largest scale of each 32 of a tile's columns over its tokens (255, which is NaN, aside),
+// 1 at least, into top[0 .. 7].
+template <int kThreads>
+__device__ __forceinline__ void largest_scales(const GemmArgs& a, const Part& part, uint32_t* top) {
+    const int64_t left = a.blocks - (part.k0 >> 5);
+    const int there = left < 8 ? int(left) : 8;
+    if (threadIdx.x < 8) top[threadIdx.x] = 1;
+    __syncthreads();
+    constexpr int batch = 8;
+    uint32_t most[8] = {};
+    const uint8_t* p = a.w.scale + (part.k0 >> 5);
+    for (int64_t t = part.t_begin + threadIdx.x; t < part.t_end; t += batch * kThreads) {
+        uint64_t x[batch];
+        if (there == 8) {
+            typedef uint64_t at __attribute__((aligned(1)));
+#pragma unroll
+            for (int i = 0; i < batch; ++i) {
+                const int64_t u = t + i * kThreads < part.t_end ? t + i * kThreads : t;
+                x[i] = *(Global<const at>*)(p + u * a.blocks);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < batch; ++i) {
+                const int64_t u = t + i * kThreads < part.t_end ? t + i * kThreads : t;
+                x[i] = 0;
+                for (int b = 0; b < there; ++b) x[i] |= uint64_t(((Global<const uint8_t>*)p)[u * a.blocks + b]) << (8 * b);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < batch; ++i)
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+                const uint32_t s = uint32_t(x[i] >> (8 * b)) & 255;
+                most[b] = max(most[b], s == 255 ? 0 : s);
+            }
+    }
+#pragma unroll
+    for (int b = 0; b < 8; ++b) atomicMax(&top[b], most[b]);
+    __syncthreads();
 }
 
 // Writes a block's products: the result, or its part of one that the tokens are
 // split for.  They go through LDS, `G` fragments of n at a time, so that a row's
 // neighbours leave together whichever way round dw is, and the code for its types
 // is there once.
-template <typename C>
-__device__ __forceinline__ void finish(const GemmArgs& a, const Part& part, char* lds,
-                                       const f32x4 (&acc)[C::MI][C::NI]) {
+template <typename C, bool kScaled>
+__device__ __forceinline__ void finish(const GemmArgs& a, const Part& part, char* lds, const f32x4 (&acc)[C::MI][C::NI],
+                                       const int (&power)[C::MI / 2]) {
     constexpr int G = C::G, K = C::MI * 16, N = 16 * G;
     constexpr int pitch_k = K + 4, pitch_n = N + 4;   // floats; 4 more spread the rows over the banks
     constexpr int bytes = 4 * (N * pitch_k > K * pitch_n ? N * pitch_k : K * pitch_n);
@@ -232,12 +339,20 @@ __device__ __forceinline__ void finish(const GemmArgs& a, const Part& part, char
     const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6;
     const int wm = wave / C::WN, wn = wave % C::WN;
     float* stage = reinterpret_cast<float*>(lds + wave * bytes);
-    const int64_t k_wave = part.k0 + wm * K, n_wave = part.n0 + wn * (C::NI * 16);
+    const bool parts = part.slot >= 0;
+    const int64_t k_wave = (parts ? 0 : part.k0) + wm * K, n_wave = (parts ? 0 : part.n0) + wn * (C::NI * 16);
     const int k_lane = 4 * (lane >> 4), n_lane = lane & 15;
-    const bool parts = a.splits > 1;
-    const Target to = {parts ? reinterpret_cast<char*>(a.part + part.split * a.part_size) : static_cast<char*>(a.w.dw),
-                       a.w.transposed ? a.w.k : a.w.n, a.w.transposed ? a.w.n : a.w.k, parts ? a.ld_part : a.w.s_dw,
-                       !parts && a.w.accumulate};
+    const Target to = parts ? Target{reinterpret_cast<char*>(a.part + part.slot * kPart), kTile, kTile, kTile, false}
+                            : Target{static_cast<char*>(a.w.dw), a.w.transposed ? a.w.k : a.w.n, a.w.transposed ? a.w.n : a.w.k, a.w.s_dw,
+                                     a.w.accumulate};
+    // 2^power of fragments m and m + 1, 32 columns
+    const auto value = [&](int m, int i) {
+        f32x4 v = acc[m][i];
+        if (kScaled)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = ldexpf(v[j], power[m / 2]);
+        return v;
+    };
     const int type = parts ? int(ZERO_DTYPE_FP32) : a.w.out_type;
     __syncthreads();   // every wave has read its last fragments
 #pragma unroll
@@ -252,14 +367,16 @@ __device__ __forceinline__ void finish(const GemmArgs& a, const Part& part, char
             for (int i = 0; i < G; ++i)
 #pragma unroll
                 for (int m = 0; m < C::MI; ++m)
-                    *reinterpret_cast<f32x4*>(stage + (16 * i + n_lane) * pitch_k + 16 * m + k_lane) = acc[m][g + i];
+                    *reinterpret_cast<f32x4*>(stage + (16 * i + n_lane) * pitch_k + 16 * m + k_lane) = value(m, g + i);
         } else {
 #pragma unroll
             for (int i = 0; i < G; ++i)
 #pragma unroll
-                for (int m = 0; m < C::MI; ++m)
+                for (int m = 0; m < C::MI; ++m) {
+                    const f32x4 v = value(m, g + i);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) stage[(16 * m + k_lane + j) * pitch_n + 16 * i + n_lane] = acc[m][g + i][j];
+                    for (int j = 0; j < 4; ++j) stage[(16 * m + k_lane + j) * pitch_n + 16 * i + n_lane] = v[j];
+                }
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         if (type == ZERO_DTYPE_FP16) store(std::integral_constant<int, ZERO_DTYPE_FP16>{});
@@ -269,17 +386,18 @@ __device__ __forceinline__ void finish(const GemmArgs& a, const Part& part, char
     }
 }
 
-// The sum over dy of a wave's 16 columns from n on.
-__device__ __forceinline__ void finish_bias(const GemmArgs& a, const Part& part, int64_t n, float sum) {
+// The sum over dy of 16 columns of the tile, from n on.
+__device__ __forceinline__ void finish_bias(const GemmArgs& a, const Part& part, int n, float sum) {
     const int lane = int(threadIdx.x) & 63;
     n += lane;
-    if (lane >= 16 || n >= a.w.n) return;
-    if (a.splits > 1) ((Global<float>*)a.part_bias)[part.split * a.w.n + n] = sum;
-    else if (a.w.out_type == ZERO_DTYPE_FP16) put_bias<ZERO_DTYPE_FP16>(a, n, sum);
-    else if (a.w.out_type == ZERO_DTYPE_BF16) put_bias<ZERO_DTYPE_BF16>(a, n, sum);
-    else put_bias<ZERO_DTYPE_FP32>(a, n, sum);
+    if (lane >= 16 || part.n0 + n >= a.w.n) return;
+    if (part.slot >= 0) ((Global<float>*)a.part)[part.slot * kPart + kTile * kTile + n] = sum;
+    else if (a.w.out_type == ZERO_DTYPE_FP16) put_bias<ZERO_DTYPE_FP16>(a, part.n0 + n, sum);
+    else if (a.w.out_type == ZERO_DTYPE_BF16) put_bias<ZERO_DTYPE_BF16>(a, part.n0 + n, sum);
+    else put_bias<ZERO_DTYPE_FP32>(a, part.n0 + n, sum);
 }
 
+// Any dy: eight waves, loads through registers.
 template <typename C>
 __global__ __launch_bounds__(C::threads) void weight_grad_kernel(const GemmArgs a) {
     constexpr int D = C::D, P = C::P;
@@ -287,8 +405,10 @@ __global__ __launch_bounds__(C::threads) void weight_grad_kernel(const GemmArgs 
     const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6;
     const int wm = wave / C::WN, wn = wave % C::WN;
 
-    const Part part = part_of<C>(a);
+    const Part part = part_of(a);
     const int64_t k0 = part.k0, n0 = part.n0, t_begin = part.t_begin, t_end = part.t_end;
+    __shared__ uint32_t top[8];
+    if (Op<D>::kScaled) largest_scales<C::threads>(a, part, top);
 
     Codes ra[C::a_chunks];
     Chunk<D> rb[C::b_chunks];
@@ -317,8 +437,9 @@ __global__ __launch_bounds__(C::threads) void weight_grad_kernel(const GemmArgs 
         for (int j = 0; j < C::a_chunks; ++j) {
             const int c = tid + j * C::threads;
             u32x4* to = reinterpret_cast<u32x4*>(base + pair_at<C::BM>(c / (C::BM / 16), c % (C::BM / 16)));
-            to[0] = ra[j].decode(0);
-            to[1] = ra[j].decode(1);
+            const uint32_t most = Op<D>::kScaled ? top[c % (C::BM / 16) / 2] : 0;
+            to[0] = decode<D>(u32x2{ra[j].code.x, ra[j].code.y}, ra[j].scale, most);
+            to[1] = decode<D>(u32x2{ra[j].code.z, ra[j].code.w}, ra[j].scale, most);
         }
 #pragma unroll
         for (int j = 0; j < C::b_chunks; ++j) {
@@ -344,9 +465,9 @@ __global__ __launch_bounds__(C::threads) void weight_grad_kernel(const GemmArgs 
         for (int m = 0; m < C::MI; ++m) acc[m][i] = f32x4{};
     }
     const bool bias = a.w.bias && k0 == 0 && wm == 0;
-    bf16x8 ones;
+    s16x8 ones;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ones[i] = __bf16(1.0f);
+    for (int i = 0; i < 8; ++i) ones[i] = Op<D>::one;
 
     // where the lane's fragments are
     const int row = 4 * (lane >> 4) + ((lane & 15) >> 2);
@@ -368,7 +489,7 @@ __global__ __launch_bounds__(C::threads) void weight_grad_kernel(const GemmArgs 
         const uint32_t buf = uint32_t(s & 1) * C::stage;
 #pragma unroll
         for (int h = 0; h < C::STEP / 32; ++h) {
-            bf16x8 fa[C::MI], fb[C::NI];
+            s16x8 fa[C::MI], fb[C::NI];
 #pragma unroll
             for (int m = 0; m < C::MI; ++m) fa[m] = fragment(at_a[m] + buf + h * 32 * C::BM * 2, C::BM * 2);
 #pragma unroll
@@ -380,24 +501,27 @@ __global__ __launch_bounds__(C::threads) void weight_grad_kernel(const GemmArgs 
                 for (int i = 0; i < C::NI; ++i)
 #pragma unroll
                     for (int m = 0; m < C::MI; ++m)
-                        acc[m][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[m], fb[i], acc[m][i], 0, 0, 0);
+                        acc[m][i] = Op<D>::multiply(fa[m], fb[i], acc[m][i]);
                 if (bias)
 #pragma unroll
                     for (int i = 0; i < C::NI; ++i)
-                        sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, fb[i], sum[i], 0, 0, 0);
+                        sum[i] = Op<D>::multiply(ones, fb[i], sum[i]);
             }
         }
         if (s + 1 < steps) stash((s + 1) & 1);
         __syncthreads();
     }
 
-    finish<C>(a, part, lds, acc);
+    int power[C::MI / 2];
+#pragma unroll
+    for (int m = 0; m < C::MI / 2; ++m) power[m] = Op<D>::kScaled ? int(top[wm * (C::MI / 2) + m]) - kTop : 0;
+    finish<C, Op<D>::kScaled>(a, part, lds, acc, power);
     if (bias)
 #pragma unroll
-        for (int i = 0; i < C::NI; ++i) finish_bias(a, part, n0 + (wn * C::NI + i) * 16, sum[i][0]);
+        for (int i = 0; i < C::NI; ++i) finish_bias(a, part, (wn * C::NI + i) * 16, sum[i][0]);
 }
 
-// The same for a dy of bf16 that is aligned to 16 bytes: four waves of 128 x 128
+// The same for a dy of 16 bits that is aligned to 16 bytes: four waves of 128 x 128
 // outputs, one to a SIMD.
 //
 // A phase is 32 tokens: 64 products of a wave, 16 cycles each on its matrix unit,
@@ -416,7 +540,7 @@ __device__ __forceinline__ void each(std::integer_sequence<int, I...>, const F& 
 }
 
 struct Fast {
-    static constexpr int BM = 256, BN = 256, WM = 2, WN = 2, STEP = 64, MI = 8, NI = 8, threads = 256, G = 4;
+    static constexpr int BM = kTile, BN = kTile, WM = 2, WN = 2, MI = 8, NI = 8, threads = 256, G = 4;
     static constexpr int rows = 32;                               // of a phase
     static constexpr int a_bytes = rows * BM * 2, b_bytes = rows * BN * 2, code_bytes = rows * BM, scale_bytes = rows * 8 * 4;
     static constexpr int a_ring = 2, b_ring = 5, code_ring = 5, turn = 10;
@@ -437,19 +561,24 @@ __device__ __forceinline__ void load1(uint32_t to, uint32_t from, u32x4 buffer) 
     asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_ubyte %2, %3, 0 offen lds" ::"s"(to), "i"(kOffset), "v"(from), "s"(buffer) : "scc");
 }
 
-// c += a b, in place.
-__device__ __forceinline__ void multiply_v(f32x4& c, const bf16x8& a, const bf16x8& b) {
-    asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
-}
-
-template <int kSums>
+template <int D, int kSums>
 __global__ __launch_bounds__(256, 1) void weight_grad_fast_kernel(const GemmArgs a) {
     typedef Fast C;
     __shared__ __attribute__((aligned(1024))) char lds[C::lds_bytes];
     const int tid = int(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / C::WN, wn = wave % C::WN;
-    const Part part = part_of<C>(a);
+    const Part part = part_of(a);
     const int64_t k0 = part.k0, n0 = part.n0, t_begin = part.t_begin;
+    uint32_t* const tops = reinterpret_cast<uint32_t*>(lds);   // until the loads come
+    uint32_t top = 0;
+    int power[C::MI / 2] = {};
+    if (Op<D>::kScaled) {
+        largest_scales<C::threads>(a, part, tops);
+        top = tops[(tid & 15) >> 1];   // of the columns that the thread decodes
+#pragma unroll
+        for (int m = 0; m < C::MI / 2; ++m) power[m] = __builtin_amdgcn_readfirstlane(int(tops[wm * (C::MI / 2) + m]) - kTop);
+        __syncthreads();
+    }
     const int tokens = int(part.t_end - part.t_begin), phases = (tokens + C::rows - 1) / C::rows;
     const uint32_t lds0 = uint32_t(reinterpret_cast<uintptr_t>((Shared<char>*)lds));
 
@@ -503,13 +632,6 @@ __global__ __launch_bounds__(256, 1) void weight_grad_fast_kernel(const GemmArgs
     const auto raw_scale = [&](int j, int slot) {
         return *(Shared<const uint32_t>*)uintptr_t(scale_from + slot * C::scale_bytes + j * 512);
     };
-    const auto decoded = [&](u32x2 code, uint32_t scale) {
-        const float f = number(scale << 23);
-        return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code.x, f, false)),
-                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code.x, f, true)),
-                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code.y, f, false)),
-                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code.y, f, true))};
-    };
     const auto place_codes = [&](u32x4 v, int j, int h, int buf) {
         *(Shared<u32x4>*)uintptr_t((code_to ^ (16 * h)) + buf * C::a_bytes + j * 16 * 512) = v;
     };
@@ -522,7 +644,7 @@ __global__ __launch_bounds__(256, 1) void weight_grad_fast_kernel(const GemmArgs
         at_a[m] = at + wm * 256;
         at_b[m] = at + C::b_at + wn * 256;
     }
-    struct Frags { bf16x8 a[C::MI], b[C::NI]; };
+    struct Frags { s16x8 a[C::MI], b[C::NI]; };
     const auto read = [&](Frags& f, int i, int buf, int slot) {   // its 16 fragments, in the order of their use
         if (i < 8) f.a[i] = fragment(at_a[i] + buf * C::a_bytes, 512);
         else f.b[i - 8] = fragment(at_b[i - 8] + slot * C::b_bytes, 512);
@@ -533,8 +655,8 @@ __global__ __launch_bounds__(256, 1) void weight_grad_fast_kernel(const GemmArgs
     for (int i = 0; i < C::NI; ++i)
 #pragma unroll
         for (int m = 0; m < C::MI; ++m) acc[m][i] = f32x4{};
-    const auto multiply = [&](const Frags& f, int j) {   // in place: the compiler's own would move sums about
-        asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc[j & 7][j >> 3]) : "v"(f.a[j & 7]), "v"(f.b[j >> 3]));
+    const auto multiply = [&](const Frags& f, int j) {
+        Op<D>::multiply_a(acc[j & 7][j >> 3], f.a[j & 7], f.b[j >> 3]);
         __builtin_amdgcn_sched_barrier(0);
     };
 
@@ -543,9 +665,9 @@ __global__ __launch_bounds__(256, 1) void weight_grad_fast_kernel(const GemmArgs
     // the last share takes the last one too and drops it.
     const int share = (int(k0 / C::BM) * 2 + wm) * kSums, first = min(share, C::NI - kSums);
     f32x4 sum[kSums + 1];
-    bf16x8 ones, fb[kSums + 1];
+    s16x8 ones, fb[kSums + 1];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ones[i] = __bf16(1.0f);
+    for (int i = 0; i < 8; ++i) ones[i] = Op<D>::one;
     uint32_t at_sum[kSums + 1];
 #pragma unroll
     for (int i = 0; i < kSums; ++i) {
@@ -568,7 +690,7 @@ __global__ __launch_bounds__(256, 1) void weight_grad_fast_kernel(const GemmArgs
                 rs[j] = raw_scale(j, (Q + 2) % C::code_ring);
             }
             if constexpr (j >= 2 && j < 50 && j % 3 == 2) read(g, (j - 2) / 3, (Q + 1) % 2, (Q + 1) % C::b_ring);
-            if constexpr (j >= 16 && j < 40 && j % 6 == 4) d = decoded(raws[(j - 16) / 12][(j - 16) / 6 % 2], rs[(j - 16) / 12]);
+            if constexpr (j >= 16 && j < 40 && j % 6 == 4) d = decode<D>(raws[(j - 16) / 12][(j - 16) / 6 % 2], rs[(j - 16) / 12], top);
             if constexpr (j >= 16 && j < 40 && j % 6 == 0) place_codes(d, (j - 16) / 12, (j - 16) / 6 % 2, Q % 2);
             if constexpr (j >= 40 && j < 52 && j % 3 == 1) load16<(Q + 4) % C::b_ring * C::b_bytes + (j - 40) / 3 * 1024>(to_b, from_b[(j - 40) / 3], dy.buffer());
             if constexpr (j == 52 || j == 55) load16<Q % C::code_ring * C::code_bytes + (j - 52) / 3 * 1024>(to_code, from_code[(j - 52) / 3], codes.buffer());
@@ -579,7 +701,7 @@ __global__ __launch_bounds__(256, 1) void weight_grad_fast_kernel(const GemmArgs
             if constexpr (j >= 12 && j < 12 + 4 * kSums && j % 4 == 0)
                 fb[(j - 12) / 4] = fragment(at_sum[(j - 12) / 4] + Q % C::b_ring * C::b_bytes, 512);
             if constexpr (j >= 44 && j < 44 + 4 * kSums && j % 4 == 0)
-                multiply_v(sum[(j - 44) / 4], ones, fb[(j - 44) / 4]);
+                Op<D>::multiply_v(sum[(j - 44) / 4], ones, fb[(j - 44) / 4]);
         });
         __builtin_amdgcn_s_waitcnt(0x0F70 | 14);   // all loads but the last two phases'
         __syncthreads();
@@ -609,7 +731,7 @@ __global__ __launch_bounds__(256, 1) void weight_grad_fast_kernel(const GemmArgs
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) place_codes(decoded(raw(j, h, p), raw_scale(j, p)), j, h, p);
+            for (int h = 0; h < 2; ++h) place_codes(decode<D>(raw(j, h, p), raw_scale(j, p), top), j, h, p);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 16; ++i) read(f0, i, 0, 0);
@@ -623,109 +745,135 @@ __global__ __launch_bounds__(256, 1) void weight_grad_fast_kernel(const GemmArgs
         __builtin_amdgcn_sched_barrier(0);
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);   // no load comes into what follows
-    finish<C>(a, part, lds, acc);
+    finish<C, Op<D>::kScaled>(a, part, lds, acc, power);
 #pragma unroll
     for (int i = 0; i < kSums; ++i)
-        if (share < C::NI) finish_bias(a, part, n0 + (wn * 8 + first + i) * 16, sum[i][0]);
+        if (share < C::NI) finish_bias(a, part, (wn * 8 + first + i) * 16, sum[i][0]);
 }
 
-// Adds up the splits' sums, in order: four neighbouring elements a thread.
-constexpr int kJoinThreads = 256;
+// Adds up the splits' sums of a tile, in order: four neighbouring elements a thread.
+constexpr int kJoinThreads = 256, kJoinBlocks = kTile * kTile / 4 / kJoinThreads;   // blocks of a tile
 template <int DO>
 __global__ __launch_bounds__(kJoinThreads) void split_join_kernel(const GemmArgs a) {
-    typedef typename Type<DO>::elem E;
-    const int64_t cols = a.w.transposed ? a.w.n : a.w.k, rows = a.w.transposed ? a.w.k : a.w.n;
-    const int64_t fours = a.ld_part / 4, i = int64_t(blockIdx.x) * kJoinThreads + threadIdx.x;
-    if (i < rows * fours) {
-        const int64_t r = i / fours, c = (i - r * fours) * 4;
-        f32x4 v = *(Global<const f32x4>*)(a.part + r * a.ld_part + c);
-        for (int s = 1; s < a.splits; ++s) v += *(Global<const f32x4>*)(a.part + s * a.part_size + r * a.ld_part + c);
+    typedef Four<DO> F;
+    typedef typename F::E E;
+    const uint32_t i = blockIdx.x / kJoinBlocks, x = (blockIdx.x % kJoinBlocks) * kJoinThreads + threadIdx.x;
+    const uint32_t tile = uint32_t(a.whole) + i;
+    const uint32_t group = tile / (kGroup * a.tiles_k), rest = tile - group * (kGroup * a.tiles_k);
+    const uint32_t wide = a.tiles_n - group * kGroup < kGroup ? a.tiles_n - group * kGroup : kGroup, tile_k = rest / wide;
+    const int64_t k0 = int64_t(tile_k) * kTile, n0 = int64_t(group * kGroup + rest - tile_k * wide) * kTile;
+    const float* part = a.part + int64_t(i) * a.splits * kPart;
+    const int64_t rows = a.w.transposed ? a.w.k : a.w.n, cols = a.w.transposed ? a.w.n : a.w.k;
+    const int64_t r = (a.w.transposed ? k0 : n0) + x / (kTile / 4), c = (a.w.transposed ? n0 : k0) + x % (kTile / 4) * 4;
+    if (r < rows && c < cols) {
+        f32x4 v = *(Global<const f32x4>*)(part + 4 * x);
+#pragma unroll 8
+        for (int s = 1; s < a.splits; ++s) v += *(Global<const f32x4>*)(part + s * kPart + 4 * x);
         Global<E>* p = (Global<E>*)a.w.dw + r * a.w.s_dw + c;
+        if (c + 4 <= cols) {
+            typename F::vec y = {};
+            if (a.w.accumulate) y = *(Global<typename F::at>*)p;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (c + j < cols) {
-                if constexpr (DO == ZERO_DTYPE_FP32) p[j] = a.w.accumulate ? p[j] + v[j] : v[j];
-                else p[j] = Type<DO>::narrow(a.w.accumulate ? Type<DO>::wide(p[j]) + v[j] : v[j]);
-            }
+            for (int j = 0; j < 4; ++j) y[j] = F::narrow(a.w.accumulate ? F::wide(y[j]) + v[j] : v[j]);
+            *(Global<typename F::at>*)p = y;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + j < cols) p[j] = F::narrow(a.w.accumulate ? F::wide(p[j]) + v[j] : v[j]);
+        }
     }
-    if (a.w.bias && i < a.w.n) {
-        float v = ((Global<const float>*)a.part_bias)[i];
-        for (int s = 1; s < a.splits; ++s) v += ((Global<const float>*)a.part_bias)[s * a.w.n + i];
-        put_bias<DO>(a, i, v);
+    if (a.w.bias && blockIdx.x % kJoinBlocks == 0 && n0 + threadIdx.x < a.w.n) {
+        const uint32_t fragment = threadIdx.x / 16 % 8;
+        if (tile_k != (a.shares ? fragment / uint32_t(2 * a.shares) : 0)) return;
+        float v = ((Global<const float>*)part)[kTile * kTile + threadIdx.x];
+        for (int s = 1; s < a.splits; ++s) v += ((Global<const float>*)part)[s * kPart + kTile * kTile + threadIdx.x];
+        put_bias<DO>(a, n0 + threadIdx.x, v);
     }
 }
 
-// How a product is cut: tiles of 256 by `bn` outputs, and splits of the tokens
-// where there are fewer tiles than CUs.
+// How a product is cut.  One block runs on a CU at a time, so tiles beyond a multiple of the
+// CUs would cost a round that leaves most of them idle: those are split by tokens, and
+// another kernel adds their parts up.  The times are those of one MI355X: a tile takes
+// `fixed` us and `step` us for kUnit tokens, the other kernel 5 us and its bytes at 4.5 TB/s
+// (13B matrix, 1600 tiles: 1443 us in seven rounds, 1320 with the last 64 split).
 constexpr int kCUs = 256;
 struct Cut {
-    int32_t tiles_k, tiles_n, splits;
-    int64_t per_split, ld_part, part_size, bytes;
+    int32_t tiles_k, tiles_n, whole, splits;
+    int64_t per_split;
+    int64_t blocks() const { return whole + (int64_t(tiles_k) * tiles_n - whole) * splits; }
+    int64_t bytes() const { return splits > 1 ? (int64_t(tiles_k) * tiles_n - whole) * splits * kPart * 4 : 0; }
 };
-Cut cut_for(int64_t T, int64_t n, int64_t k, int bn, int step) {
+Cut cut_for(int64_t T, int64_t n, int64_t k, int32_t dy_type) {
+    const double fixed = 9, step = dy_type == ZERO_DTYPE_FP32 ? 4.2 : 1.35, join = 5, part = kPart * 4 / 4.5e6;
     Cut c;
-    c.tiles_k = k > 0 ? int32_t((k + 255) / 256) : 1;   // the bias needs a tile
-    c.tiles_n = int32_t((n + bn - 1) / bn);
-    const int64_t tiles = int64_t(c.tiles_k) * c.tiles_n, steps = (T + step - 1) / step;
-    int64_t best = 1, best_cost = -1;
-    for (int64_t s = 1; s <= 64 && (s == 1 || (s <= steps / 4 && tiles * s <= 2 * kCUs)); ++s) {
-        const int64_t per = (steps + s - 1) / s;
-        const int64_t cost = ((tiles * s + kCUs - 1) / kCUs) * (per + 4) * 100 + (s > 1 ? 800 + 20 * s : 0);
-        if (best_cost < 0 || cost < best_cost) {
-            best = s;
-            best_cost = cost;
+    c.tiles_k = k > 0 ? int32_t((k + kTile - 1) / kTile) : 1;   // the bias needs a tile
+    c.tiles_n = int32_t((n + kTile - 1) / kTile);
+    const int64_t tiles = int64_t(c.tiles_k) * c.tiles_n, units = (T + kUnit - 1) / kUnit, rest = tiles % kCUs;
+    c.whole = int32_t(tiles);
+    c.splits = 1;
+    c.per_split = units * kUnit;
+    if (rest == 0) return c;
+    double best = fixed + step * double(units);
+    // at most 2 rounds of blocks, of 4 units at least
+    for (int64_t s = 2; s <= 64 && rest * s <= 2 * kCUs && 4 * s <= units; ++s) {
+        int64_t per = (units + s - 1) / s;
+        per = (per + 4) / 5 * 5;   // the fast kernel goes by 5 of them
+        const int64_t used = (units + per - 1) / per;
+        if (used < 2) continue;
+        const double cost = double((rest * used + kCUs - 1) / kCUs) * (fixed + step * double(per)) + join + double(rest * used) * part;
+        if (cost < best) {
+            best = cost;
+            c.whole = int32_t(tiles - rest);
+            c.splits = int32_t(used);
+            c.per_split = per * kUnit;
         }
-    }
-    c.per_split = steps > 0 ? (steps + best - 1) / best : 0;
-    c.splits = steps > 0 ? int32_t((steps + c.per_split - 1) / c.per_split) : 1;
-    c.ld_part = 0;
-    c.part_size = c.bytes = 0;
-    if (c.splits > 1) {
-        // either way round
-        const int64_t a = n * ((k + 3) / 4 * 4), b = k * ((n + 3) / 4 * 4);
-        c.part_size = a > b ? a : b;
-        c.bytes = 4 * c.splits * (c.part_size + n);
     }
     return c;
 }
 
 // Whether the loads of the fast kernel reach everything: 16 bytes of dy at a time,
-// whole words up to the last value, offsets of 31 bits inside a split's `tokens`.
+// whole words up to the last value, offsets of 31 bits inside a block's `tokens`;
+// and whether there are tokens enough for a turn of its loop.
 bool fast(const WeightGradLaunch& w, int64_t tokens) {
     constexpr int64_t most = int64_t(1) << 31;
-    return tokens > 0 && tokens < most && reinterpret_cast<uintptr_t>(w.dy) % 16 == 0 && w.s_dy % 8 == 0 && w.s_dy >= w.n && w.n % 2 == 0 &&
-           w.s_dy < most / 64 && tokens * w.s_dy < most / 2 && w.k < most / 64 && tokens * (w.k + 32) < most;
+    return tokens > 3 * kUnit && tokens < most && reinterpret_cast<uintptr_t>(w.dy) % 16 == 0 && w.s_dy % 8 == 0 && w.s_dy >= w.n &&
+           w.n % 2 == 0 && w.s_dy < most / 64 && tokens * w.s_dy < most / 2 && w.k < most / 64 && tokens * (w.k + 32) < most;
+}
+
+template <int D>
+void run_fast(const GemmArgs& a, dim3 blocks, hipStream_t s, const KernelEvents& ev) {
+    switch (a.shares) {
+        case 0: launch(weight_grad_fast_kernel<D, 0>, blocks, Fast::threads, s, ev, a); break;
+        case 1: launch(weight_grad_fast_kernel<D, 1>, blocks, Fast::threads, s, ev, a); break;
+        case 2: launch(weight_grad_fast_kernel<D, 2>, blocks, Fast::threads, s, ev, a); break;
+        default: launch(weight_grad_fast_kernel<D, 4>, blocks, Fast::threads, s, ev, a); break;
+    }
 }
 
 template <typename C>
 hipError_t run(const WeightGradLaunch& w, hipStream_t s, const KernelEvents& ev) {
-    const Cut c = cut_for(w.T, w.n, w.k, C::BN, C::STEP);
+    const Cut c = cut_for(w.T, w.n, w.k, w.dy_type);
     GemmArgs a = {};
     a.w = w;
     a.blocks = (w.k + 31) / 32;
     a.pitch = 32 * a.blocks;
     a.tiles_k = c.tiles_k;
     a.tiles_n = c.tiles_n;
+    a.whole = c.whole;
     a.splits = c.splits;
     a.per_split = c.per_split;
-    a.part_size = c.part_size;
-    a.ld_part = ((w.transposed ? w.n : w.k) + 3) / 4 * 4;
     a.part = w.work;
-    a.part_bias = c.splits > 1 ? w.work + c.splits * c.part_size : nullptr;
     KernelEvents one = {ev.start, c.splits > 1 ? nullptr : ev.stop};
-    const dim3 blocks(uint32_t(int64_t(c.tiles_k) * c.tiles_n * c.splits));
-    if (C::D == ZERO_DTYPE_BF16 && fast(w, c.per_split * C::STEP)) {
-        if (!w.bias) launch(weight_grad_fast_kernel<0>, blocks, Fast::threads, s, one, a);
-        else if (c.tiles_k >= 4) launch(weight_grad_fast_kernel<1>, blocks, Fast::threads, s, one, a);
-        else if (c.tiles_k >= 2) launch(weight_grad_fast_kernel<2>, blocks, Fast::threads, s, one, a);
-        else launch(weight_grad_fast_kernel<4>, blocks, Fast::threads, s, one, a);
-    } else launch(weight_grad_kernel<C>, blocks, C::threads, s, one, a);
+    const dim3 blocks{uint32_t(c.blocks())};
+    if (C::D != ZERO_DTYPE_FP32 && fast(w, c.whole > 0 ? w.T : c.per_split)) {
+        a.shares = !w.bias ? 0 : c.tiles_k >= 4 ? 1 : c.tiles_k >= 2 ? 2 : 4;
+        if constexpr (C::D != ZERO_DTYPE_FP32) run_fast<C::D>(a, blocks, s, one);
+    } else {
+        launch(weight_grad_kernel<C>, blocks, C::threads, s, one, a);
+    }
     if (c.splits > 1) {
         one = {nullptr, ev.stop};
-        const int64_t rows = w.transposed ? w.k : w.n;
-        int64_t items = rows * (a.ld_part / 4);
-        if (w.bias && items < w.n) items = w.n;
-        const dim3 grid(uint32_t((items + kJoinThreads - 1) / kJoinThreads));
+        const dim3 grid(uint32_t((int64_t(c.tiles_k) * c.tiles_n - c.whole) * kJoinBlocks));
         if (w.out_type == ZERO_DTYPE_FP16) launch(split_join_kernel<ZERO_DTYPE_FP16>, grid, kJoinThreads, s, one, a);
         else if (w.out_type == ZERO_DTYPE_BF16) launch(split_join_kernel<ZERO_DTYPE_BF16>, grid, kJoinThreads, s, one, a);
         else launch(split_join_kernel<ZERO_DTYPE_FP32>, grid, kJoinThreads, s, one, a);
@@ -733,22 +881,14 @@ hipError_t run(const WeightGradLaunch& w, hipStream_t s, const KernelEvents& ev)
     return hipGetLastError();
 }
 
-typedef Config<ZERO_DTYPE_BF16, 256, 2, 4, 64> Bf16;
-typedef Config<ZERO_DTYPE_FP16, 128, 4, 2, 64> Fp16;
-typedef Config<ZERO_DTYPE_FP32, 256, 2, 4, 32> Fp32;
-
 }  // namespace
 
-int64_t weight_grad_work(int64_t T, int64_t n, int64_t k, int32_t dy_type) {
-    if (dy_type == ZERO_DTYPE_BF16) return cut_for(T, n, k, Bf16::BN, Bf16::STEP).bytes;
-    if (dy_type == ZERO_DTYPE_FP16) return cut_for(T, n, k, Fp16::BN, Fp16::STEP).bytes;
-    return cut_for(T, n, k, Fp32::BN, Fp32::STEP).bytes;
-}
+int64_t weight_grad_work(int64_t T, int64_t n, int64_t k, int32_t dy_type) { return cut_for(T, n, k, dy_type).bytes(); }
 
 hipError_t launch_weight_grad(const WeightGradLaunch& w, hipStream_t s, const KernelEvents& ev) {
-    if (w.dy_type == ZERO_DTYPE_BF16) return run<Bf16>(w, s, ev);
-    if (w.dy_type == ZERO_DTYPE_FP16) return run<Fp16>(w, s, ev);
-    return run<Fp32>(w, s, ev);
+    if (w.dy_type == ZERO_DTYPE_BF16) return run<Config<ZERO_DTYPE_BF16, 64>>(w, s, ev);
+    if (w.dy_type == ZERO_DTYPE_FP16) return run<Config<ZERO_DTYPE_FP16, 64>>(w, s, ev);
+    return run<Config<ZERO_DTYPE_FP32, 32>>(w, s, ev);
 }
 
 }  // namespace zp
