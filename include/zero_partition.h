@@ -715,7 +715,7 @@ int zero_embedding_lookup(const zero_matrix* table, const void* tokens, int32_t 
  *   dtable[r] = scale * (sum of dy[i] over the i with tokens[i] - first == r)
  * added to what is there when accumulate is 1 (rows without a token are not
  * touched then, and are zeros otherwise).  Tokens are sorted, each row's sum is
- * taken in fp32 in an order fixed by how often it is named, and rounded once.
+ * taken in fp32 in an order fixed by the tokens, and rounded once.
  *   dy           one row for each token, at most 2^30
  *   dtable       at most 2^30 rows
  *   work         device, zero_embedding_grad_work_bytes() bytes, 16-byte aligned,

@@ -86,27 +86,42 @@ __device__ __forceinline__ uint32_t key_of(const SortArgs& a, int64_t i) {
 }
 
 // Few tokens: each one's place is how many keys are smaller, or equal and before
-// it.  8 threads count for a token, 32 tokens a block; n^2 comparisons, but one
-// launch (8192 tokens: measured below at its launch), where digit by digit takes four.
+// it.  16 threads count for a token, 32 tokens a block: n^2 comparisons, but one
+// launch where digit by digit takes four that wait for each other.
 constexpr int64_t kRankMost = 8192;
-constexpr int kRankTokens = kThreads / 8;
+constexpr int kRankThreads = 512, kRankShare = 16, kRankTokens = kRankThreads / kRankShare;
 template <typename I>
-__global__ __launch_bounds__(kThreads) void rank_kernel(const SortArgs a) {
-    __shared__ uint32_t keys[kRankMost];
-    const int n = int(a.n), tid = int(threadIdx.x);
-    for (int j = tid; j < n; j += kThreads) keys[j] = key_of<I>(a, j);
-    __syncthreads();
-    const int i = int(blockIdx.x) * kRankTokens + (tid >> 3);
-    const int part = tid & 7;
-    const uint32_t mine = i < n ? keys[i] : 0;
-    int rank = 0;
-    for (int j = part; j < n; j += 8) {
-        const uint32_t k = keys[j];
-        rank += (k < mine || (k == mine && j < i)) ? 1 : 0;
+__global__ __launch_bounds__(kRankThreads) void rank_kernel(const SortArgs a) {
+    __shared__ u32x4 keys[kRankMost / 4];
+    const int n = int(a.n), tid = int(threadIdx.x), fours = (n + 3) / 4;
+    uint32_t* flat = reinterpret_cast<uint32_t*>(keys);
+    constexpr int ahead = 8;
+    for (int j0 = tid; j0 < 4 * fours; j0 += ahead * kRankThreads) {
+        uint32_t k[ahead];
+#pragma unroll
+        for (int u = 0; u < ahead; ++u) k[u] = j0 + u * kRankThreads < n ? key_of<I>(a, j0 + u * kRankThreads) : 0xFFFFFFFFu;   // above all keys
+#pragma unroll
+        for (int u = 0; u < ahead; ++u)
+            if (j0 + u * kRankThreads < 4 * fours) flat[j0 + u * kRankThreads] = k[u];
     }
-    rank += __shfl_xor(rank, 1);
-    rank += __shfl_xor(rank, 2);
-    rank += __shfl_xor(rank, 4);
+    __syncthreads();
+    const int first = int(blockIdx.x) * kRankTokens, i = first + tid / kRankShare, part = tid % kRankShare;
+    const uint32_t mine = i < n ? flat[i] : 0;
+    int rank = 0;
+    // fours before the block's tokens (first is one's start), its own, and those after
+    const int lo = first / 4, hi = min(lo + kRankTokens / 4, fours);
+    const auto count = [&](int j, auto f) {
+        const u32x4 k = keys[j];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) rank += f(k[q], 4 * j + q) ? 1 : 0;
+    };
+#pragma unroll 4
+    for (int j = part; j < lo; j += kRankShare) count(j, [&](uint32_t k, int) { return k <= mine; });
+    for (int j = lo + part; j < hi; j += kRankShare) count(j, [&](uint32_t k, int at) { return k < mine || (k == mine && at < i); });
+#pragma unroll 4
+    for (int j = hi + part; j < fours; j += kRankShare) count(j, [&](uint32_t k, int) { return k < mine; });
+#pragma unroll
+    for (int h = 1; h < kRankShare; h *= 2) rank += __shfl_xor(rank, h);
     if (part == 0 && i < n) {
         a.key[rank] = mine;
         a.order[rank] = uint32_t(i);
@@ -123,31 +138,46 @@ constexpr int kSortWaves = kThreads / 64;
 constexpr int64_t kMaxSortBlocks = 256;
 struct DigitArgs {
     SortArgs s;
-    const uint32_t* in_key;     // NULL in the first pass: from the tokens
+    const uint32_t* in_key;     // not in the first pass, which takes the tokens
     const uint32_t* in_order;
     uint32_t* count;            // blocks x digits
-    int64_t part;               // elements of a block, a multiple of kThreads
+    int64_t part;               // elements of a block, a multiple of 4 kThreads
     int32_t blocks, shift, digits;   // digits: a power of two
 };
 
-template <typename I>
-__device__ __forceinline__ uint32_t digit_key(const DigitArgs& a, int64_t i) {
-    return a.in_key ? ((Global<const uint32_t>*)a.in_key)[i] : key_of<I>(a.s, i);
+// Four elements of a lane, 64 apart; those from hi on are no elements.  One branch-free
+// batch of loads.
+constexpr int kSortAhead = 4;
+template <typename I, bool kFirst>
+__device__ __forceinline__ void digit_load(const DigitArgs& a, int64_t i0, int64_t hi, uint32_t k[kSortAhead]) {
+#pragma unroll
+    for (int u = 0; u < kSortAhead; ++u) {
+        const int64_t i = i0 + 64 * u < hi ? i0 + 64 * u : hi - 1;   // hi > i0 of the wave's first lane
+        if constexpr (kFirst) k[u] = key_of<I>(a.s, i);
+        else k[u] = ((Global<const uint32_t>*)a.in_key)[i];
+    }
 }
 
-template <typename I>
+template <typename I, bool kFirst>
 __global__ __launch_bounds__(kThreads) void digit_count_kernel(const DigitArgs a) {
     __shared__ uint32_t count[kMaxDigits];
     for (int d = threadIdx.x; d < a.digits; d += kThreads) count[d] = 0;
     __syncthreads();
-    const int64_t lo = int64_t(blockIdx.x) * a.part, hi = lo + a.part < a.s.n ? lo + a.part : a.s.n;
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads)
-        atomicAdd(&count[(digit_key<I>(a, i) >> a.shift) & (a.digits - 1)], 1u);
+    const int wave = int(threadIdx.x) >> 6, lane = int(threadIdx.x) & 63;
+    const int64_t quarter = a.part / kSortWaves, lo = int64_t(blockIdx.x) * a.part + wave * quarter;
+    const int64_t hi = lo + quarter < a.s.n ? lo + quarter : a.s.n;
+    for (int64_t i0 = lo; i0 < hi; i0 += 64 * kSortAhead) {
+        uint32_t k[kSortAhead];
+        digit_load<I, kFirst>(a, i0 + lane, hi, k);
+#pragma unroll
+        for (int u = 0; u < kSortAhead; ++u)
+            if (i0 + 64 * u + lane < hi) atomicAdd(&count[(k[u] >> a.shift) & (a.digits - 1)], 1u);
+    }
     __syncthreads();
     for (int d = threadIdx.x; d < a.digits; d += kThreads) a.count[int64_t(blockIdx.x) * a.digits + d] = count[d];
 }
 
-template <typename I>
+template <typename I, bool kFirst>
 __global__ __launch_bounds__(kThreads) void digit_move_kernel(const DigitArgs a) {
     __shared__ uint32_t next[kSortWaves][kMaxDigits];   // where a wave's next element with the digit goes
     __shared__ uint32_t total[kMaxDigits];
@@ -155,25 +185,38 @@ __global__ __launch_bounds__(kThreads) void digit_move_kernel(const DigitArgs a)
     const int64_t quarter = a.part / kSortWaves;
     const int64_t lo = int64_t(blockIdx.x) * a.part + wave * quarter;
     const int64_t hi = lo + quarter < a.s.n ? lo + quarter : a.s.n;
-    for (int d = tid; d < a.digits; d += kThreads) {
-        uint32_t before = 0, all = 0;
-        for (int b = 0; b < a.blocks; ++b) {
-            const uint32_t c = a.count[int64_t(b) * a.digits + d];
-            before += b < int(blockIdx.x) ? c : 0;
-            all += c;
-        }
-        total[d] = all;
+    for (int d = tid; d < a.digits; d += kThreads)
 #pragma unroll
-        for (int w = 0; w < kSortWaves; ++w) next[w][d] = w == 0 ? before : 0;
-    }
+        for (int w = 0; w < kSortWaves; ++w) next[w][d] = 0;
     __syncthreads();
     // each wave's counts, for the waves after it
-    for (int64_t i = lo + lane; i < hi; i += 64) {
-        const uint32_t d = (digit_key<I>(a, i) >> a.shift) & (a.digits - 1);
-        for (int w = wave + 1; w < kSortWaves; ++w) atomicAdd(&next[w][d], 1u);
+    for (int64_t i0 = lo; i0 < hi; i0 += 64 * kSortAhead) {
+        uint32_t k[kSortAhead];
+        digit_load<I, kFirst>(a, i0 + lane, hi, k);
+#pragma unroll
+        for (int u = 0; u < kSortAhead; ++u)
+            if (i0 + 64 * u + lane < hi)
+                for (int w = wave + 1; w < kSortWaves; ++w) atomicAdd(&next[w][(k[u] >> a.shift) & (a.digits - 1)], 1u);
     }
-    // sums of the lower digits, by one wave: 64 digits at a time
+    // the earlier blocks' counts, and all blocks'
+    for (int d = tid; d < a.digits; d += kThreads) {
+        uint32_t before = 0, all = 0;
+        constexpr int ahead = 16;   // loads at once
+        for (int b0 = 0; b0 < a.blocks; b0 += ahead) {
+            uint32_t c[ahead];
+#pragma unroll
+            for (int j = 0; j < ahead; ++j) c[j] = a.count[int64_t(min(b0 + j, a.blocks - 1)) * a.digits + d];
+#pragma unroll
+            for (int j = 0; j < ahead; ++j) {
+                before += b0 + j < int(blockIdx.x) ? c[j] : 0;
+                all += b0 + j < a.blocks ? c[j] : 0;
+            }
+        }
+        total[d] = all;
+        next[0][d] = before;   // nothing is counted there
+    }
     __syncthreads();
+    // sums of the lower digits, by one wave: 64 digits at a time
     if (wave == 0) {
         uint32_t below = 0;
         for (int d0 = 0; d0 < a.digits; d0 += 64) {
@@ -197,26 +240,35 @@ __global__ __launch_bounds__(kThreads) void digit_move_kernel(const DigitArgs a)
         next[0][d] = first;
     }
     __syncthreads();
-    for (int64_t i0 = lo; i0 < hi; i0 += 64) {   // wave-uniform bounds
-        const int64_t i = i0 + lane;
-        const bool there = i < hi;
-        const uint32_t key = there ? digit_key<I>(a, i) : 0;
-        const uint32_t d = (key >> a.shift) & (a.digits - 1);
-        // lanes with the same digit
-        uint64_t same = __ballot(there);
-        for (int bit = 1; bit < a.digits; bit *= 2) {
-            const uint64_t with = __ballot((d & bit) != 0);
-            same &= (d & bit) ? with : ~with;
+    for (int64_t i0 = lo; i0 < hi; i0 += 64 * kSortAhead) {   // wave-uniform bounds
+        uint32_t k[kSortAhead], o[kSortAhead];
+        digit_load<I, kFirst>(a, i0 + lane, hi, k);
+#pragma unroll
+        for (int u = 0; u < kSortAhead; ++u) {
+            const int64_t i = i0 + 64 * u + lane;
+            if constexpr (kFirst) o[u] = uint32_t(i);
+            else o[u] = ((Global<const uint32_t>*)a.in_order)[i < hi ? i : hi - 1];
         }
-        uint32_t to = 0;
-        const int before = __popcll(same & ((uint64_t(1) << lane) - 1));
-        if (there) to = next[wave][d] + before;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (there && (same >> lane) == 1) next[wave][d] += before + 1;   // the last of them
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (there) {
-            a.s.key[to] = key;
-            a.s.order[to] = a.in_order ? a.in_order[i] : uint32_t(i);
+#pragma unroll
+        for (int u = 0; u < kSortAhead; ++u) {
+            const bool there = i0 + 64 * u + lane < hi;
+            const uint32_t d = (k[u] >> a.shift) & (a.digits - 1);
+            // lanes with the same digit
+            uint64_t same = __ballot(there);
+            for (int bit = 1; bit < a.digits; bit *= 2) {
+                const uint64_t with = __ballot((d & bit) != 0);
+                same &= (d & bit) ? with : ~with;
+            }
+            uint32_t to = 0;
+            const int before = __popcll(same & ((uint64_t(1) << lane) - 1));
+            if (there) to = next[wave][d] + before;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (there && (same >> lane) == 1) next[wave][d] += before + 1;   // the last of them
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (there && int64_t(to) < a.s.n) {
+                a.s.key[to] = k[u];
+                a.s.order[to] = o[u];
+            }
         }
     }
 }
@@ -226,7 +278,8 @@ __global__ __launch_bounds__(kThreads) void digit_move_kernel(const DigitArgs a)
 // ---------------------------------------------------------------------------
 
 constexpr int kChunk = 64 * kOctet;   // columns of a wave
-constexpr int kAhead = 8;             // rows of dy loaded at once
+template <int D>
+constexpr int kAhead = D == ZERO_DTYPE_FP32 ? 8 : 16;   // rows of dy loaded at once
 constexpr int kZeroRows = 16;         // table rows that a block looks through for unnamed ones
 
 struct SumArgs {
@@ -235,7 +288,8 @@ struct SumArgs {
     const uint32_t* order;
     float* part;              // [tiles][2][chunks * kChunk]: of the run that enters a tile, and of the one that leaves it
     int64_t tiles;
-    int32_t tile;             // length: a multiple of 64
+    int32_t tile;             // length: 8, 16, 32 or a multiple of 64
+    Divisor per_row;          // octets of a row
     int32_t chunks;
     int64_t tile_blocks;      // blocks that sum tiles; those after them fill rows with zeros
 };
@@ -272,7 +326,7 @@ __device__ __forceinline__ void sum_tile(const SumArgs& a, int64_t t, int chunk)
     float* mine = a.part + t * 2 * a.chunks * kChunk + col;
 
     const auto flush = [&](bool leaves) {
-        if (run == none) return;
+        if (run >= none) return;
         if (enters || leaves) {
             float* at = mine + (enters ? 0 : a.chunks * kChunk);
             ((Global<f32x4>*)at)[0] = f32x4{acc[0], acc[1], acc[2], acc[3]};
@@ -285,17 +339,18 @@ __device__ __forceinline__ void sum_tile(const SumArgs& a, int64_t t, int chunk)
         const int64_t p = p0 + lane;
         const uint32_t keys = p < hi ? a.key[p] : none, places = p < hi ? a.order[p] : 0;
         const int m = int(hi - p0 < 64 ? hi - p0 : 64);
-        for (int j0 = 0; j0 < m; j0 += kAhead) {
-            Octet<DI> x[kAhead];
+        constexpr int ahead = kAhead<DI>;
+        for (int j0 = 0; j0 < m; j0 += ahead) {
+            Octet<DI> x[ahead];
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
+            for (int j = 0; j < ahead; ++j) {
                 x[j].zero();
                 const uint32_t r = uint32_t(__builtin_amdgcn_readlane(int(keys), j0 + j));   // none behind hi
                 const uint32_t i = uint32_t(__builtin_amdgcn_readlane(int(places), j0 + j));
-                if (r != none) x[j] = load_octet<DI>(place<DI>(a.e.in, i, a.e.s_in, col), left);
+                if (r < none && i < a.e.n) x[j] = load_octet<DI>(place<DI>(a.e.in, i, a.e.s_in, col), left);
             }
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
+            for (int j = 0; j < ahead; ++j) {
                 if (j0 + j >= m) break;
                 const uint32_t r = uint32_t(__builtin_amdgcn_readlane(int(keys), j0 + j));
                 if (r != run) {
@@ -355,6 +410,15 @@ __global__ __launch_bounds__(kThreads) void tile_sum_kernel(const SumArgs a) {
     const uint32_t there = uniform(named);
     Octet<DO> zero;
     zero.zero();
+    if (a.per_row.g < kThreads) {   // short rows: all of them at once
+        const uint32_t all = uint32_t(r1 - r0) * a.per_row.g;
+        for (uint32_t x = threadIdx.x; x < all; x += kThreads) {
+            const uint32_t r = divide(x, a.per_row);
+            const int64_t c = int64_t(x - r * a.per_row.g) * kOctet;
+            if (!(there >> r & 1)) store_octet<DO>(place<DO>(a.e.out, r0 + r, a.e.s_out, c), a.e.cols - c, zero);
+        }
+        return;
+    }
     for (int64_t r = r0; r < r1; ++r) {
         if (there >> (r - r0) & 1) continue;
         for (int64_t c = int64_t(threadIdx.x) * kOctet; c < a.e.cols; c += kThreads * kOctet)
@@ -362,20 +426,21 @@ __global__ __launch_bounds__(kThreads) void tile_sum_kernel(const SumArgs a) {
     }
 }
 
-// Adds up the partial sums of a run that crosses tiles: a wave for each tile that
-// such a run leaves from where it began, and 512 columns.
+// Adds up the partial sums of a run that crosses tiles: a block for each tile that
+// such a run leaves from where it began, and 512 columns.  Its four waves have a
+// quarter of the tiles each.
 template <int DO>
 __global__ __launch_bounds__(kThreads) void join_kernel(const SumArgs a) {
-    const int lane = int(threadIdx.x) & 63;
-    const int64_t w = int64_t(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6);
-    const int64_t t = w / a.chunks;
-    if (t + 1 >= a.tiles) return;
+    __shared__ f32x4 sums[3][2][64];
+    const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6;
+    const int64_t t = int64_t(blockIdx.x) / a.chunks;
     const int64_t end = (t + 1) * a.tile;   // below n
-    const uint32_t run = uniform(a.key[end]);
-    if (run == uint32_t(a.e.rows) || uniform(a.key[end - 1]) != run) return;
     const int64_t lo = t * a.tile;
-    if (lo > 0 && uniform(a.key[lo]) == run && uniform(a.key[lo - 1]) == run) return;   // began earlier
-    // the tiles after t that the run enters
+    const uint32_t after = a.key[end], before = a.key[end - 1], at = a.key[lo], earlier = a.key[lo > 0 ? lo - 1 : 0];
+    const uint32_t run = uniform(after);
+    if (run >= uint32_t(a.e.rows) || uniform(before) != run) return;
+    if (lo > 0 && uniform(at) == run && uniform(earlier) == run) return;   // began earlier
+    // the last tile that the run enters: the sorted list's run ends there
     int64_t last = t + 1;
     for (;;) {
         const int64_t p = (last + 1 + lane) * a.tile;
@@ -384,54 +449,66 @@ __global__ __launch_bounds__(kThreads) void join_kernel(const SumArgs a) {
         last += c;
         if (c < 64) break;
     }
-    const int64_t col = int64_t(w - t * a.chunks) * kChunk + lane * kOctet;
+    const int64_t col = (int64_t(blockIdx.x) - t * a.chunks) * kChunk + lane * kOctet;
     const int64_t half = int64_t(a.chunks) * kChunk;
-    float acc[kOctet];
-    const auto load = [&](int64_t tile, bool leaving, f32x4 v[2]) {
-        const float* p = a.part + (tile * 2 + (leaving ? 1 : 0)) * half + col;
-        v[0] = ((Global<const f32x4>*)p)[0];
-        v[1] = ((Global<const f32x4>*)p)[1];
-    };
-    f32x4 v[2];
-    load(t, true, v);   // the run began in t, at its first place or after it
+    const int64_t count = last - t + 1, share = (count + 3) / 4;
+    const int64_t begin = t + wave * share, stop = begin + share < last + 1 ? begin + share : last + 1;
+    f32x4 acc[2] = {};
+    constexpr int ahead = 8;
+    for (int64_t u = begin; u < stop; u += ahead) {
+        f32x4 x[ahead][2];
 #pragma unroll
-    for (int k = 0; k < kOctet; ++k) acc[k] = v[k >> 2][k & 3];
-    for (int64_t u = t + 1; u <= last; u += kAhead) {
-        f32x4 x[kAhead][2];
+        for (int j = 0; j < ahead; ++j) {
+            const int64_t v = u + j < stop ? u + j : stop - 1;
+            // (the run began in t, at its first place or after it: it leaves t, and enters the others)
+            const float* p = a.part + (v * 2 + (v == t ? 1 : 0)) * half + col;
+            x[j][0] = ((Global<const f32x4>*)p)[0];
+            x[j][1] = ((Global<const f32x4>*)p)[1];
+        }
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) load(u + j <= last ? u + j : last, false, x[j]);
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (u + j <= last)
-#pragma unroll
-                for (int k = 0; k < kOctet; ++k) acc[k] += x[j][k >> 2][k & 3];
+        for (int j = 0; j < ahead; ++j)
+            if (u + j < stop) {
+                acc[0] += x[j][0];
+                acc[1] += x[j][1];
+            }
     }
-    finish_row<DO>(a.e, run, col, a.e.cols - col, acc);
+    if (wave > 0) {
+        sums[wave - 1][0][lane] = acc[0];
+        sums[wave - 1][1][lane] = acc[1];
+    }
+    __syncthreads();
+    if (wave > 0) return;
+    for (int w = 1; w < 4; ++w)
+        if (w * share < count) {
+            acc[0] += sums[w - 1][0][lane];
+            acc[1] += sums[w - 1][1][lane];
+        }
+    const float all[kOctet] = {acc[0].x, acc[0].y, acc[0].z, acc[0].w, acc[1].x, acc[1].y, acc[1].z, acc[1].w};
+    finish_row<DO>(a.e, run, col, a.e.cols - col, all);
 }
 
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
 
-// Tiles long enough that the most frequent token has few of them, short enough
-// that all CUs have some.
-int tile_length(int64_t n) {
-    int t = 64;
-    while (t < 512 && n / t > 2048) t *= 2;
+// Tiles of 8 tokens while 8192 waves take them, a multiple of what the card holds:
+// short ones hide the loads' latency, long ones leave fewer partial sums.
+int tile_length(int64_t n, int64_t chunks) {
+    int t = 8;
+    while (t < 512 && n / t * chunks > 8192) t *= 2;
     return t;
 }
 
 struct Plan {
     int64_t tiles, part;        // part: elements of a sorting block
     int32_t tile, chunks, blocks, passes, digits;
-    int64_t lists;              // bytes of a list of n numbers
     int64_t off_key[2], off_order[2], off_count, off_part, bytes;
 };
 Plan plan_for(int64_t n, int64_t rows, int64_t cols) {
     Plan p = {};
-    p.tile = tile_length(n);
-    p.tiles = (n + p.tile - 1) / p.tile;
     p.chunks = int32_t((cols + kChunk - 1) / kChunk);
+    p.tile = tile_length(n, p.chunks);
+    p.tiles = (n + p.tile - 1) / p.tile;
     int bits = 1;   // rows is a key too
     while ((int64_t(1) << bits) <= rows) ++bits;
     p.passes = n <= kRankMost ? 0 : (bits + kDigitBits - 1) / kDigitBits;
@@ -460,8 +537,7 @@ void run_sum(const SumArgs& a, int64_t blocks, hipStream_t s, const KernelEvents
     launch(tile_sum_kernel<DI, DO>, dim3(uint32_t(blocks)), kThreads, s, one, a);
     if (!join) return;
     one = {nullptr, ev.stop};
-    const int64_t waves = (a.tiles - 1) * a.chunks;
-    launch(join_kernel<DO>, dim3(uint32_t((waves + 3) / 4)), kThreads, s, one, a);
+    launch(join_kernel<DO>, dim3(uint32_t((a.tiles - 1) * a.chunks)), kThreads, s, one, a);
 }
 
 template <int DI, int DO>
@@ -487,11 +563,16 @@ void for_types(int32_t in, int32_t out, const F& f) {
 
 }  // namespace
 
+// Octets of a row: two at least, the second one of nothing where there is one.
+static Divisor octets_of(int64_t cols) {
+    const int64_t g = (cols + kOctet - 1) / kOctet;
+    return divisor(uint32_t(g < 2 ? 2 : g));
+}
+
 hipError_t launch_lookup(const EmbedLaunch& e, hipStream_t s, const KernelEvents& ev) {
     LookupArgs a;
     a.e = e;
-    const int64_t per_row = (e.cols + kOctet - 1) / kOctet;
-    a.per_row = divisor(uint32_t(per_row < 2 ? 2 : per_row));   // a second octet of nothing where there is one
+    a.per_row = octets_of(e.cols);
     a.octets = e.n * a.per_row.g;
     for_types(e.type, e.out_type, [&](auto di, auto d_o) { run_lookup<decltype(di)::value, decltype(d_o)::value>(a, s, ev); });
     return hipGetLastError();
@@ -501,7 +582,8 @@ int64_t embedding_work(int64_t n, int64_t rows, int64_t cols) { return plan_for(
 
 bool embedding_fits(int64_t n, int64_t rows, int64_t cols) {
     const Plan p = plan_for(n, rows, cols);
-    return (p.tiles * p.chunks + 3) / 4 + (rows + kZeroRows - 1) / kZeroRows < int64_t(1) << 24;
+    constexpr int64_t most = int64_t(1) << 24;   // blocks of a launch
+    return (p.tiles * p.chunks + 3) / 4 + (rows + kZeroRows - 1) / kZeroRows < most && p.tiles * p.chunks < most;
 }
 
 hipError_t launch_embedding_grad(const EmbedLaunch& e, hipStream_t s, const KernelEvents& ev) {
@@ -514,6 +596,7 @@ hipError_t launch_embedding_grad(const EmbedLaunch& e, hipStream_t s, const Kern
     a.tiles = p.tiles;
     a.chunks = p.chunks;
     a.part = reinterpret_cast<float*>(work + p.off_part);
+    a.per_row = octets_of(e.cols);
     const int last = p.passes ? (p.passes - 1) & 1 : 0;   // the lists that the last pass writes
     a.key = list(p.off_key[last]);
     a.order = list(p.off_order[last]);
@@ -523,8 +606,7 @@ hipError_t launch_embedding_grad(const EmbedLaunch& e, hipStream_t s, const Kern
     const bool wide = e.token_bytes == 8;
     if (p.passes == 0 && e.n > 0) {
         const dim3 grid(uint32_t((e.n + kRankTokens - 1) / kRankTokens));
-        if (wide) launch(rank_kernel<int64_t>, grid, kThreads, s, one, so);
-        else launch(rank_kernel<int32_t>, grid, kThreads, s, one, so);
+        launch(wide ? rank_kernel<int64_t> : rank_kernel<int32_t>, grid, kRankThreads, s, one, so);
         one.start = nullptr;
     }
     for (int k = 0; k < p.passes; ++k) {
@@ -540,14 +622,11 @@ hipError_t launch_embedding_grad(const EmbedLaunch& e, hipStream_t s, const Kern
         d.digits = p.digits;
         d.shift = k * __builtin_ctz(uint32_t(p.digits));
         const KernelEvents none;
-        if (wide) {
-            launch(digit_count_kernel<int64_t>, dim3(p.blocks), kThreads, s, one, d);
-            launch(digit_move_kernel<int64_t>, dim3(p.blocks), kThreads, s, none, d);
-        } else {
-            launch(digit_count_kernel<int32_t>, dim3(p.blocks), kThreads, s, one, d);
-            launch(digit_move_kernel<int32_t>, dim3(p.blocks), kThreads, s, none, d);
-        }
+        const auto count = k > 0 ? digit_count_kernel<int32_t, false> : wide ? digit_count_kernel<int64_t, true> : digit_count_kernel<int32_t, true>;
+        launch(count, dim3(p.blocks), kThreads, s, one, d);
         one.start = nullptr;
+        const auto move = k > 0 ? digit_move_kernel<int32_t, false> : wide ? digit_move_kernel<int64_t, true> : digit_move_kernel<int32_t, true>;
+        launch(move, dim3(p.blocks), kThreads, s, none, d);
     }
     a.tile_blocks = (p.tiles * p.chunks + 3) / 4;
     const int64_t zero_blocks = e.accumulate ? 0 : (e.rows + kZeroRows - 1) / kZeroRows;
