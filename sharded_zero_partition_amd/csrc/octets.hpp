@@ -30,35 +30,41 @@ __device__ __forceinline__ void divide(int64_t x, const Divisor& d, int64_t* q, 
     *r = uint32_t(b);
 }
 
-// Eight values as they are in memory.
+// Eight values as they are in memory, at any element's address.  kPast: past the
+// caches, which keep no such line for long.
 template <int D>
 struct Octet {   // 16-bit types
+    typedef u16x8 at __attribute__((aligned(2)));
     u16x8 v;
     __device__ __forceinline__ void zero() { v = u16x8{}; }
+    template <bool kPast>
     __device__ __forceinline__ void load(const void* p) {
-        typedef u16x8 at __attribute__((aligned(2)));
-        v = *(Global<const at>*)p;
+        v = kPast ? __builtin_nontemporal_load((Global<const at>*)p) : *(Global<const at>*)p;
     }
+    template <bool kPast>
     __device__ __forceinline__ void store(void* p) const {
-        typedef u16x8 at __attribute__((aligned(2)));
-        *(Global<at>*)p = v;
+        if (kPast) __builtin_nontemporal_store(v, (Global<at>*)p);
+        else *(Global<at>*)p = v;
     }
     __device__ __forceinline__ float get(int i) const { return Type<D>::wide(v[i]); }
     __device__ __forceinline__ void set(int i, float x) { v[i] = Type<D>::narrow(x); }
 };
 template <>
 struct Octet<ZERO_DTYPE_FP32> {
+    typedef f32x4 at __attribute__((aligned(4)));
     f32x4 v[2];
     __device__ __forceinline__ void zero() { v[0] = v[1] = f32x4{}; }
+    template <bool kPast>
     __device__ __forceinline__ void load(const void* p) {
-        typedef f32x4 at __attribute__((aligned(4)));
-        v[0] = ((Global<const at>*)p)[0];
-        v[1] = ((Global<const at>*)p)[1];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) v[h] = kPast ? __builtin_nontemporal_load((Global<const at>*)p + h) : ((Global<const at>*)p)[h];
     }
+    template <bool kPast>
     __device__ __forceinline__ void store(void* p) const {
-        typedef f32x4 at __attribute__((aligned(4)));
-        ((Global<at>*)p)[0] = v[0];
-        ((Global<at>*)p)[1] = v[1];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (kPast) __builtin_nontemporal_store(v[h], (Global<at>*)p + h);
+            else ((Global<at>*)p)[h] = v[h];
     }
     __device__ __forceinline__ float get(int i) const { return v[i >> 2][i & 3]; }
     __device__ __forceinline__ void set(int i, float x) { v[i >> 2][i & 3] = x; }
@@ -66,12 +72,12 @@ struct Octet<ZERO_DTYPE_FP32> {
 
 // The octet at p of which `n` values exist (8 or more: all; 0 or less: none);
 // the others are zero.
-template <int D>
+template <int D, bool kPast = false>
 __device__ __forceinline__ Octet<D> load_octet(const void* p, int64_t n) {
     typedef typename Type<D>::elem E;
     Octet<D> x;
     if (n >= kOctet) {
-        x.load(p);
+        x.template load<kPast>(p);
         return x;
     }
     x.zero();
@@ -84,11 +90,11 @@ __device__ __forceinline__ Octet<D> load_octet(const void* p, int64_t n) {
         }
     return x;
 }
-template <int D>
+template <int D, bool kPast = false>
 __device__ __forceinline__ void store_octet(void* p, int64_t n, const Octet<D>& x) {
     typedef typename Type<D>::elem E;
     if (n >= kOctet) {
-        x.store(p);
+        x.template store<kPast>(p);
         return;
     }
 #pragma unroll
