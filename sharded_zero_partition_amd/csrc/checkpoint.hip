@@ -37,11 +37,6 @@ struct Packed {
 
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-template <int kCtrl>
-__device__ __forceinline__ uint32_t across(uint32_t x) {
-    return uint32_t(__builtin_amdgcn_update_dpp(0, int(x), kCtrl, 0xF, 0xF, true));
-}
-
 // The bits, as an fp32's, of the largest magnitude of the octet.
 template <int D>
 __device__ __forceinline__ uint32_t largest(const Octet<D>& x) {

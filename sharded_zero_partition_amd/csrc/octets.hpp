@@ -105,6 +105,12 @@ __device__ __forceinline__ void store_octet(void* p, int64_t n, const Octet<D>& 
         }
 }
 
+// Another lane's value (DPP control).
+template <int kCtrl>
+__device__ __forceinline__ uint32_t across(uint32_t x) {
+    return uint32_t(__builtin_amdgcn_update_dpp(0, int(x), kCtrl, 0xF, 0xF, true));
+}
+
 // Where the value at (row, col) of a matrix is.
 template <int D>
 __device__ __forceinline__ char* place(const void* p, int64_t row, int64_t stride, int64_t col) {

@@ -26,7 +26,7 @@ using Shared = __attribute__((address_space(3))) T;
 // over all banks.
 template <int W>
 __device__ __forceinline__ uint32_t pair_at(int t, int q) {
-    return uint32_t(t * (W * 2) + ((q ^ (t & 7)) << 5));
+    return uint32_t(t * (W * 2) + ((q ^ (t & 7 & (W / 16 - 1))) << 5));
 }
 
 // The products are of 16-bit numbers, exact in fp32, and what they are made from is
@@ -94,11 +94,11 @@ __device__ __forceinline__ u32x4 decode(u32x2 code, uint32_t s, uint32_t top) {
     return u32x4{Op<D>::pair(code.x, f, false), Op<D>::pair(code.x, f, true), Op<D>::pair(code.y, f, false), Op<D>::pair(code.y, f, true)};
 }
 
-// Tiles of 256 x 256 outputs, steps of STEP tokens.
-constexpr int kTile = 256;
-template <int D_, int STEP_>
+// Tiles of W x W outputs, steps of STEP tokens.
+constexpr int kTile = 256, kSmall = 64;
+template <int D_, int STEP_, int W_>
 struct Config {
-    static constexpr int D = D_, BM = kTile, BN = kTile, WM = 2, WN = 4, STEP = STEP_;
+    static constexpr int D = D_, W = W_, BM = W, BN = W, WM = 2, WN = W == kTile ? 4 : 2, STEP = STEP_;
     static constexpr int P = parts_of(D);
     static constexpr int threads = 64 * WM * WN;
     static constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
@@ -106,7 +106,7 @@ struct Config {
     static constexpr int b_chunks = STEP * BN / 16 / threads;
     static constexpr int a_bytes = STEP * BM * 2, b_bytes = STEP * BN * 2;
     static constexpr int stage = a_bytes + P * b_bytes, lds_bytes = 2 * stage;
-    static constexpr int G = 1;   // fragments of n that leave at a time
+    static constexpr int G = W == kTile ? 1 : 2;   // fragments of n that leave at a time
     static_assert(a_chunks * threads * 16 == STEP * BM && b_chunks * threads * 16 == STEP * BN, "loads");
     static_assert(2 * stage <= 160 * 1024, "LDS");
 };
@@ -119,11 +119,11 @@ struct GemmArgs {
     int32_t whole;       // tiles that one block has for all tokens, the first ones; each of the others has
     int32_t splits;      // `splits` blocks (1: all are whole)
     int64_t per_split;   // tokens of a split, a multiple of kUnit
-    float* part;         // sums of tile whole + i and split j: kTile x kTile at (i splits + j) kPart, as dw has them,
-                         // then kTile of dy's columns
+    float* part;         // sums of tile whole + i and split j: W x W at (i splits + j) part_size(W), as dw has
+                         // them, then W of dy's columns
     int32_t shares;      // whose the bias is: 0: the first k-tile's, else k-tile i / 2's for fragments i shares on of each 8
 };
-constexpr int64_t kPart = kTile * kTile + kTile;
+constexpr int64_t part_size(int w) { return w * w + w; }
 constexpr int64_t kUnit = 64;
 
 // 16 values of dy.
@@ -226,13 +226,25 @@ __device__ __forceinline__ void store_rows(const Target& t, const float* stage, 
         }
         return;
     }
+    if (col >= t.cols) return;
+    const int64_t left = t.cols - col - c;   // may be negative
 #pragma unroll 1
-    for (int x = 0; x < count; ++x) {
-        const f32x4 v = *reinterpret_cast<const f32x4*>(from + x * per * kPitch);
-        const int64_t left = row + r0 + x * per < t.rows ? t.cols - col - c : 0;
+    for (int64_t x = 0; x < R && row + x < t.rows; x += per) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(from);
+        from += per * kPitch;
+        if (row + r0 + x < t.rows) {
+            if (left >= 4) {
+                typename F::vec y = {};
+                if (t.accumulate) y = *(Global<typename F::at>*)p;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (k < left) p[k] = F::narrow(t.accumulate ? F::wide(p[k]) + v[k] : v[k]);
+                for (int k = 0; k < 4; ++k) y[k] = F::narrow(t.accumulate ? F::wide(y[k]) + v[k] : v[k]);
+                *(Global<typename F::at>*)p = y;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    if (k < left) p[k] = F::narrow(t.accumulate ? F::wide(p[k]) + v[k] : v[k]);
+            }
+        }
         p += step;
     }
 }
@@ -258,6 +270,7 @@ __device__ __forceinline__ uint32_t in_order(uint32_t id, uint32_t total) {
     const uint32_t xcd = id & 7, q8 = total >> 3, r8 = total & 7;
     return xcd * q8 + (xcd < r8 ? xcd : r8) + (id >> 3);
 }
+template <int W>
 __device__ __forceinline__ Part part_of(const GemmArgs& a) {
     const uint32_t id = blockIdx.x, whole = uint32_t(a.whole);
     Part p;
@@ -278,49 +291,62 @@ __device__ __forceinline__ Part part_of(const GemmArgs& a) {
     const uint32_t group = uniform(tile / (kGroup * a.tiles_k)), rest = tile - group * (kGroup * a.tiles_k);
     const uint32_t wide = a.tiles_n - group * kGroup < kGroup ? a.tiles_n - group * kGroup : kGroup;
     const uint32_t tile_k = uniform(rest / wide);
-    p.k0 = int64_t(tile_k) * kTile;
-    p.n0 = int64_t(group * kGroup + rest - tile_k * wide) * kTile;
+    p.k0 = int64_t(tile_k) * W;
+    p.n0 = int64_t(group * kGroup + rest - tile_k * wide) * W;
     return p;
 }
 
 // The largest scale of each 32 of a tile's columns over its tokens (255, which is NaN, aside),
-// 1 at least, into top[0 .. 7].
-template <int kThreads>
+// 1 at least, into top[0 .. kBlocks - 1].
+template <int kThreads, int kBlocks>
 __device__ __forceinline__ void largest_scales(const GemmArgs& a, const Part& part, uint32_t* top) {
     const int64_t left = a.blocks - (part.k0 >> 5);
-    const int there = left < 8 ? int(left) : 8;
+    const int there = left < kBlocks ? int(left) : kBlocks;
     if (threadIdx.x < 8) top[threadIdx.x] = 1;
     __syncthreads();
     constexpr int batch = 8;
     uint32_t most[8] = {};
-    const uint8_t* p = a.w.scale + (part.k0 >> 5);
+    // eight bytes at once, the last ones from where eight end, whatever follows a row cut off
+    const Global<const uint8_t>* all = (Global<const uint8_t>*)a.w.scale;
+    const int64_t end = a.w.T * a.blocks - 8, first = part.k0 >> 5;
+    const uint64_t mine = there > 0 ? ~uint64_t(0) >> (8 * (8 - there)) : 0;
     for (int64_t t = part.t_begin + threadIdx.x; t < part.t_end; t += batch * kThreads) {
         uint64_t x[batch];
-        if (there == 8) {
+        if (end >= 0) {
             typedef uint64_t at __attribute__((aligned(1)));
+            int past[batch];
 #pragma unroll
             for (int i = 0; i < batch; ++i) {
-                const int64_t u = t + i * kThreads < part.t_end ? t + i * kThreads : t;
-                x[i] = *(Global<const at>*)(p + u * a.blocks);
+                const int64_t u = t + i * kThreads < part.t_end ? t + i * kThreads : t, from = u * a.blocks + first;
+                past[i] = from > end ? int(from - end) : 0;
+                x[i] = *(Global<const at>*)(all + from - past[i]);
             }
-        } else {
 #pragma unroll
-            for (int i = 0; i < batch; ++i) {
-                const int64_t u = t + i * kThreads < part.t_end ? t + i * kThreads : t;
-                x[i] = 0;
-                for (int b = 0; b < there; ++b) x[i] |= uint64_t(((Global<const uint8_t>*)p)[u * a.blocks + b]) << (8 * b);
-            }
+            for (int i = 0; i < batch; ++i) x[i] = x[i] >> (8 * past[i]) & mine;
+        } else {   // 7 bytes at most in all
+#pragma unroll
+            for (int i = 0; i < batch; ++i) x[i] = 0;
+            for (int b = 0; b < there; ++b) x[0] |= uint64_t(all[t * a.blocks + first + b]) << (8 * b);
         }
 #pragma unroll
         for (int i = 0; i < batch; ++i)
 #pragma unroll
-            for (int b = 0; b < 8; ++b) {
+            for (int b = 0; b < kBlocks; ++b) {
                 const uint32_t s = uint32_t(x[i] >> (8 * b)) & 255;
                 most[b] = max(most[b], s == 255 ? 0 : s);
             }
     }
+    // the largest of each row of 16 lanes, so that LDS has few to put in order
 #pragma unroll
-    for (int b = 0; b < 8; ++b) atomicMax(&top[b], most[b]);
+    for (int b = 0; b < kBlocks; ++b) {
+        most[b] = max(most[b], across<0xB1>(most[b]));    // lanes 1, 0, 3, 2 of each four
+        most[b] = max(most[b], across<0x4E>(most[b]));    // lanes 2, 3, 0, 1
+        most[b] = max(most[b], across<0x141>(most[b]));   // eight lanes mirrored
+        most[b] = max(most[b], across<0x140>(most[b]));   // sixteen
+    }
+    if ((threadIdx.x & 15) == 0)
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) atomicMax(&top[b], most[b]);
     __syncthreads();
 }
 
@@ -341,7 +367,7 @@ __device__ __forceinline__ void finish(const GemmArgs& a, const Part& part, char
     const bool parts = part.slot >= 0;
     const int64_t k_wave = (parts ? 0 : part.k0) + wm * K, n_wave = (parts ? 0 : part.n0) + wn * (C::NI * 16);
     const int k_lane = 4 * (lane >> 4), n_lane = lane & 15;
-    const Target to = parts ? Target{reinterpret_cast<char*>(a.part + part.slot * kPart), kTile, kTile, kTile, false}
+    const Target to = parts ? Target{reinterpret_cast<char*>(a.part + part.slot * part_size(C::W)), C::W, C::W, C::W, false}
                             : Target{static_cast<char*>(a.w.dw), a.w.transposed ? a.w.k : a.w.n, a.w.transposed ? a.w.n : a.w.k, a.w.s_dw,
                                      a.w.accumulate};
     // 2^power of fragments m and m + 1, 32 columns
@@ -386,11 +412,12 @@ __device__ __forceinline__ void finish(const GemmArgs& a, const Part& part, char
 }
 
 // The sum over dy of 16 columns of the tile, from n on.
+template <int W>
 __device__ __forceinline__ void finish_bias(const GemmArgs& a, const Part& part, int n, float sum) {
     const int lane = int(threadIdx.x) & 63;
     n += lane;
     if (lane >= 16 || part.n0 + n >= a.w.n) return;
-    if (part.slot >= 0) ((Global<float>*)a.part)[part.slot * kPart + kTile * kTile + n] = sum;
+    if (part.slot >= 0) ((Global<float>*)a.part)[part.slot * part_size(W) + W * W + n] = sum;
     else if (a.w.out_type == ZERO_DTYPE_FP16) put_bias<ZERO_DTYPE_FP16>(a, part.n0 + n, sum);
     else if (a.w.out_type == ZERO_DTYPE_BF16) put_bias<ZERO_DTYPE_BF16>(a, part.n0 + n, sum);
     else put_bias<ZERO_DTYPE_FP32>(a, part.n0 + n, sum);
@@ -404,10 +431,10 @@ __global__ __launch_bounds__(C::threads) void weight_grad_kernel(const GemmArgs 
     const int tid = int(threadIdx.x), lane = tid & 63, wave = tid >> 6;
     const int wm = wave / C::WN, wn = wave % C::WN;
 
-    const Part part = part_of(a);
+    const Part part = part_of<C::W>(a);
     const int64_t k0 = part.k0, n0 = part.n0, t_begin = part.t_begin, t_end = part.t_end;
     __shared__ uint32_t top[8];
-    if (Op<D>::kScaled) largest_scales<C::threads>(a, part, top);
+    if (Op<D>::kScaled) largest_scales<C::threads, C::W / 32>(a, part, top);
 
     Codes ra[C::a_chunks];
     Chunk<D> rb[C::b_chunks];
@@ -517,7 +544,7 @@ __global__ __launch_bounds__(C::threads) void weight_grad_kernel(const GemmArgs 
     finish<C, Op<D>::kScaled>(a, part, lds, acc, power);
     if (bias)
 #pragma unroll
-        for (int i = 0; i < C::NI; ++i) finish_bias(a, part, (wn * C::NI + i) * 16, sum[i][0]);
+        for (int i = 0; i < C::NI; ++i) finish_bias<C::W>(a, part, (wn * C::NI + i) * 16, sum[i][0]);
 }
 
 // The same for a dy of 16 bits that is aligned to 16 bytes: four waves of 128 x 128
@@ -539,7 +566,7 @@ __device__ __forceinline__ void each(std::integer_sequence<int, I...>, const F& 
 }
 
 struct Fast {
-    static constexpr int BM = kTile, BN = kTile, WM = 2, WN = 2, MI = 8, NI = 8, threads = 256, G = 4;
+    static constexpr int W = kTile, BM = W, BN = W, WM = 2, WN = 2, MI = 8, NI = 8, threads = 256, G = 4;
     static constexpr int rows = 32;                               // of a phase
     static constexpr int a_bytes = rows * BM * 2, b_bytes = rows * BN * 2, code_bytes = rows * BM, scale_bytes = rows * 8 * 4;
     static constexpr int a_ring = 2, b_ring = 5, code_ring = 5, turn = 10;
@@ -566,13 +593,13 @@ __global__ __launch_bounds__(256, 1) void weight_grad_fast_kernel(const GemmArgs
     __shared__ __attribute__((aligned(1024))) char lds[C::lds_bytes];
     const int tid = int(threadIdx.x), lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / C::WN, wn = wave % C::WN;
-    const Part part = part_of(a);
+    const Part part = part_of<C::W>(a);
     const int64_t k0 = part.k0, n0 = part.n0, t_begin = part.t_begin;
     uint32_t* const tops = reinterpret_cast<uint32_t*>(lds);   // until the loads come
     uint32_t top = 0;
     int power[C::MI / 2] = {};
     if (Op<D>::kScaled) {
-        largest_scales<C::threads>(a, part, tops);
+        largest_scales<C::threads, C::W / 32>(a, part, tops);
         top = tops[(tid & 15) >> 1];   // of the columns that the thread decodes
 #pragma unroll
         for (int m = 0; m < C::MI / 2; ++m) power[m] = __builtin_amdgcn_readfirstlane(int(tops[wm * (C::MI / 2) + m]) - kTop);
@@ -747,27 +774,29 @@ __global__ __launch_bounds__(256, 1) void weight_grad_fast_kernel(const GemmArgs
     finish<C, Op<D>::kScaled>(a, part, lds, acc, power);
 #pragma unroll
     for (int i = 0; i < kSums; ++i)
-        if (share < C::NI) finish_bias(a, part, (wn * 8 + first + i) * 16, sum[i][0]);
+        if (share < C::NI) finish_bias<C::W>(a, part, (wn * 8 + first + i) * 16, sum[i][0]);
 }
 
 // Adds up the splits' sums of a tile, in order: four neighbouring elements a thread.
-constexpr int kJoinThreads = 256, kJoinBlocks = kTile * kTile / 4 / kJoinThreads;   // blocks of a tile
-template <int DO>
+constexpr int kJoinThreads = 256;
+constexpr int join_blocks(int w) { return w * w / 4 / kJoinThreads; }   // of a tile
+template <int DO, int W>
 __global__ __launch_bounds__(kJoinThreads) void split_join_kernel(const GemmArgs a) {
     typedef Four<DO> F;
     typedef typename F::E E;
-    const uint32_t i = blockIdx.x / kJoinBlocks, x = (blockIdx.x % kJoinBlocks) * kJoinThreads + threadIdx.x;
+    constexpr int blocks = join_blocks(W);
+    const uint32_t i = blockIdx.x / blocks, x = (blockIdx.x % blocks) * kJoinThreads + threadIdx.x;
     const uint32_t tile = uint32_t(a.whole) + i;
     const uint32_t group = tile / (kGroup * a.tiles_k), rest = tile - group * (kGroup * a.tiles_k);
     const uint32_t wide = a.tiles_n - group * kGroup < kGroup ? a.tiles_n - group * kGroup : kGroup, tile_k = rest / wide;
-    const int64_t k0 = int64_t(tile_k) * kTile, n0 = int64_t(group * kGroup + rest - tile_k * wide) * kTile;
-    const float* part = a.part + int64_t(i) * a.splits * kPart;
+    const int64_t k0 = int64_t(tile_k) * W, n0 = int64_t(group * kGroup + rest - tile_k * wide) * W;
+    const float* part = a.part + int64_t(i) * a.splits * part_size(W);
     const int64_t rows = a.w.transposed ? a.w.k : a.w.n, cols = a.w.transposed ? a.w.n : a.w.k;
-    const int64_t r = (a.w.transposed ? k0 : n0) + x / (kTile / 4), c = (a.w.transposed ? n0 : k0) + x % (kTile / 4) * 4;
+    const int64_t r = (a.w.transposed ? k0 : n0) + x / (W / 4), c = (a.w.transposed ? n0 : k0) + x % (W / 4) * 4;
     if (r < rows && c < cols) {
         f32x4 v = *(Global<const f32x4>*)(part + 4 * x);
 #pragma unroll 8
-        for (int s = 1; s < a.splits; ++s) v += *(Global<const f32x4>*)(part + s * kPart + 4 * x);
+        for (int s = 1; s < a.splits; ++s) v += *(Global<const f32x4>*)(part + s * part_size(W) + 4 * x);
         Global<E>* p = (Global<E>*)a.w.dw + r * a.w.s_dw + c;
         if (c + 4 <= cols) {
             typename F::vec y = {};
@@ -781,53 +810,86 @@ __global__ __launch_bounds__(kJoinThreads) void split_join_kernel(const GemmArgs
                 if (c + j < cols) p[j] = F::narrow(a.w.accumulate ? F::wide(p[j]) + v[j] : v[j]);
         }
     }
-    if (a.w.bias && blockIdx.x % kJoinBlocks == 0 && n0 + threadIdx.x < a.w.n) {
+    if (a.w.bias && blockIdx.x % blocks == 0 && threadIdx.x < W && n0 + threadIdx.x < a.w.n) {
         const uint32_t fragment = threadIdx.x / 16 % 8;
         if (tile_k != (a.shares ? fragment / uint32_t(2 * a.shares) : 0)) return;
-        float v = ((Global<const float>*)part)[kTile * kTile + threadIdx.x];
-        for (int s = 1; s < a.splits; ++s) v += ((Global<const float>*)part)[s * kPart + kTile * kTile + threadIdx.x];
+        float v = ((Global<const float>*)part)[W * W + threadIdx.x];
+        for (int s = 1; s < a.splits; ++s) v += ((Global<const float>*)part)[s * part_size(W) + W * W + threadIdx.x];
         put_bias<DO>(a, n0 + threadIdx.x, v);
     }
 }
 
-// How a product is cut.  One block runs on a CU at a time, so tiles beyond a multiple of the
-// CUs would cost a round that leaves most of them idle: those are split by tokens, and
-// another kernel adds their parts up.  The times are those of one MI355X: a tile takes
-// `fixed` us and `step` us for kUnit tokens, the other kernel 5 us and its bytes at 4.5 TB/s
-// (13B matrix, 1600 tiles: 1443 us in seven rounds, 1320 with the last 64 split).
+// How a product is cut: into tiles of 256 x 256 outputs, one of which runs on a CU at a
+// time, or of 64 x 64, of which several do; and where tiles are few, or some of the large are
+// left over after whole rounds of all CUs, these by tokens, another kernel adding the parts up.
+// What is expected to take the least time is taken, by this model of one MI355X in us: a round
+// of blocks takes `fixed` and `step` for kUnit tokens (small ones overlap, so their rounds
+// need not be whole, and `first` is what the first costs more), the other kernel 5 and its
+// bytes at 4.5 TB/s.
+//   bf16, large / small tiles      77 x 200 x 136: 15.5 / under 10.6, 1024 x 1024 x 1024: 26.4 / 12.5,
+//       1024 x 2048 x 2048: 33 / 21, 4096 x 1024 x 1024: 35 / 32, 16384 x 1024 x 1024: 52 / 85
+//   13B matrix, 1600 large tiles   1443 in seven rounds, 1364 with the last 64 tiles split
 constexpr int kCUs = 256;
 struct Cut {
-    int32_t tiles_k, tiles_n, whole, splits;
+    int32_t tile, tiles_k, tiles_n, whole, splits;
     int64_t per_split;
+    double cost;
     int64_t blocks() const { return whole + (int64_t(tiles_k) * tiles_n - whole) * splits; }
-    int64_t bytes() const { return splits > 1 ? (int64_t(tiles_k) * tiles_n - whole) * splits * kPart * 4 : 0; }
+    int64_t bytes() const { return splits > 1 ? (int64_t(tiles_k) * tiles_n - whole) * splits * part_size(tile) * 4 : 0; }
 };
-Cut cut_for(int64_t T, int64_t n, int64_t k, int32_t dy_type) {
-    const double fixed = 9, step = dy_type == ZERO_DTYPE_FP32 ? 4.2 : 1.35, join = 5, part = kPart * 4 / 4.5e6;
+struct Times {
+    int32_t tile, at_once;   // blocks that run on a CU at a time
+    double first, fixed, step;
+};
+Cut cut_into(const Times& x, int64_t T, int64_t n, int64_t k) {
+    const double part = part_size(x.tile) * 4 / 4.5e6;
+    const int64_t slots = int64_t(kCUs) * x.at_once;
+    const auto rounds = [&](int64_t blocks) {
+        if (x.at_once == 1) return double((blocks + slots - 1) / slots);
+        return blocks > slots ? double(blocks) / double(slots) : 1.0;
+    };
     Cut c;
-    c.tiles_k = k > 0 ? int32_t((k + kTile - 1) / kTile) : 1;   // the bias needs a tile
-    c.tiles_n = int32_t((n + kTile - 1) / kTile);
-    const int64_t tiles = int64_t(c.tiles_k) * c.tiles_n, units = (T + kUnit - 1) / kUnit, rest = tiles % kCUs;
+    c.tile = x.tile;
+    c.tiles_k = k > 0 ? int32_t((k + x.tile - 1) / x.tile) : 1;   // the bias needs a tile
+    c.tiles_n = int32_t((n + x.tile - 1) / x.tile);
+    const int64_t tiles = int64_t(c.tiles_k) * c.tiles_n, units = (T + kUnit - 1) / kUnit;
     c.whole = int32_t(tiles);
     c.splits = 1;
     c.per_split = units * kUnit;
+    c.cost = x.first + rounds(tiles) * (x.fixed + x.step * double(units));
+    const int64_t rest = x.at_once == 1 ? tiles % slots : tiles;
     if (rest == 0) return c;
-    double best = fixed + step * double(units);
+    const double before = x.first + double((tiles - rest) / slots) * (x.fixed + x.step * double(units));
     // at most 2 rounds of blocks, of 4 units at least
-    for (int64_t s = 2; s <= 64 && rest * s <= 2 * kCUs && 4 * s <= units; ++s) {
+    for (int64_t s = 2; s <= 64 && rest * s <= 2 * slots && 4 * s <= units; ++s) {
         int64_t per = (units + s - 1) / s;
         per = (per + 4) / 5 * 5;   // the fast kernel goes by 5 of them
         const int64_t used = (units + per - 1) / per;
         if (used < 2) continue;
-        const double cost = double((rest * used + kCUs - 1) / kCUs) * (fixed + step * double(per)) + join + double(rest * used) * part;
-        if (cost < best) {
-            best = cost;
+        const double cost = before + rounds(rest * used) * (x.fixed + x.step * double(per)) + 5 + double(rest * used) * part;
+        if (cost < c.cost) {
+            c.cost = cost;
             c.whole = int32_t(tiles - rest);
             c.splits = int32_t(used);
             c.per_split = per * kUnit;
         }
     }
     return c;
+}
+Cut cut_for(int64_t T, int64_t n, int64_t k, int32_t dy_type) {
+    const bool few = T <= 3 * kUnit;   // not for the fast kernel
+    Cut large, small;
+    if (dy_type == ZERO_DTYPE_FP32) {
+        large = cut_into({kTile, 1, 0, 10, 5}, T, n, k);
+        small = cut_into({kSmall, 2, 4, 0.8, 1.8}, T, n, k);
+    } else if (dy_type == ZERO_DTYPE_FP16) {
+        large = cut_into(few ? Times{kTile, 1, 0, 13, 2.6} : Times{kTile, 1, 0, 16, 1.6}, T, n, k);
+        small = cut_into({kSmall, 3, 4, 3.5, 0.87}, T, n, k);
+    } else {
+        large = cut_into(few ? Times{kTile, 1, 0, 7.5, 2.6} : Times{kTile, 1, 0, 10, 1.5}, T, n, k);
+        small = cut_into({kSmall, 3, 4, 0.7, 0.85}, T, n, k);
+    }
+    return small.cost < large.cost ? small : large;
 }
 
 // Whether the loads of the fast kernel reach everything: 16 bytes of dy at a time,
@@ -849,9 +911,17 @@ void run_fast(const GemmArgs& a, dim3 blocks, hipStream_t s, const KernelEvents&
     }
 }
 
-template <typename C>
+template <int W>
+void join(const GemmArgs& a, hipStream_t s, const KernelEvents& ev) {
+    const dim3 grid(uint32_t((int64_t(a.tiles_k) * a.tiles_n - a.whole) * join_blocks(W)));
+    if (a.w.out_type == ZERO_DTYPE_FP16) launch(split_join_kernel<ZERO_DTYPE_FP16, W>, grid, kJoinThreads, s, ev, a);
+    else if (a.w.out_type == ZERO_DTYPE_BF16) launch(split_join_kernel<ZERO_DTYPE_BF16, W>, grid, kJoinThreads, s, ev, a);
+    else launch(split_join_kernel<ZERO_DTYPE_FP32, W>, grid, kJoinThreads, s, ev, a);
+}
+
+template <int D>
 hipError_t run(const WeightGradLaunch& w, hipStream_t s, const KernelEvents& ev) {
-    const Cut c = cut_for(w.T, w.n, w.k, w.dy_type);
+    const Cut c = cut_for(w.T, w.n, w.k, D);
     GemmArgs a = {};
     a.w = w;
     a.blocks = (w.k + 31) / 32;
@@ -864,18 +934,20 @@ hipError_t run(const WeightGradLaunch& w, hipStream_t s, const KernelEvents& ev)
     a.part = w.work;
     KernelEvents one = {ev.start, c.splits > 1 ? nullptr : ev.stop};
     const dim3 blocks{uint32_t(c.blocks())};
-    if (C::D != ZERO_DTYPE_FP32 && fast(w, c.whole > 0 ? w.T : c.per_split)) {
+    typedef Config<D, D == ZERO_DTYPE_FP32 ? 32 : 64, kTile> Large;
+    typedef Config<D, 64, kSmall> Small;
+    if (c.tile == kSmall) {
+        launch(weight_grad_kernel<Small>, blocks, Small::threads, s, one, a);
+    } else if (D != ZERO_DTYPE_FP32 && fast(w, c.whole > 0 ? w.T : c.per_split)) {
         a.shares = !w.bias ? 0 : c.tiles_k >= 4 ? 1 : c.tiles_k >= 2 ? 2 : 4;
-        if constexpr (C::D != ZERO_DTYPE_FP32) run_fast<C::D>(a, blocks, s, one);
+        if constexpr (D != ZERO_DTYPE_FP32) run_fast<D>(a, blocks, s, one);
     } else {
-        launch(weight_grad_kernel<C>, blocks, C::threads, s, one, a);
+        launch(weight_grad_kernel<Large>, blocks, Large::threads, s, one, a);
     }
     if (c.splits > 1) {
         one = {nullptr, ev.stop};
-        const dim3 grid(uint32_t((int64_t(c.tiles_k) * c.tiles_n - c.whole) * kJoinBlocks));
-        if (w.out_type == ZERO_DTYPE_FP16) launch(split_join_kernel<ZERO_DTYPE_FP16>, grid, kJoinThreads, s, one, a);
-        else if (w.out_type == ZERO_DTYPE_BF16) launch(split_join_kernel<ZERO_DTYPE_BF16>, grid, kJoinThreads, s, one, a);
-        else launch(split_join_kernel<ZERO_DTYPE_FP32>, grid, kJoinThreads, s, one, a);
+        if (c.tile == kSmall) join<kSmall>(a, s, one);
+        else join<kTile>(a, s, one);
     }
     return hipGetLastError();
 }
@@ -885,9 +957,9 @@ hipError_t run(const WeightGradLaunch& w, hipStream_t s, const KernelEvents& ev)
 int64_t weight_grad_work(int64_t T, int64_t n, int64_t k, int32_t dy_type) { return cut_for(T, n, k, dy_type).bytes(); }
 
 hipError_t launch_weight_grad(const WeightGradLaunch& w, hipStream_t s, const KernelEvents& ev) {
-    if (w.dy_type == ZERO_DTYPE_BF16) return run<Config<ZERO_DTYPE_BF16, 64>>(w, s, ev);
-    if (w.dy_type == ZERO_DTYPE_FP16) return run<Config<ZERO_DTYPE_FP16, 64>>(w, s, ev);
-    return run<Config<ZERO_DTYPE_FP32, 32>>(w, s, ev);
+    if (w.dy_type == ZERO_DTYPE_BF16) return run<ZERO_DTYPE_BF16>(w, s, ev);
+    if (w.dy_type == ZERO_DTYPE_FP16) return run<ZERO_DTYPE_FP16>(w, s, ev);
+    return run<ZERO_DTYPE_FP32>(w, s, ev);
 }
 
 }  // namespace zp
