@@ -28,8 +28,9 @@ constexpr int kThreads = 256;
 // Row of the table that token i names, or -1.
 template <typename I>
 __device__ __forceinline__ int64_t named_row(const void* tokens, int64_t i, int64_t first, int64_t rows) {
-    const uint64_t r = uint64_t(int64_t(((Global<const I>*)tokens)[i])) - uint64_t(first);
-    return r < uint64_t(rows) ? int64_t(r) : -1;
+    const int64_t t = ((Global<const I>*)tokens)[i];
+    const uint64_t r = uint64_t(t) - uint64_t(first);   // right for every t that is not below
+    return t >= first && r < uint64_t(rows) ? int64_t(r) : -1;
 }
 
 struct LookupArgs {

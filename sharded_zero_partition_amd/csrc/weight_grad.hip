@@ -580,11 +580,11 @@ struct Fast {
 // `to` + kOffset on (m0).
 template <int kOffset>
 __device__ __forceinline__ void load16(uint32_t to, uint32_t from, u32x4 buffer) {
-    asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds" ::"s"(to), "i"(kOffset), "v"(from), "s"(buffer) : "scc");
+    asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_dwordx4 %2, %3, 0 offen lds" ::"s"(to), "i"(kOffset), "v"(from), "s"(buffer) : "scc", "m0");
 }
 template <int kOffset>
 __device__ __forceinline__ void load1(uint32_t to, uint32_t from, u32x4 buffer) {
-    asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_ubyte %2, %3, 0 offen lds" ::"s"(to), "i"(kOffset), "v"(from), "s"(buffer) : "scc");
+    asm volatile("s_add_u32 m0, %0, %1\n\ts_nop 0\n\tbuffer_load_ubyte %2, %3, 0 offen lds" ::"s"(to), "i"(kOffset), "v"(from), "s"(buffer) : "scc", "m0");
 }
 
 template <int D, int kSums>
@@ -889,7 +889,8 @@ Cut cut_for(int64_t T, int64_t n, int64_t k, int32_t dy_type) {
         large = cut_into(few ? Times{kTile, 1, 0, 7.5, 2.6} : Times{kTile, 1, 0, 10, 1.5}, T, n, k);
         small = cut_into({kSmall, 3, 4, 0.7, 0.85}, T, n, k);
     }
-    return small.cost < large.cost ? small : large;
+    const bool fits = small.blocks() < int64_t(1) << 23;   // threads of a launch, in 32 bits
+    return fits && small.cost < large.cost ? small : large;
 }
 
 // Whether the loads of the fast kernel reach everything: 16 bytes of dy at a time,

@@ -171,3 +171,22 @@ def test_refusals_of_the_binding():
             zp.embedding_grad(y, bad, table)
     with pytest.raises(zp.ZeroError, match="overlaps"):
         zp.embedding_lookup(table, t, table[:3])
+
+
+def test_tokens_and_first_rows_at_the_ends_of_their_range():
+    """Tokens whose distance to the first row is beyond 64 bits name no row."""
+    least, most = -2 ** 63, 2 ** 63 - 1
+    table = torch.arange(1, 5, device="cuda").float()[:, None].expand(4, 9).contiguous()
+    t = torch.tensor([least, least + 1, -1, 0, most - 3, most - 1, most], device="cuda")
+    for first, named in ((most - 3, [0, 0, 0, 0, 1, 3, 4]), (least, [1, 2, 0, 0, 0, 0, 0]), (-1, [0, 0, 1, 2, 0, 0, 0])):
+        y, d = torch.empty(7, 9, device="cuda"), torch.empty_like(table)
+        zp.embedding_lookup(table, t, y, first=first)
+        assert y[:, 0].tolist() == named
+        zp.embedding_grad(torch.ones_like(y), t, d, first=first)
+        assert d[:, 8].tolist() == [float(named.count(r + 1)) for r in range(4)]
+    small = torch.tensor([-2 ** 31, 2 ** 31 - 1], device="cuda", dtype=torch.int32)
+    y = torch.empty(2, 9, device="cuda")
+    zp.embedding_lookup(table, small, y, first=2 ** 31 - 2)
+    assert y[:, 0].tolist() == [0, 2]
+    zp.embedding_lookup(table, small, y, first=most)
+    assert y[:, 0].tolist() == [0, 0]

@@ -96,3 +96,13 @@ def test_scales_of_every_size(T, n, k):
     bad[32:64] = True
     assert bool(again[:, bad].isnan().all())
     assert torch.equal(again[:, ~bad], w[:, ~bad])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,n", [(1003, 70000), (200, 4096), (40, 100), (9000, 64)])
+def test_a_bias_alone(dtype, T, n):
+    """A layer of no inputs, whose gradient is that of its bias."""
+    dy = Guarded(T, n, DTYPES[dtype], 0, 0, torch.randint(-3, 4, (T, n), device="cuda", dtype=torch.int8))
+    b = torch.ones(n, device="cuda")
+    zp.weight_grad(dy.t, zp.Checkpoint(T, 0), torch.empty(n, 0, device="cuda"), bias=b, accumulate=True)
+    assert torch.equal(b.double(), dy.t.double().sum(0) + 1)
