@@ -1,5 +1,8 @@
 // embedding.hip -- rows of a table by tokens, and the table's gradient (gfx950).
 //
+// Both are bound by HBM: a lookup reads and writes each row once (8192 rows of 5120 bf16:
+// 168 MB in 25 us), a gradient reads dy once and writes the table once.
+//
 // The gradient adds up rows of dy that have the same token.  Atomic adds would
 // take an order of their own each time; here the tokens are sorted (stable, so a
 // row's summands come as the tokens do), the sorted list is cut into tiles of
@@ -7,8 +10,9 @@
 // are as uneven as text is (the most frequent one has several per cent), and
 // equal tiles make the waves' work equal.  A run of equal tokens inside a tile
 // is a finished row; one that crosses tiles leaves a partial sum for each, which
-// a last kernel adds in order.  Rows that no token names are filled with zeros by
-// the same launch that sums the tiles.
+// a last kernel adds in order.  Rows that no token names are zeros from the start.
+//   8192 tokens, 50257 x 5120 bf16: sorting under the fill 99 us, sums 22, joining 6
+//   32768 tokens, 1600 fp16 columns added to fp32: sorting 25 us, sums 39, joining 11
 #include <type_traits>
 
 #include "octets.hpp"
@@ -64,7 +68,7 @@ __global__ __launch_bounds__(kThreads) void lookup_kernel(const LookupArgs a) {
         Octet<DO> y;
 #pragma unroll
         for (int k = 0; k < kOctet; ++k) y.set(k, r[u] < 0 ? 0.0f : x[u].get(k) * a.e.scale);
-        store_octet<DO>(place<DO>(a.e.out, i[u], a.e.s_out, col[u]), left[u], y);
+        store_octet<DO, true>(place<DO>(a.e.out, i[u], a.e.s_out, col[u]), left[u], y);
     }
 }
 
@@ -73,11 +77,44 @@ __global__ __launch_bounds__(kThreads) void lookup_kernel(const LookupArgs a) {
 // that name no row count as row `rows` and come last
 // ---------------------------------------------------------------------------
 
+// Zeros into the whole table, by the blocks of the first sorting launch that come after
+// the sorting ones: sorting waits for memory, a fill is nothing but memory, which it writes
+// at 6 TB/s.  (The gradient of 8192 tokens of 50257 x 5120 bf16 takes 125 us; 142 where the
+// launch that sums filled only the rows that no token names.)
+constexpr int kFillRows = 16;   // of a block
+struct Fill {
+    char* out;
+    int64_t pitch, rows, cols;   // bytes; cols in 16-bit units, whatever the type; rows: 0 if nothing is filled
+    Divisor per_row;             // 16-byte pieces of a row
+    int32_t before;              // blocks of the launch that sort
+    int64_t blocks() const { return (rows + kFillRows - 1) / kFillRows; }
+};
+template <int kBlock>
+__device__ __forceinline__ void fill(const Fill& f) {
+    const int64_t r0 = (int64_t(blockIdx.x) - f.before) * kFillRows;
+    const int64_t r1 = r0 + kFillRows < f.rows ? r0 + kFillRows : f.rows;
+    Octet<ZERO_DTYPE_FP16> zero;
+    zero.zero();
+    if (f.per_row.g < kBlock) {   // short rows: all of them at once
+        const uint32_t all = uint32_t(r1 - r0) * f.per_row.g;
+        for (uint32_t x = threadIdx.x; x < all; x += kBlock) {
+            const uint32_t r = divide(x, f.per_row);
+            const int64_t c = int64_t(x - r * f.per_row.g) * kOctet;
+            store_octet<ZERO_DTYPE_FP16, true>(f.out + (r0 + r) * f.pitch + 2 * c, f.cols - c, zero);
+        }
+        return;
+    }
+    for (int64_t r = r0; r < r1; ++r)
+        for (int64_t c = int64_t(threadIdx.x) * kOctet; c < f.cols; c += kBlock * kOctet)
+            store_octet<ZERO_DTYPE_FP16, true>(f.out + r * f.pitch + 2 * c, f.cols - c, zero);
+}
+
 struct SortArgs {
     const void* tokens;
     int64_t n, first, rows;
     uint32_t* key;      // sorted rows
     uint32_t* order;    // and their places
+    Fill fill;          // of the first launch
 };
 
 template <typename I>
@@ -94,6 +131,7 @@ constexpr int kRankThreads = 512, kRankShare = 16, kRankTokens = kRankThreads / 
 template <typename I>
 __global__ __launch_bounds__(kRankThreads) void rank_kernel(const SortArgs a) {
     __shared__ u32x4 keys[kRankMost / 4];
+    if (int(blockIdx.x) >= a.fill.before) return fill<kRankThreads>(a.fill);
     const int n = int(a.n), tid = int(threadIdx.x), fours = (n + 3) / 4;
     uint32_t* flat = reinterpret_cast<uint32_t*>(keys);
     constexpr int ahead = 8;
@@ -162,6 +200,7 @@ __device__ __forceinline__ void digit_load(const DigitArgs& a, int64_t i0, int64
 template <typename I, bool kFirst>
 __global__ __launch_bounds__(kThreads) void digit_count_kernel(const DigitArgs a) {
     __shared__ uint32_t count[kMaxDigits];
+    if (kFirst && int(blockIdx.x) >= a.s.fill.before) return fill<kThreads>(a.s.fill);
     for (int d = threadIdx.x; d < a.digits; d += kThreads) count[d] = 0;
     __syncthreads();
     const int wave = int(threadIdx.x) >> 6, lane = int(threadIdx.x) & 63;
@@ -279,9 +318,7 @@ __global__ __launch_bounds__(kThreads) void digit_move_kernel(const DigitArgs a)
 // ---------------------------------------------------------------------------
 
 constexpr int kChunk = 64 * kOctet;   // columns of a wave
-template <int D>
-constexpr int kAhead = D == ZERO_DTYPE_FP32 ? 8 : 16;   // rows of dy loaded at once
-constexpr int kZeroRows = 16;         // table rows that a block looks through for unnamed ones
+constexpr int kAhead = 4;             // rows of dy loaded at once: few registers, more waves (16: 81 us where 4 take 71)
 
 struct SumArgs {
     EmbedLaunch e;
@@ -290,9 +327,7 @@ struct SumArgs {
     float* part;              // [tiles][2][chunks * kChunk]: of the run that enters a tile, and of the one that leaves it
     int64_t tiles;
     int32_t tile;             // length: 8, 16, 32 or a multiple of 64
-    Divisor per_row;          // octets of a row
     int32_t chunks;
-    int64_t tile_blocks;      // blocks that sum tiles; those after them fill rows with zeros
 };
 
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return uint32_t(__builtin_amdgcn_readfirstlane(int(x))); }
@@ -340,7 +375,7 @@ __device__ __forceinline__ void sum_tile(const SumArgs& a, int64_t t, int chunk)
         const int64_t p = p0 + lane;
         const uint32_t keys = p < hi ? a.key[p] : none, places = p < hi ? a.order[p] : 0;
         const int m = int(hi - p0 < 64 ? hi - p0 : 64);
-        constexpr int ahead = kAhead<DI>;
+        constexpr int ahead = kAhead;
         for (int j0 = 0; j0 < m; j0 += ahead) {
             Octet<DI> x[ahead];
 #pragma unroll
@@ -369,100 +404,52 @@ __device__ __forceinline__ void sum_tile(const SumArgs& a, int64_t t, int chunk)
     flush(hi < a.e.n && uniform(a.key[hi < a.e.n ? hi : 0]) == run);
 }
 
-// First place of the sorted list whose row is not below r: 64 probes at a time.
-__device__ __forceinline__ int64_t lower_bound(const uint32_t* key, int64_t n, uint32_t r) {
-    const int lane = int(threadIdx.x) & 63;
-    int64_t lo = 0, len = n;   // the answer is in [lo, lo + len]
-    while (len > 0) {
-        const int64_t step = (len + 63) / 64;
-        const int64_t p = lo + step * lane;
-        const bool below = step * lane < len && key[p] < r;
-        const int c = __popcll(__ballot(below));   // probes 0 .. c - 1 are below
-        if (c == 0) return lo;
-        const int64_t end = lo + len;
-        lo += step * (c - 1) + 1;
-        len = step - 1 < end - lo ? step - 1 : end - lo;
-    }
-    return lo;
-}
-
 template <int DI, int DO>
 __global__ __launch_bounds__(kThreads) void tile_sum_kernel(const SumArgs a) {
-    const int wave = int(threadIdx.x) >> 6;
-    if (int64_t(blockIdx.x) < a.tile_blocks) {
-        const int64_t w = int64_t(blockIdx.x) * (kThreads / 64) + wave;
-        const int64_t t = w / a.chunks;
-        if (t < a.tiles) sum_tile<DI, DO>(a, t, int(w - t * a.chunks));
-        return;
-    }
-    // zeros into the unnamed ones of kZeroRows rows
-    __shared__ uint32_t named;
-    const int64_t r0 = (int64_t(blockIdx.x) - a.tile_blocks) * kZeroRows;
-    const int64_t r1 = r0 + kZeroRows < a.e.rows ? r0 + kZeroRows : a.e.rows;
-    if (threadIdx.x == 0) named = 0;
-    __syncthreads();
-    const int64_t begin = lower_bound(a.key, a.e.n, uint32_t(r0));
-    for (int64_t p = begin + threadIdx.x; p < a.e.n; p += kThreads) {
-        const uint32_t k = a.key[p];
-        if (k >= r1) break;
-        atomicOr(&named, 1u << (k - uint32_t(r0)));
-    }
-    __syncthreads();
-    const uint32_t there = uniform(named);
-    Octet<DO> zero;
-    zero.zero();
-    if (a.per_row.g < kThreads) {   // short rows: all of them at once
-        const uint32_t all = uint32_t(r1 - r0) * a.per_row.g;
-        for (uint32_t x = threadIdx.x; x < all; x += kThreads) {
-            const uint32_t r = divide(x, a.per_row);
-            const int64_t c = int64_t(x - r * a.per_row.g) * kOctet;
-            if (!(there >> r & 1)) store_octet<DO>(place<DO>(a.e.out, r0 + r, a.e.s_out, c), a.e.cols - c, zero);
-        }
-        return;
-    }
-    for (int64_t r = r0; r < r1; ++r) {
-        if (there >> (r - r0) & 1) continue;
-        for (int64_t c = int64_t(threadIdx.x) * kOctet; c < a.e.cols; c += kThreads * kOctet)
-            store_octet<DO>(place<DO>(a.e.out, r, a.e.s_out, c), a.e.cols - c, zero);
-    }
+    const int64_t w = int64_t(blockIdx.x) * (kThreads / 64) + (int(threadIdx.x) >> 6);
+    const int64_t t = w / a.chunks;
+    if (t < a.tiles) sum_tile<DI, DO>(a, t, int(w - t * a.chunks));
 }
 
-// Adds up the partial sums of a run that crosses tiles: a block for each tile that
-// such a run leaves from where it began, and 512 columns.  Its four waves have a
-// quarter of the tiles each.
-template <int DO>
-__global__ __launch_bounds__(kThreads) void join_kernel(const SumArgs a) {
-    __shared__ f32x4 sums[3][2][64];
-    const int lane = int(threadIdx.x) & 63, wave = int(threadIdx.x) >> 6;
-    const int64_t t = int64_t(blockIdx.x) / a.chunks;
-    const int64_t end = (t + 1) * a.tile;   // below n
-    const int64_t lo = t * a.tile;
+// Adds up the partial sums of the runs that cross tiles, 512 columns of them.  A wave looks
+// at one tile's end; a run that leaves the tile and began in it is the wave's own if it
+// crosses few tiles, and else the block's, whose four waves have a quarter of its tiles each.
+constexpr int kJoinWaves = kThreads / 64, kJoinOwn = 8;
+struct Run {
+    int64_t first, count;   // tiles
+    uint32_t row;
+};
+// The run that leaves tile t and began in it; count 0: there is none.
+__device__ __forceinline__ Run run_from(const SumArgs& a, int64_t t) {
+    const int lane = int(threadIdx.x) & 63;
+    const int64_t end = (t + 1) * a.tile, lo = t * a.tile;   // end is below n
     const uint32_t after = a.key[end], before = a.key[end - 1], at = a.key[lo], earlier = a.key[lo > 0 ? lo - 1 : 0];
-    const uint32_t run = uniform(after);
-    if (run >= uint32_t(a.e.rows) || uniform(before) != run) return;
-    if (lo > 0 && uniform(at) == run && uniform(earlier) == run) return;   // began earlier
-    // the last tile that the run enters: the sorted list's run ends there
+    Run r = {t, 0, uniform(after)};
+    if (r.row >= uint32_t(a.e.rows) || uniform(before) != r.row) return r;
+    if (lo > 0 && uniform(at) == r.row && uniform(earlier) == r.row) return r;   // began earlier
+    // the last tile that the run enters
     int64_t last = t + 1;
     for (;;) {
         const int64_t p = (last + 1 + lane) * a.tile;
-        const uint64_t on = __ballot(p < a.e.n && a.key[p < a.e.n ? p : 0] == run && a.key[p < a.e.n ? p - 1 : 0] == run);
+        const uint64_t on = __ballot(p < a.e.n && a.key[p < a.e.n ? p : 0] == r.row && a.key[p < a.e.n ? p - 1 : 0] == r.row);
         const int c = on == ~uint64_t(0) ? 64 : __ffsll((unsigned long long)~on) - 1;
         last += c;
         if (c < 64) break;
     }
-    const int64_t col = (int64_t(blockIdx.x) - t * a.chunks) * kChunk + lane * kOctet;
+    r.count = last - t + 1;
+    return r;
+}
+// The sum of the run's parts `begin` .. `stop` - 1, in order.
+__device__ __forceinline__ void add_parts(const SumArgs& a, const Run& r, int64_t begin, int64_t stop, int64_t col, f32x4 acc[2]) {
     const int64_t half = int64_t(a.chunks) * kChunk;
-    const int64_t count = last - t + 1, share = (count + 3) / 4;
-    const int64_t begin = t + wave * share, stop = begin + share < last + 1 ? begin + share : last + 1;
-    f32x4 acc[2] = {};
     constexpr int ahead = 8;
     for (int64_t u = begin; u < stop; u += ahead) {
         f32x4 x[ahead][2];
 #pragma unroll
         for (int j = 0; j < ahead; ++j) {
             const int64_t v = u + j < stop ? u + j : stop - 1;
-            // (the run began in t, at its first place or after it: it leaves t, and enters the others)
-            const float* p = a.part + (v * 2 + (v == t ? 1 : 0)) * half + col;
+            // (it leaves its first tile, wherever it began there, and enters the others)
+            const float* p = a.part + ((r.first + v) * 2 + (v == 0 ? 1 : 0)) * half + col;
             x[j][0] = ((Global<const f32x4>*)p)[0];
             x[j][1] = ((Global<const f32x4>*)p)[1];
         }
@@ -473,19 +460,49 @@ __global__ __launch_bounds__(kThreads) void join_kernel(const SumArgs a) {
                 acc[1] += x[j][1];
             }
     }
-    if (wave > 0) {
-        sums[wave - 1][0][lane] = acc[0];
-        sums[wave - 1][1][lane] = acc[1];
+}
+template <int DO>
+__device__ __forceinline__ void put_run(const SumArgs& a, const Run& r, int64_t col, const f32x4 acc[2]) {
+    const float all[kOctet] = {acc[0].x, acc[0].y, acc[0].z, acc[0].w, acc[1].x, acc[1].y, acc[1].z, acc[1].w};
+    finish_row<DO>(a.e, r.row, col, a.e.cols - col, all);
+}
+template <int DO>
+__global__ __launch_bounds__(kThreads) void join_kernel(const SumArgs a) {
+    __shared__ f32x4 sums[kJoinWaves - 1][2][64];
+    __shared__ Run runs[kJoinWaves];
+    const int lane = int(threadIdx.x) & 63, wave = int(uniform(threadIdx.x >> 6));
+    const int64_t four = int64_t(blockIdx.x) / a.chunks, t = four * kJoinWaves + wave;
+    const int64_t col = (int64_t(blockIdx.x) - four * a.chunks) * kChunk + lane * kOctet;
+    Run own = {t, 0, 0};
+    if (t < a.tiles - 1) own = run_from(a, t);
+    if (lane == 0) runs[wave] = own;
+    if (own.count > 0 && own.count <= kJoinOwn) {
+        f32x4 acc[2] = {};
+        add_parts(a, own, 0, own.count, col, acc);
+        put_run<DO>(a, own, col, acc);
     }
     __syncthreads();
-    if (wave > 0) return;
-    for (int w = 1; w < 4; ++w)
-        if (w * share < count) {
-            acc[0] += sums[w - 1][0][lane];
-            acc[1] += sums[w - 1][1][lane];
+    for (int i = 0; i < kJoinWaves; ++i) {
+        const Run r = runs[i];
+        if (r.count <= kJoinOwn) continue;   // the same for all waves
+        const int64_t share = (r.count + kJoinWaves - 1) / kJoinWaves, begin = wave * share;
+        f32x4 acc[2] = {};
+        add_parts(a, r, begin, begin + share < r.count ? begin + share : r.count, col, acc);
+        if (wave > 0) {
+            sums[wave - 1][0][lane] = acc[0];
+            sums[wave - 1][1][lane] = acc[1];
         }
-    const float all[kOctet] = {acc[0].x, acc[0].y, acc[0].z, acc[0].w, acc[1].x, acc[1].y, acc[1].z, acc[1].w};
-    finish_row<DO>(a.e, run, col, a.e.cols - col, all);
+        __syncthreads();
+        if (wave == 0) {
+            for (int w = 1; w < kJoinWaves; ++w)
+                if (w * share < r.count) {
+                    acc[0] += sums[w - 1][0][lane];
+                    acc[1] += sums[w - 1][1][lane];
+                }
+            put_run<DO>(a, r, col, acc);
+        }
+        __syncthreads();
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -532,13 +549,13 @@ Plan plan_for(int64_t n, int64_t rows, int64_t cols) {
 }
 
 template <int DI, int DO>
-void run_sum(const SumArgs& a, int64_t blocks, hipStream_t s, const KernelEvents& ev) {
+void run_sum(const SumArgs& a, hipStream_t s, const KernelEvents& ev) {
     const bool join = a.tiles > 1;
     KernelEvents one = {ev.start, join ? nullptr : ev.stop};
-    launch(tile_sum_kernel<DI, DO>, dim3(uint32_t(blocks)), kThreads, s, one, a);
+    launch(tile_sum_kernel<DI, DO>, dim3(uint32_t((a.tiles * a.chunks + 3) / 4)), kThreads, s, one, a);
     if (!join) return;
     one = {nullptr, ev.stop};
-    launch(join_kernel<DO>, dim3(uint32_t((a.tiles - 1) * a.chunks)), kThreads, s, one, a);
+    launch(join_kernel<DO>, dim3(uint32_t((a.tiles - 1 + kJoinWaves - 1) / kJoinWaves * a.chunks)), kThreads, s, one, a);
 }
 
 template <int DI, int DO>
@@ -584,7 +601,8 @@ int64_t embedding_work(int64_t n, int64_t rows, int64_t cols) { return plan_for(
 bool embedding_fits(int64_t n, int64_t rows, int64_t cols) {
     const Plan p = plan_for(n, rows, cols);
     constexpr int64_t most = int64_t(1) << 24;   // blocks of a launch
-    return (p.tiles * p.chunks + 3) / 4 + (rows + kZeroRows - 1) / kZeroRows < most && p.tiles * p.chunks < most;
+    // the first launch sorts and fills, by 512 threads a block
+    return (n + kRankTokens - 1) / kRankTokens + (rows + kFillRows - 1) / kFillRows < most / 2 && p.tiles * p.chunks < most;
 }
 
 hipError_t launch_embedding_grad(const EmbedLaunch& e, hipStream_t s, const KernelEvents& ev) {
@@ -597,17 +615,21 @@ hipError_t launch_embedding_grad(const EmbedLaunch& e, hipStream_t s, const Kern
     a.tiles = p.tiles;
     a.chunks = p.chunks;
     a.part = reinterpret_cast<float*>(work + p.off_part);
-    a.per_row = octets_of(e.cols);
     const int last = p.passes ? (p.passes - 1) & 1 : 0;   // the lists that the last pass writes
     a.key = list(p.off_key[last]);
     a.order = list(p.off_order[last]);
 
-    SortArgs so = {e.tokens, e.n, e.first, e.rows, list(p.off_key[0]), list(p.off_order[0])};
+    SortArgs so = {e.tokens, e.n, e.first, e.rows, list(p.off_key[0]), list(p.off_order[0]), {}};
+    const int64_t units = e.out_type == ZERO_DTYPE_FP32 ? 2 : 1;   // of 16 bits
+    so.fill = {static_cast<char*>(e.out), 2 * units * e.s_out, e.accumulate ? 0 : e.rows, units * e.cols, octets_of(units * e.cols),
+               p.passes ? p.blocks : int32_t((e.n + kRankTokens - 1) / kRankTokens)};
+    const dim3 first(uint32_t(so.fill.before + so.fill.blocks()));
     KernelEvents one = {ev.start, nullptr};
     const bool wide = e.token_bytes == 8;
-    if (p.passes == 0 && e.n > 0) {
-        const dim3 grid(uint32_t((e.n + kRankTokens - 1) / kRankTokens));
-        launch(wide ? rank_kernel<int64_t> : rank_kernel<int32_t>, grid, kRankThreads, s, one, so);
+    if (p.passes == 0) {
+        if (e.n == 0) one.stop = ev.stop;   // nothing comes after
+        launch(wide ? rank_kernel<int64_t> : rank_kernel<int32_t>, first, kRankThreads, s, one, so);
+        if (e.n == 0) return hipGetLastError();
         one.start = nullptr;
     }
     for (int k = 0; k < p.passes; ++k) {
@@ -624,15 +646,12 @@ hipError_t launch_embedding_grad(const EmbedLaunch& e, hipStream_t s, const Kern
         d.shift = k * __builtin_ctz(uint32_t(p.digits));
         const KernelEvents none;
         const auto count = k > 0 ? digit_count_kernel<int32_t, false> : wide ? digit_count_kernel<int64_t, true> : digit_count_kernel<int32_t, true>;
-        launch(count, dim3(p.blocks), kThreads, s, one, d);
+        launch(count, k > 0 ? dim3(p.blocks) : first, kThreads, s, one, d);
         one.start = nullptr;
         const auto move = k > 0 ? digit_move_kernel<int32_t, false> : wide ? digit_move_kernel<int64_t, true> : digit_move_kernel<int32_t, true>;
         launch(move, dim3(p.blocks), kThreads, s, none, d);
     }
-    a.tile_blocks = (p.tiles * p.chunks + 3) / 4;
-    const int64_t zero_blocks = e.accumulate ? 0 : (e.rows + kZeroRows - 1) / kZeroRows;
-    for_types(e.type, e.out_type,
-              [&](auto di, auto d_o) { run_sum<decltype(di)::value, decltype(d_o)::value>(a, a.tile_blocks + zero_blocks, s, {one.start, ev.stop}); });
+    for_types(e.type, e.out_type, [&](auto di, auto d_o) { run_sum<decltype(di)::value, decltype(d_o)::value>(a, s, {one.start, ev.stop}); });
     return hipGetLastError();
 }
 
