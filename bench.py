@@ -125,6 +125,10 @@ def parse_args():
                     help="instead of the default measurement: the tensor-set kernels (gradient norm, "
                          "AdamW with fp32 and MXFP8 states, state conversion) on the tensor pieces of "
                          "the 13B rank-63 shard, K timed calls each, one JSON line")
+    ap.add_argument("--layer", action="store_true",
+                    help="instead of the default measurement: 8-bit activation checkpoints and the gradients made "
+                         "from them, for the feed-forward layer and the embedding of the 13B model on 8192 tokens "
+                         "(bf16), K timed calls each, one JSON line")
     ap.add_argument("--no-pack", action="store_true", help="skip the bucket-pack measurement")
     ap.add_argument("--no-cpu-baseline", action="store_true", help="skip the CPU oracle timing")
     ap.add_argument("--calibration-copy", action="store_true",
@@ -299,6 +303,68 @@ def tensor_set_main(args):
     print(json.dumps(result), flush=True)
 
 
+def layer_main(args):
+    """One JSON line: the embedding and the feed-forward layer (width 5120, hidden
+    20480) of the 13B model on 8192 tokens in bf16: 8-bit checkpoints, activation,
+    and all parameter gradients made from them, each call's kernels timed by
+    their events."""
+    import numpy as np
+    import torch
+
+    import sharded_zero_partition_amd as zp
+
+    torch.cuda.set_device(0)
+    tokens, width, hidden, vocab = 8192, 5120, 20480, 50257
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    new = lambda *s: torch.randn(*s, device="cuda", generator=gen).to(torch.bfloat16)   # noqa: E731
+    table, x, z, h, dy, dz = (new(*s) for s in ((vocab, width), (tokens, width), (tokens, hidden), (tokens, hidden),
+                                                (tokens, width), (tokens, hidden)))
+    kept = {k: zp.Checkpoint(tokens, c) for k, c in (("x", width), ("z", hidden), ("h", hidden))}
+    up, down, bias = torch.empty_like(new(hidden, width)), torch.empty_like(new(width, hidden)), torch.empty_like(z[0])
+    # as uneven as text: log-uniform ranks
+    named = (torch.exp(torch.rand(tokens, device="cuda", generator=gen) * float(np.log(vocab))) - 1).long()
+    rows, n, m = [], tokens * width, tokens * hidden
+
+    def timed(name, call, bytes_=None, flops=None):
+        for _ in range(args.warmup):
+            call()
+        torch.cuda.synchronize()
+        zp.set_kernel_timing(True)
+        for _ in range(args.steps):
+            call()
+        torch.cuda.synchronize()
+        t = zp.kernel_times()
+        zp.set_kernel_timing(False)
+        s = float(np.mean(t)) * 1e-3
+        if flops:
+            line = {"bound": "mfma", "achieved": round(flops / s / 1e12, 1), "peak": 2500.0, "unit": "TFLOP/s"}
+        else:
+            line = {"bound": "hbm", "achieved": round(bytes_ / s / 1e9, 1), "peak": HBM_PEAK_GBS, "unit": "GB/s"}
+        line["frac"] = round(line["achieved"] / line["peak"], 4)
+        rows.append({"kernel": name, "ms": round(s * 1e3, 4), "ms_median": round(float(np.median(t)), 4), "roofline": line})
+        return rows[-1]
+
+    timed("embedding lookup", lambda: zp.embedding_lookup(table, named, x), 4 * n)
+    timed("checkpoint store", lambda: kept["x"].store(x), 3 * n + n // 32)
+    timed("checkpoint load", lambda: kept["x"].load(x), 3 * n + n // 32)
+    timed("gelu_tanh with checkpoints of its input and result",
+          lambda: zp.activation("gelu_tanh", z, h, kept["z"], out_checkpoint=kept["h"]), 6 * m + m // 16)
+    timed("gelu_tanh gradient", lambda: zp.activation_grad("gelu_tanh", h, kept["z"], dz), 5 * m + m // 32)
+    main_row = timed("weight gradient, 20480 x 5120, with bias", lambda: zp.weight_grad(dz, kept["x"], up, bias=bias), flops=2 * n * hidden)
+    timed("weight gradient, 5120 x 20480", lambda: zp.weight_grad(dy, kept["h"], down), flops=2 * n * hidden)
+    timed("embedding gradient", lambda: zp.embedding_grad(dy, named, table), 2 * n + 2 * vocab * width)
+    assert all(bool(torch.isfinite(t).all()) for t in (h, dz, up, down, bias, table))
+    total = sum(r["ms"] for r in rows)
+    result = {"metric": METRIC, "value": round(tokens / (total * 1e-3), 1), "unit": "tokens/s",
+              "n_gpus": 1, "steps": args.steps, "warmup": args.warmup, "ms_per_step": round(total, 4),
+              "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+              "config": {"workload": "8-bit activation checkpoints and the gradients made from them: embedding and "
+                                     "feed-forward layer of the 13B model", "tokens": tokens, "width": width,
+                         "hidden": hidden, "vocab": vocab},
+              "roofline": main_row["roofline"], "kernels": rows}
+    print(json.dumps(result), flush=True)
+
+
 def main():
     args = parse_args()
     world = int(os.environ.get("WORLD_SIZE", "1"))
@@ -315,6 +381,9 @@ def main():
         return
     if args.tensor_set:
         tensor_set_main(args)
+        return
+    if args.layer:
+        layer_main(args)
         return
 
     import numpy as np

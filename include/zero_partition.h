@@ -636,9 +636,9 @@ typedef struct zero_matrix {
  * s = scale[r * B + c / 32] stands for e4m3(code[r * 32 B + c]) * 2^(s - 127), B
  * being ceil(cols / 32).  Storing takes the least s >= 1 that brings the block's
  * largest magnitude to 448 or below, rounds to nearest, ties to even (what is
- * beyond 1.875 2^127 to that), and pads rows of codes with zeros.  A block with an inf or NaN gets s = 255 and codes
- * 0x7F: all of it reads back as NaN.  Other bytes than those that a store writes
- * are not a checkpoint. */
+ * beyond 1.875 2^127 to that), and pads rows of codes with zeros.  A block with
+ * an inf or NaN gets s = 255 and codes 0x7F: all of it reads back as NaN.  Other
+ * bytes than those that a store writes are not a checkpoint. */
 typedef struct zero_checkpoint {
     uint8_t* code;      /* rows * 32 B bytes, 16-byte aligned */
     uint8_t* scale;     /* rows * B bytes */
@@ -688,8 +688,12 @@ int zero_activation_grad(int32_t kind, const zero_matrix* dy, const zero_checkpo
 /* Gradients of a linear layer y[t, n] = sum_k x[t, k] w[n, k] + b[n] from the
  * gradient of y and the checkpoint of x:
  *   dw[n, k] = sum_t dy[t, n] x[t, k]        bias[n] = sum_t dy[t, n]
- * added to what is there when accumulate is 1.  Products are exact and sums in
- * fp32, in an order fixed by the sizes; results are rounded once.
+ * added to what is there when accumulate is 1.  Sums are in fp32, in an order
+ * fixed by the sizes; results are rounded once.  Products are exact for a dy in
+ * bf16 or fp32.  For one in fp16 x is taken in fp16 too, with a common scale for
+ * the tokens of each 32 columns, by which the largest of their blocks (448
+ * 2^(s - 127) for scale byte s) becomes 57344: blocks down to 2^-22 of that one keep all
+ * bits, the values of smaller ones are rounded to multiples of 2^(s - 158).
  *   dy          fp16, bf16 or fp32, T rows
  *   dw          fp16, bf16 or fp32, n by k; with transposed = 1 it is k by n (for a
  *               weight kept as inputs by outputs)
@@ -717,7 +721,7 @@ int zero_embedding_lookup(const zero_matrix* table, const void* tokens, int32_t 
  * touched then, and are zeros otherwise).  Tokens are sorted, each row's sum is
  * taken in fp32 in an order fixed by the tokens, and rounded once.
  *   dy           one row for each token, at most 2^30
- *   dtable       at most 2^30 rows
+ *   dtable       fewer than 2^27 rows
  *   work         device, zero_embedding_grad_work_bytes() bytes, 16-byte aligned,
  *                as for zero_weight_grad
  * Nothing written may overlap anything else.

@@ -10,11 +10,13 @@
 // value is read and written once, with the checkpoint's scales and codes
 // computed from the registers that the activation is computed from.
 //
-// Wide values pass by the caches where a pass has more of them than these hold at once
-// (8192 x 20480 bf16: gelu_tanh 128 us, its gradient 149; plain 144 and 162; rows of 13653,
-// which start anywhere: 92 and 90, plain 106 and 107).  A plain store keeps its loads in the
-// caches' way, where its input mostly comes from (20.4 us for 8192 x 5120, else 24), and so
-// do all codes (24 us for loading them back, else 19).
+// Wide values pass by the caches.  8192 x 20480 bf16 (845 MB), gelu_tanh and its gradient:
+// 130 and 152 us, plain 144 and 162, where the same buffers come again (the last-level
+// cache then keeps what does not pass by it); 141 and 149, plain 144 and 160, where all
+// that is read comes from HBM.  Rows of 13653, which start anywhere, gated silu: 92 and 91,
+// plain 106 and 107; from HBM 107 and 105, plain 105 and 104.  A plain store keeps its
+// loads in the caches' way, where its input mostly comes from (8192 x 5120: 20.3 us, else
+// 24), and so do all codes (24 us for loading them back, else 19).
 #include <type_traits>
 
 #include "octets.hpp"

@@ -602,7 +602,8 @@ bool embedding_fits(int64_t n, int64_t rows, int64_t cols) {
     const Plan p = plan_for(n, rows, cols);
     constexpr int64_t most = int64_t(1) << 24;   // blocks of a launch
     // the first launch sorts and fills, by 512 threads a block
-    return (n + kRankTokens - 1) / kRankTokens + (rows + kFillRows - 1) / kFillRows < most / 2 && p.tiles * p.chunks < most;
+    const int64_t sorting = p.passes ? p.blocks : (n + kRankTokens - 1) / kRankTokens;
+    return sorting + (rows + kFillRows - 1) / kFillRows < most / 2 && p.tiles * p.chunks < most;
 }
 
 hipError_t launch_embedding_grad(const EmbedLaunch& e, hipStream_t s, const KernelEvents& ev) {

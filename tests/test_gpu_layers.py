@@ -1,6 +1,7 @@
 """Embedding, gated feed-forward layer, their gradients and the optimizer's step together, as a training step runs them:
 each result against 64 bits, eager against captured, on streams and threads."""
 
+import os
 import threading
 
 import numpy as np
@@ -292,3 +293,27 @@ def test_version_counters_and_times():
     zp.activation("relu", z.detach(), z.detach())
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         z.sum().backward()
+
+
+def test_the_readme_s_layer():
+    """The README's code runs as it stands, and its gradients are those of its formulas on what it kept."""
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    code = next(b for b in text.split("```python\n")[1:] if b.startswith("tokens = ids.numel()")).split("```")[0]
+    g = torch.Generator(device="cuda").manual_seed(7)
+    vocab, width, hidden, n = 300, 64, 96, 130
+    make = lambda *s: (torch.randn(*s, device="cuda", generator=g) * 0.2).bfloat16()   # noqa: E731
+    v = dict(torch=torch, zp=zp, width=width, hidden=hidden, ids=torch.randint(0, vocab, (n,), device="cuda", generator=g),
+             table=make(vocab, width), w_gate=make(hidden, width), w_up=make(hidden, width), w_down=make(width, hidden), dy=make(n, width),
+             x=make(n, width), **{k: make(n, hidden) for k in ("g", "u", "h", "dh", "dg", "du")},
+             **{f"grad_{k}": torch.empty(s, device="cuda") for k, s in dict(gate=(hidden, width), up=(hidden, width), down=(width, hidden),
+                                                                         bias=(width,), table=(vocab, width)).items()})
+    exec(code, v)
+    kept = {k: held_in(c) for k, c in v["kept"].items()}
+    for dw, left, right in (("grad_down", "dy", "h"), ("grad_gate", "dg", "x"), ("grad_up", "du", "x")):
+        (want, want_b), (mag, mag_b) = A.weight_grad(wide(v[left]), kept[right])
+        assert (np.abs(wide(v[dw]) - want) <= (n + 2) * 2.0 ** -23 * mag).all()
+        if dw == "grad_down":
+            assert (np.abs(wide(v["grad_bias"]) - want_b) <= (n + 2) * 2.0 ** -23 * mag_b).all()
+    dx = wide(v["dg"] @ v["w_gate"] + v["du"] @ v["w_up"])
+    want, mag, count = A.embedding_grad(dx, v["ids"].cpu().numpy(), vocab, 0, 1.0)
+    assert (np.abs(wide(v["grad_table"]) - want) <= (count[:, None] + 3) * U * mag).all()
