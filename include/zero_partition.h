@@ -690,10 +690,12 @@ int zero_activation_grad(int32_t kind, const zero_matrix* dy, const zero_checkpo
  *   dw[n, k] = sum_t dy[t, n] x[t, k]        bias[n] = sum_t dy[t, n]
  * added to what is there when accumulate is 1.  Sums are in fp32, in an order
  * fixed by the sizes; results are rounded once.  Products are exact for a dy in
- * bf16 or fp32.  For one in fp16 x is taken in fp16 too, with a common scale for
- * the tokens of each 32 columns, by which the largest of their blocks (448
- * 2^(s - 127) for scale byte s) becomes 57344: blocks down to 2^-22 of that one keep all
- * bits, the values of smaller ones are rounded to multiples of 2^(s - 158).
+ * bf16 or fp32 (what is below 2^-126 in x, and in the low bits of an fp32 dy, is
+ * rounded to multiples of 2^-133).  For one in fp16 x is taken in fp16 too, with
+ * a common scale for the tokens of each 32 columns, by which the largest of their
+ * blocks (448 2^(s - 127) for scale byte s) becomes 57344: blocks down to 2^-22 of
+ * that one keep all bits, the values of smaller ones are rounded to multiples of
+ * 2^(s - 158).
  *   dy          fp16, bf16 or fp32, T rows
  *   dw          fp16, bf16 or fp32, n by k; with transposed = 1 it is k by n (for a
  *               weight kept as inputs by outputs)

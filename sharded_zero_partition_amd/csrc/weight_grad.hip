@@ -905,12 +905,13 @@ Cut cut_for(int64_t T, int64_t n, int64_t k, int32_t dy_type) {
 }
 
 // Whether the loads of the fast kernel reach everything: 16 bytes of dy at a time,
-// whole words up to the last value, offsets of 31 bits inside a block's `tokens`;
+// whole words up to the last value, dy's bytes of a block's `tokens` in 32 bits and
+// the codes' in 31 (the highest one marks what is behind a row);
 // and whether there are tokens enough for a turn of its loop.
 bool fast(const WeightGradLaunch& w, int64_t tokens) {
     constexpr int64_t most = int64_t(1) << 31;
     return tokens > 3 * kUnit && tokens < most && reinterpret_cast<uintptr_t>(w.dy) % 16 == 0 && w.s_dy % 8 == 0 && w.s_dy >= w.n &&
-           w.n % 2 == 0 && w.s_dy < most / 64 && tokens * w.s_dy < most / 2 && w.k < most / 64 && tokens * (w.k + 32) < most;
+           w.n % 2 == 0 && w.s_dy < most / 64 && tokens * w.s_dy < most && w.k < most / 64 && tokens * (w.k + 32) < most;
 }
 
 template <int D>

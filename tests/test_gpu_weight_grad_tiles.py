@@ -106,3 +106,33 @@ def test_a_bias_alone(dtype, T, n):
     b = torch.ones(n, device="cuda")
     zp.weight_grad(dy.t, zp.Checkpoint(T, 0), torch.empty(n, 0, device="cuda"), bias=b, accumulate=True)
     assert torch.equal(b.double(), dy.t.double().sum(0) + 1)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,n,k", [(40, 24, 70), (200, 4096, 4096)])
+def test_the_smallest_values(dtype, T, n, k):
+    """Values of x below 2^-126 are rounded in bf16 to multiples of 2^-133, a half of that off (with fp16 gradients their common
+    scale keeps them); sums are off by a unit of fp32 of the magnitudes, or 2^-149, for each token."""
+    t = DTYPES[dtype]
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(T, k, device="cuda", generator=g) * torch.exp2(-torch.randint(118, 140, (1, k), device="cuda", generator=g).float())
+    c, x64 = zp.Checkpoint(T, k), torch.empty(T, k, device="cuda")
+    c.store(x)
+    c.load(x64)
+    x64 = x64.double()
+    dy = torch.randn(T, n, device="cuda", generator=g).to(t)
+    w = torch.empty(n, k, device="cuda")
+    zp.weight_grad(dy, c, w)
+    want, mag, most = dy.double().t() @ x64, dy.double().abs().t() @ x64.abs(), dy.double().abs().sum(0)[:, None]
+    low = torch.zeros_like(most) if dtype == "fp16" else most * 2.0 ** -134
+    assert bool(((w.double() - want).abs() <= 3 * (T + 2) * (2.0 ** -23 * mag + 2.0 ** -149) + low).all())
+
+
+def test_more_than_2_31_bytes_of_gradients():
+    """Sums of 65536 whole numbers up to 24 are exact in fp32, the library's too."""
+    T, n, k = 65536, 20480, 4200
+    dy, x, c = whole(T, n, k, torch.bfloat16, 0, 9)
+    w, b = torch.empty(n, k, device="cuda"), torch.empty(n, device="cuda")
+    zp.weight_grad(dy.t, c, w, bias=b)
+    wide = dy.t.float()
+    assert torch.equal(w, wide.t() @ x) and torch.equal(b, wide.sum(0))
