@@ -8,7 +8,7 @@
 // and LDS reads that transpose (ds_read_b64_tr_b16) make the matrix unit's fragments of
 // them.  Bound by the matrix unit's feeding; measured, with 2 T n k operations:
 //   8192 x 8192 x 8192           bf16 776 us (1417 TFLOP/s), fp16 853 (1289)
-//   8192 x 20480 x 5120, bias    bf16 1322 to 1390 us (1236 to 1300)
+//   8192 x 20480 x 5120, bias    bf16 1292 to 1390 us (1236 to 1330)
 //   8192 x 4096 x 4096           fp32 619 us (444: three products for one)
 // where the library's product of two 16-bit matrices takes 733 us for 8192^3 (1501) and
 // 1075 to 1597 us for the second.
