@@ -189,13 +189,14 @@ struct Act {
             float rest;
             const float q = square(z), p = sigmoid(angle(z, q), &rest);
             *a = z * p;
-            *da = p + *a * (rest * (1.5957691f + 0.21406541f * q));
+            *da = p + *a * (rest * (float(k1) + float(3 * k3) * q));
         }
     }
+    static constexpr double k1 = 1.5957691216057308, k3 = 0.044715 * k1;   // 2 sqrt(2 / pi)
     static __device__ __forceinline__ float square(float z) { return fminf(z * z, 400.0f); }
     static __device__ __forceinline__ float angle(float z, float q) {   // 2 sqrt(2 / pi) (z + 0.044715 z^3), q = z^2
 #pragma clang fp contract(fast)
-        return z * (1.5957691f + 0.071354814f * q);
+        return z * (float(k1) + float(k3) * q);
     }
 };
 
