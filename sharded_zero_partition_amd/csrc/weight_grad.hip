@@ -137,6 +137,10 @@ struct GemmArgs {
 constexpr int64_t part_size(int w) { return w * w + w; }
 constexpr int64_t kUnit = 64;
 
+// What is left of x without its first part, of bits u: nothing of an infinity, where the
+// difference would be NaN.
+__device__ __forceinline__ float less(float x, uint32_t u) { return fabsf(x) == INFINITY ? 0.0f : x - number(u); }
+
 // 16 values of dy.
 template <int D>
 struct Chunk {
@@ -159,8 +163,8 @@ struct Chunk {
                     for (int j = 0; j < parts_of(D); ++j) {
                         const uint32_t ua = bits(a) & 0xFFFF0000u, ub = bits(b) & 0xFFFF0000u;
                         to[j][h][i] = ua >> 16 | ub;
-                        a -= number(ua);
-                        b -= number(ub);
+                        a = j ? a - number(ua) : less(a, ua);
+                        b = j ? b - number(ub) : less(b, ub);
                     }
                 }
             }
