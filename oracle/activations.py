@@ -61,7 +61,7 @@ def act(kind, z):
     with np.errstate(over="ignore", invalid="ignore"):
         if kind == "relu":
             d = np.where(z > 0, 1.0, np.where(z <= 0, 0.0, z))
-            return np.where(z < 0, 0.0, z), d, np.abs(d)
+            return np.where(z <= 0, 0.0, z), d, np.abs(d)
         if kind == "gelu":
             p = 0.5 * _erfc(-z / np.sqrt(2.0))
             q = z * np.exp(-z * z / 2) / np.sqrt(2 * np.pi)

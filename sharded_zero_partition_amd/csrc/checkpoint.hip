@@ -161,7 +161,7 @@ __device__ __forceinline__ float normal(float z, float* e) {
 template <int K>
 struct Act {
     static __device__ __forceinline__ float value(float z) {
-        if constexpr (K == ZERO_ACT_RELU) return z < 0.0f ? 0.0f : z;
+        if constexpr (K == ZERO_ACT_RELU) return z <= 0.0f ? 0.0f : z;
         if constexpr (K == ZERO_ACT_SILU) return z * sigmoid(z);
         if constexpr (K == ZERO_ACT_GELU) {
             float e;
@@ -173,7 +173,7 @@ struct Act {
     static __device__ __forceinline__ void both(float z, float* a, float* da) {
 #pragma clang fp contract(fast)
         if constexpr (K == ZERO_ACT_RELU) {
-            *a = z < 0.0f ? 0.0f : z;
+            *a = z <= 0.0f ? 0.0f : z;
             *da = z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;
         } else if constexpr (K == ZERO_ACT_GELU) {
             float e;
