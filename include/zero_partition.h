@@ -696,7 +696,7 @@ int zero_activation_grad(int32_t kind, const zero_matrix* dy, const zero_checkpo
  * blocks (448 2^(s - 127) for scale byte s) becomes 57344: blocks down to 2^-22 of
  * that one keep all bits, the values of smaller ones are rounded to multiples of
  * 2^(s - 158).
- *   dy          fp16, bf16 or fp32, T rows
+ *   dy          fp16, bf16 or fp32, T rows, at most 2^40
  *   dw          fp16, bf16 or fp32, n by k; with transposed = 1 it is k by n (for a
  *               weight kept as inputs by outputs)
  *   bias        n values of dw's type, or NULL
@@ -712,7 +712,8 @@ int zero_weight_grad(const zero_matrix* dy, const zero_checkpoint* x, const zero
 /* out[i] = scale * table[tokens[i] - first], in fp32, rounded once.  A token that
  * names no row (tokens[i] - first outside 0 .. rows - 1) gives zeros: padding,
  * or another rank's part of a table cut by rows.
- *   tokens       device, out->rows of them, int32 or int64 (token_bytes 4 or 8)
+ *   tokens       device, out->rows of them (at most 2^40), int32 or int64 (token_bytes
+ *                4 or 8)
  * out may not overlap the others.  Errors: as for zero_checkpoint_store. */
 int zero_embedding_lookup(const zero_matrix* table, const void* tokens, int32_t token_bytes, int64_t first,
                           float scale, const zero_matrix* out, void* stream);

@@ -12,6 +12,7 @@ namespace {
 
 constexpr int64_t kMaxCols = int64_t(1) << 31;    // exclusive
 constexpr int64_t kMaxSpan = int64_t(1) << 56;    // elements from a matrix's first to its last
+constexpr int64_t kMaxTokens = int64_t(1) << 40;  // also of matrices without columns, and of one row for all tokens
 
 int type_bytes(int32_t t) {
     switch (t) {
@@ -153,6 +154,7 @@ int check_tokens(const void* tokens, int32_t token_bytes, int64_t n, Area* area)
     if (token_bytes != 4 && token_bytes != 8) return fail(ZERO_ERR_INVALID_ARG, "token_bytes must be 4 or 8");
     *area = Area();
     if (n == 0) return ZERO_OK;
+    if (n > kMaxTokens) return fail(ZERO_ERR_INDEX_OVERFLOW, "too many tokens");
     if (!tokens) return fail(ZERO_ERR_INVALID_ARG, "tokens is NULL");
     if (reinterpret_cast<uintptr_t>(tokens) % uintptr_t(token_bytes) != 0)
         return fail(ZERO_ERR_ALIGNMENT, "tokens lack their alignment");
@@ -327,7 +329,7 @@ extern "C" int zero_activation_grad(int32_t kind, const zero_matrix* dy, const z
 }
 
 extern "C" int64_t zero_weight_grad_work_bytes(int64_t T, int64_t n, int64_t k, int32_t dy_type) {
-    if (T <= 0 || n <= 0 || k < 0 || T > zp::kMaxSpan || n >= zp::kMaxCols || k >= zp::kMaxCols || zp::type_bytes(dy_type) == 0) return 0;
+    if (T <= 0 || n <= 0 || k < 0 || T > zp::kMaxTokens || n >= zp::kMaxCols || k >= zp::kMaxCols || zp::type_bytes(dy_type) == 0) return 0;
     return zp::weight_grad_work(T, n, k, dy_type);
 }
 
@@ -342,6 +344,7 @@ extern "C" int zero_weight_grad(const zero_matrix* dy, const zero_checkpoint* x,
     if (rc == ZERO_OK) rc = zp::check_matrix(dw, "dw", true, &aw);
     if (rc != ZERO_OK) return rc;
     const int64_t T = dy->rows, n = dy->cols, k = x->cols;
+    if (T > zp::kMaxTokens) return fail(ZERO_ERR_INDEX_OVERFLOW, "zero_weight_grad: too many tokens");
     if (x->rows != T) return fail(ZERO_ERR_INVALID_ARG, "dy and the checkpoint have different numbers of rows");
     if (!zp::same_shape(dw, transposed ? k : n, transposed ? n : k))
         return fail(ZERO_ERR_INVALID_ARG, "dw's shape is not that of the gradient");
