@@ -345,7 +345,7 @@ def layer_main(args):
         rows.append({"kernel": name, "ms": round(s * 1e3, 4), "ms_median": round(float(np.median(t)), 4), "roofline": line})
         return rows[-1]
 
-    timed("embedding lookup", lambda: zp.embedding_lookup(table, named, x), 4 * n)
+    timed("embedding lookup", lambda: zp.embedding_lookup(table, named, x), 2 * n + 2 * width * len(named.unique()))
     timed("checkpoint store", lambda: kept["x"].store(x), 3 * n + n // 32)
     timed("checkpoint load", lambda: kept["x"].load(x), 3 * n + n // 32)
     timed("gelu_tanh with checkpoints of its input and result",
