@@ -29,6 +29,7 @@ Names follow the C ABI in include/zero_partition.h:
 """
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass
 from typing import List, Optional, Sequence
@@ -809,7 +810,7 @@ def _matrix(t, what: str, dev: int) -> MatrixC:
         if t.dim() == 0:
             raise ValueError(f"{what} must have a last dimension")
         try:
-            t = t.view(t.numel() // t.shape[-1] if t.shape[-1] else 0, t.shape[-1])
+            t = t.view(math.prod(t.shape[:-1]), t.shape[-1])
         except RuntimeError:
             raise ValueError(f"{what}: its rows are not equally far apart") from None
     rows, cols = t.shape
