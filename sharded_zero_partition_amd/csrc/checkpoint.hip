@@ -17,6 +17,12 @@
 // plain 106 and 107; from HBM 107 and 105, plain 105 and 104.  A plain store keeps its
 // loads in the caches' way, where its input mostly comes from (8192 x 5120: 20.3 us, else
 // 24), and so do all codes (24 us for loading them back, else 19).
+// Results that pass by the caches are not there for the call that reads them.  Both calls
+// in a row, results of 1 / 10 / 80 / 300 MB in bf16, us, and with plain stores:
+//   lookup, checkpoint store           5.4 8.5 47 184       plain 5.4 9.1 47 197
+//   silu, library product              14.4 26 142 434      plain 12.3 27 138 440
+//   silu's gradient, weight gradient   13.6 40 124 400      plain 12.1 40 121 396
+// Neither is better throughout, nor is there one size where it turns: one rule for all.
 #include <type_traits>
 
 #include "octets.hpp"

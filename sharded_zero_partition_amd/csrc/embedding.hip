@@ -13,7 +13,7 @@
 // a last kernel adds in order.  Rows that no token names are zeros from the start.
 // dy and finished rows pass by the caches (8192 tokens, 50257 x 5120 bf16, from HBM: 132 us
 // instead of 138; as fast where dy was just written).
-//   8192 tokens, 50257 x 5120 bf16: sorting under the fill 99 us, sums 22, joining 6
+//   8192 tokens, 50257 x 5120 bf16: sorting under the fill 89 to 99 us, sums 22 to 27, joining 6
 //   32768 tokens, 1600 fp16 columns added to fp32: sorting 25 us, sums 39, joining 11
 #include <type_traits>
 
@@ -127,7 +127,12 @@ __device__ __forceinline__ uint32_t key_of(const SortArgs& a, int64_t i) {
 
 // Few tokens: each one's place is how many keys are smaller, or equal and before
 // it.  16 threads count for a token, 32 tokens a block: n^2 comparisons, but one
-// launch where digit by digit takes four that wait for each other.
+// launch where digit by digit takes four that wait for each other.  The whole gradient by
+// ranks / by digits, us:
+//   50257 x 64 added to fp32      2048 tokens 18.6 / 34.8, 8192 27.4 / 36.8, 12288 37.3 / 38.9, 16384 47.6 / 42.2
+//   50257 x 1600 added to fp32    2048 20.4 / 37.0, 8192 37.4 / 45.7, 12288 56.8 / 54.2, 16384 74.1 / 63.9
+//   50257 x 5120 bf16, written    2048 113 / 132, 8192 132 / 152, 12288 144 / 164, 16384 173 / 174
+// They cross between 8192 and 16384.
 constexpr int64_t kRankMost = 8192;
 constexpr int kRankThreads = 512, kRankShare = 16, kRankTokens = kRankThreads / kRankShare;
 template <typename I>
@@ -307,7 +312,7 @@ __global__ __launch_bounds__(kThreads) void digit_move_kernel(const DigitArgs a)
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             if (there && (same >> lane) == 1) next[wave][d] += before + 1;   // the last of them
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            if (there && int64_t(to) < a.s.n) {
+            if (there && int64_t(to) < a.s.n) {   // always, unless tokens changed between the passes, which read them again
                 a.s.key[to] = k[u];
                 a.s.order[to] = o[u];
             }
@@ -385,6 +390,7 @@ __device__ __forceinline__ void sum_tile(const SumArgs& a, int64_t t, int chunk)
                 x[j].zero();
                 const uint32_t r = uint32_t(__builtin_amdgcn_readlane(int(keys), j0 + j));   // none behind hi
                 const uint32_t i = uint32_t(__builtin_amdgcn_readlane(int(places), j0 + j));
+                // (i is below n unless tokens changed while they were sorted: places that nothing wrote)
                 if (r < none && i < a.e.n) x[j] = load_octet<DI, true>(place<DI>(a.e.in, i, a.e.s_in, col), left);
             }
 #pragma unroll

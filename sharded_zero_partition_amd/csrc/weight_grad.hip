@@ -7,9 +7,12 @@
 // without writing a 16-bit copy first.  Both operands go through LDS as they lie in memory,
 // and LDS reads that transpose (ds_read_b64_tr_b16) make the matrix unit's fragments of
 // them.  Bound by the matrix unit's feeding; measured, with 2 T n k operations:
-//   8192 x 8192 x 8192           bf16 776 us (1417 TFLOP/s), fp16 853 (1289)
-//   8192 x 20480 x 5120, bias    bf16 1292 to 1390 us (1236 to 1330)
-//   8192 x 4096 x 4096           fp32 619 us (444: three products for one)
+//   8192 x 8192 x 8192           bf16 740 to 790 us (1390 to 1490 TFLOP/s), fp16 812 to 870 (1260 to 1354)
+//   8192 x 20480 x 5120, bias    bf16 1292 to 1423 us (1208 to 1330)
+//   8192 x 4096 x 4096           fp32 604 to 653 us (421 to 455: three products for one)
+// for rows of dy that start on 16 bytes, and an even n.  Others go through registers:
+//   8192 x 13653 x 5120, bias    bf16 1393 us (822), fp16 1445 to 1468 (780 to 793); n = 13656: 952, 986 to 1021
+//   8192 x 50257 x 5120, bias    bf16 4940 us (853), fp16 4903 (860); n = 50264: 3250 to 3352, 3543 to 3623
 // where the library's product of two 16-bit matrices takes 733 us for 8192^3 (1501) and
 // 1075 to 1597 us for the second.
 #include <type_traits>
@@ -438,7 +441,8 @@ __device__ __forceinline__ void finish_bias(const GemmArgs& a, const Part& part,
     else put_bias<ZERO_DTYPE_FP32>(a, part.n0 + n, sum);
 }
 
-// Any dy: eight waves, loads through registers.
+// Any dy: eight waves, loads through registers, all 256 of which the large tiles take (16-bit
+// types spill some).
 template <typename C>
 __global__ __launch_bounds__(C::threads) void weight_grad_kernel(const GemmArgs a) {
     constexpr int D = C::D, P = C::P;
@@ -837,6 +841,8 @@ __global__ __launch_bounds__(kJoinThreads) void split_join_kernel(const GemmArgs
 // How a product is cut: into tiles of 256 x 256 outputs, one of which runs on a CU at a
 // time, or of 64 x 64, of which several do; and where tiles are few, or some of the large are
 // left over after whole rounds of all CUs, these by tokens, another kernel adding the parts up.
+// Sums are in an order that the sizes alone fix, so where dy starts plays no part: one that only
+// the general kernel takes is cut as for the fast one, if not at its best.
 // What is expected to take the least time is taken, by this model of one MI355X in us: a round
 // of blocks takes `fixed` and `step` for kUnit tokens (small ones overlap, so their rounds
 // need not be whole, and `first` is what the first costs more), the other kernel 5 and its
