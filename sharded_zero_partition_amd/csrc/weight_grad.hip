@@ -8,7 +8,7 @@
 // and LDS reads that transpose (ds_read_b64_tr_b16) make the matrix unit's fragments of
 // them.  Bound by the matrix unit's feeding; measured, with 2 T n k operations:
 //   8192 x 8192 x 8192           bf16 740 to 790 us (1390 to 1490 TFLOP/s), fp16 812 to 870 (1260 to 1354)
-//   8192 x 20480 x 5120, bias    bf16 1292 to 1423 us (1208 to 1330)
+//   8192 x 20480 x 5120, bias    bf16 1283 to 1423 us (1208 to 1340)
 //   8192 x 4096 x 4096           fp32 604 to 653 us (421 to 455: three products for one)
 // for rows of dy that start on 16 bytes, and an even n.  Others go through registers:
 //   8192 x 13653 x 5120, bias    bf16 1393 us (822), fp16 1445 to 1468 (780 to 793); n = 13656: 952, 986 to 1021
